@@ -4,7 +4,7 @@ block-scaled GEMM on AMD Instinct MI355X (gfx950).
 Two layers:
   * mx_quantize, mx_dequantize, mx_gemm, ... : the C ABI (include/mx.h) under
     the same names, taking integers and raw device pointers;
-  * quantize, dequantize, gemm : torch conveniences that allocate outputs on
+  * quantize, dequantize, gemm, gemm_grouped, norm_quantize : torch conveniences that allocate outputs on
     the input's device and pass data_ptr() plus the current HIP stream.
 
 Every step of the computation runs in libmx's HIP kernels. If libmx.so is not
@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(HERE, "libmx.so")
 
 MX_FMT_BF16, MX_FMT_MXFP4, MX_FMT_MXFP8, MX_FMT_NVFP4 = 0, 1, 2, 3
 MX_FMT_MXFP8_E5M2, MX_FMT_MXFP6_E3M2, MX_FMT_MXFP4_MBS, MX_FMT_MXFP4_MBS16 = 4, 5, 6, 7
+MX_FMT_FP8_B128, MX_FMT_FP8_B128X128 = 8, 9
 MX_ROUND_RNE = 0
 MX_SCALE_CEIL, MX_SCALE_OAS = 0, 1
 MX_ROTATE_NONE, MX_ROTATE_WHT32 = 0, 1
@@ -28,16 +29,18 @@ MX_LAYOUT_ROWS, MX_LAYOUT_KPANEL = 0, 1
 
 FORMATS = {"mxfp4": MX_FMT_MXFP4, "mxfp8": MX_FMT_MXFP8, "nvfp4": MX_FMT_NVFP4, "bf16": MX_FMT_BF16,
            "mxfp8_e5m2": MX_FMT_MXFP8_E5M2, "mxfp6_e3m2": MX_FMT_MXFP6_E3M2,
-           "mxfp4_mbs": MX_FMT_MXFP4_MBS, "mxfp4_mbs16": MX_FMT_MXFP4_MBS16}
+           "mxfp4_mbs": MX_FMT_MXFP4_MBS, "mxfp4_mbs16": MX_FMT_MXFP4_MBS16,
+           "fp8_b128": MX_FMT_FP8_B128, "fp8_b128x128": MX_FMT_FP8_B128X128}
 BLOCK = {MX_FMT_MXFP4: 32, MX_FMT_MXFP8: 32, MX_FMT_NVFP4: 16, MX_FMT_BF16: 32,
          MX_FMT_MXFP8_E5M2: 32, MX_FMT_MXFP6_E3M2: 32, MX_FMT_MXFP4_MBS: 32,
-         MX_FMT_MXFP4_MBS16: 16}
+         MX_FMT_MXFP4_MBS16: 16, MX_FMT_FP8_B128: 128, MX_FMT_FP8_B128X128: 128}
 MBS_FORMATS = (MX_FMT_MXFP4_MBS, MX_FMT_MXFP4_MBS16)
+FP8_BLOCK_FORMATS = (MX_FMT_FP8_B128, MX_FMT_FP8_B128X128)  # fp32 scales
 
 
 def code_cols(fmt, cols):
     """Bytes of codes per row of `cols` elements."""
-    if fmt in (MX_FMT_MXFP8, MX_FMT_MXFP8_E5M2):
+    if fmt in (MX_FMT_MXFP8, MX_FMT_MXFP8_E5M2) or fmt in FP8_BLOCK_FORMATS:
         return cols
     if fmt == MX_FMT_MXFP6_E3M2:
         return cols * 3 // 4
@@ -46,7 +49,10 @@ def code_cols(fmt, cols):
 def scale_shape(fmt, rows, cols):
     """Shape of the scales tensor: [rows][cols/block]; for MXFP4-MBS (block 32)
     and MXFP4-MBS16 (block 16) one flat buffer, the E8M0 plane
-    [rows][cols/block] followed by the macro mantissa plane [rows][cols/128]."""
+    [rows][cols/block] followed by the macro mantissa plane [rows][cols/128];
+    for FP8_B128X128 [ceil(rows/128)][cols/128]."""
+    if fmt == MX_FMT_FP8_B128X128:
+        return (-(-rows // 128), cols // 128)
     if fmt in MBS_FORMATS:
         return (rows * (cols // BLOCK[fmt]) + rows * (cols // 128),)
     return (rows, cols // BLOCK[fmt])
@@ -63,7 +69,7 @@ def mbs_planes(scales, rows, cols, block=32):
 EXPORTS = ("mx_quantize", "mx_quantize_workspace_bytes", "mx_quantize_ex", "mx_quantize_layout",
            "mx_dequantize",
            "mx_gemm", "mx_gemm_workspace_bytes", "mx_last_hip_error", "mx_status_string",
-           "mx_pack", "mx_gemm_ex", "mx_gemm_noalloc")
+           "mx_pack", "mx_gemm_ex", "mx_gemm_noalloc", "mx_gemm_grouped", "mx_norm_quantize")
 
 _lib = None
 
@@ -108,6 +114,12 @@ def lib():
         L.mx_gemm_noalloc.restype = i32
         L.mx_gemm_noalloc.argtypes = [i32, i32, i32, i32, i64, i64, i64, P, P, P, P, P, P, i32, P,
                                       i64, P]
+        L.mx_gemm_grouped.restype = i32
+        L.mx_gemm_grouped.argtypes = [i32, i32, i32, i32, i64, i64, i64, i64, P, P, P, P, P, i32, P,
+                                      i64, P]
+        L.mx_norm_quantize.restype = i32
+        L.mx_norm_quantize.argtypes = [i32, i32, i32, i64, i64, P, i64, P, i64, P, i64, P,
+                                       ctypes.c_float, P, ctypes.c_float, P, i64, P, P, P, i32]
         L.mx_pack.restype = i32
         L.mx_pack.argtypes = [i32, i32, i64, i64, P, P, P, P, P]
         L.mx_gemm_workspace_bytes.restype = sz
@@ -166,6 +178,19 @@ def mx_gemm_noalloc(fmt_a, fmt_b, block, rnd, M, N, K, a, a_scales, a_ts, b, b_s
                                  b_ts, out_dtype, c, ldc, stream)
 
 
+def mx_gemm_grouped(fmt_a, fmt_b, block, rnd, groups, M, N, K, offsets, a, a_scales, b, b_scales,
+                    out_dtype, c, ldc, stream):
+    return lib().mx_gemm_grouped(fmt_a, fmt_b, block, rnd, groups, M, N, K, offsets, a, a_scales, b,
+                                 b_scales, out_dtype, c, ldc, stream)
+
+
+def mx_norm_quantize(fmt, block, rnd, rows, cols, x, ldx, residual, ldr, gate, gate_rows, post_weight,
+                     alpha, weight, eps, h, ldh, codes, scales, stream, layout):
+    return lib().mx_norm_quantize(fmt, block, rnd, rows, cols, x, ldx, residual, ldr, gate, gate_rows,
+                                  post_weight, alpha, weight, eps, h, ldh, codes, scales, stream,
+                                  layout)
+
+
 def mx_pack(fmt, block, rows, cols, codes, scales, packed_codes, packed_scales, stream):
     return lib().mx_pack(fmt, block, rows, cols, codes, scales, packed_codes, packed_scales, stream)
 
@@ -190,7 +215,10 @@ def status_string(status):
 @dataclass
 class QTensor:
     """A block-quantized [rows][cols] tensor: codes, scales and (NVFP4) the
-    fp32 tensor scale, all device tensors; layout MX_LAYOUT_KPANEL after pack()."""
+    fp32 tensor scale, all device tensors; layout MX_LAYOUT_KPANEL after pack().
+    Scales are uint8, or float32 for the FP8 block formats. groups: a stack of
+    that many [rows / groups][cols] weights, each quantized by itself (the b of
+    gemm_grouped)."""
     fmt: int
     rows: int
     cols: int
@@ -198,6 +226,7 @@ class QTensor:
     scales: "object"
     tensor_scale: "object" = None
     layout: int = MX_LAYOUT_ROWS
+    groups: int = 1
 
     @property
     def block(self):
@@ -210,13 +239,17 @@ def _check_qtensor(q, what):
     import torch
     if q.fmt not in BLOCK or q.fmt == MX_FMT_BF16 or q.cols % BLOCK[q.fmt] != 0:
         raise ValueError(f"{what}: not a quantized tensor of a supported format")
+    if q.groups < 1 or q.rows % q.groups != 0:
+        raise ValueError(f"{what}: {q.rows} rows are not a stack of {q.groups} weights")
     need_c = q.rows * code_cols(q.fmt, q.cols)
-    need_s = 1
-    for d in scale_shape(q.fmt, q.rows, q.cols):
+    need_s = q.groups
+    for d in scale_shape(q.fmt, q.rows // q.groups, q.cols):
         need_s *= d
-    for t, n, name in ((q.codes, need_c, "codes"), (q.scales, need_s, "scales")):
-        if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
-            raise ValueError(f"{what}: {name} must be a contiguous uint8 tensor of {n} bytes")
+    if q.codes.dtype != torch.uint8 or not q.codes.is_contiguous() or q.codes.numel() != need_c:
+        raise ValueError(f"{what}: codes must be a contiguous uint8 tensor of {need_c} bytes")
+    st, name = (torch.float32, "float32") if q.fmt in FP8_BLOCK_FORMATS else (torch.uint8, "uint8")
+    if q.scales.dtype != st or not q.scales.is_contiguous() or q.scales.numel() != need_s:
+        raise ValueError(f"{what}: scales must be a contiguous {name} tensor of {need_s} elements")
     if q.fmt == MX_FMT_NVFP4:
         ts = q.tensor_scale
         if ts is None or ts.dtype != torch.float32 or ts.numel() < 1:
@@ -248,6 +281,16 @@ def _check(status, what):
         raise MXError(status, what)
 
 
+def _on(device, call, *args):
+    """call(*args) with `device` (the tensors' and the stream's) current: a
+    kernel is launched on the current device."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
+
+
 SCALE_RULES = {"ceil": MX_SCALE_CEIL, "oas": MX_SCALE_OAS}
 ROTATIONS = {None: MX_ROTATE_NONE, "none": MX_ROTATE_NONE, "wht32": MX_ROTATE_WHT32}
 
@@ -259,10 +302,22 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
     """Quantize a contiguous bf16 [rows][cols] device tensor. scale_rule "oas"
     (MXFP4) and rotation "wht32" (MXFP4, MXFP8) select mx_quantize_ex, with
     the layout given; otherwise layout "kpanel" (MXFP4, MXFP8, E5M2, E3M2,
-    NVFP4) selects mx_quantize_layout."""
+    NVFP4) selects mx_quantize_layout. A [groups][rows][cols] tensor ("mxfp4"
+    or "fp8_b128x128", row layout) is a stack of weights for gemm_grouped, each
+    quantized by itself."""
     import torch
     f = _fmt_id(fmt)
     lay = LAYOUTS[layout]
+    if x.dim() == 3:
+        if f not in (MX_FMT_MXFP4, MX_FMT_FP8_B128X128) or lay != MX_LAYOUT_ROWS:
+            raise ValueError("a stack of weights is quantized to mxfp4 or fp8_b128x128 in the row layout")
+        if f == MX_FMT_FP8_B128X128:
+            return _quantize_tile_stack(x, scale_rule, rotation)
+        if not x.is_contiguous():
+            raise ValueError("quantize expects a contiguous bfloat16 tensor")
+        q = quantize(x.view(-1, x.shape[2]), fmt, scale_rule, rotation)
+        q.groups = x.shape[0]
+        return q
     if scale_rule != "ceil" or rotation not in (None, "none"):
         if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_contiguous():
             raise ValueError("quantize expects a contiguous 2-D bfloat16 tensor")
@@ -278,7 +333,8 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
     rows, cols = x.shape
     dev = x.device
     codes = torch.empty((rows, code_cols(f, cols)), dtype=torch.uint8, device=dev)
-    scales = torch.empty(scale_shape(f, rows, cols), dtype=torch.uint8, device=dev)
+    scales = torch.empty(scale_shape(f, rows, cols), device=dev,
+                         dtype=torch.float32 if f in FP8_BLOCK_FORMATS else torch.uint8)
     ts = ws = None
     wsb = 0
     if f == MX_FMT_NVFP4:
@@ -286,13 +342,32 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
         wsb = mx_quantize_workspace_bytes(f, rows, cols)
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
     if lay == MX_LAYOUT_ROWS:
-        _check(mx_quantize(f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes), _ptr(scales),
-                           _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x)), "mx_quantize")
+        _check(_on(dev, mx_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
+                   _ptr(scales), _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x)), "mx_quantize")
     else:
         _check(mx_quantize_layout(f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
                                   _ptr(scales), _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x), lay),
                "mx_quantize_layout")
     return QTensor(f, rows, cols, codes, scales, ts, lay)
+
+
+def _quantize_tile_stack(x, scale_rule, rotation):
+    """A [groups][rows][cols] stack to FP8_B128X128: a call per weight, so that
+    no tile holds rows of two of them."""
+    import torch
+    if scale_rule != "ceil" or rotation not in (None, "none"):
+        raise ValueError("scale rules and rotations are not for fp8_b128x128")
+    if x.dtype != torch.bfloat16 or not x.is_contiguous():
+        raise ValueError("quantize expects a contiguous bfloat16 tensor")
+    g, rows, cols = x.shape
+    f, dev = MX_FMT_FP8_B128X128, x.device
+    stream = _stream(torch, dev, x)
+    codes = torch.empty((g * rows, cols), dtype=torch.uint8, device=dev)
+    scales = torch.empty((g, *scale_shape(f, rows, cols)), dtype=torch.float32, device=dev)
+    for i in range(g):
+        _check(_on(dev, mx_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x[i]),
+                   _ptr(codes[i * rows:]), _ptr(scales[i]), None, None, 0, stream), "mx_quantize")
+    return QTensor(f, g * rows, cols, codes, scales, groups=g)
 
 
 def dequantize(q, out_dtype=None):
@@ -305,10 +380,15 @@ def dequantize(q, out_dtype=None):
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
     od = MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16
+    if q.groups > 1 and q.fmt == MX_FMT_FP8_B128X128:  # each weight has tiles of its own
+        n = q.rows // q.groups
+        codes, scales = q.codes.view(q.groups, n, q.cols), q.scales.view(q.groups, -1)
+        return torch.cat([dequantize(QTensor(q.fmt, n, q.cols, codes[i], scales[i]), out_dtype)
+                          for i in range(q.groups)])
     y = torch.empty((q.rows, q.cols), dtype=out_dtype, device=q.codes.device)
-    _check(mx_dequantize(q.fmt, q.block, MX_ROUND_RNE, q.rows, q.cols, _ptr(q.codes),
-                         _ptr(q.scales), _ptr(q.tensor_scale), od, _ptr(y),
-                         _stream(torch, q.codes.device, q.codes, q.scales, q.tensor_scale)), "mx_dequantize")
+    _check(_on(q.codes.device, mx_dequantize, q.fmt, q.block, MX_ROUND_RNE, q.rows, q.cols,
+               _ptr(q.codes), _ptr(q.scales), _ptr(q.tensor_scale), od, _ptr(y),
+               _stream(torch, q.codes.device, q.codes, q.scales, q.tensor_scale)), "mx_dequantize")
     return y
 
 
@@ -319,6 +399,8 @@ def pack(q):
     if q.layout != MX_LAYOUT_ROWS:
         raise ValueError("pack() takes a tensor in the row layout")
     _check_qtensor(q, "pack")
+    if q.groups != 1:
+        raise ValueError("pack() takes one weight, not a stack")
     codes = torch.empty_like(q.codes)
     scales = torch.empty_like(q.scales)
     _check(mx_pack(q.fmt, q.block, q.rows, q.cols, _ptr(q.codes), _ptr(q.scales), _ptr(codes),
@@ -327,15 +409,17 @@ def pack(q):
 
 
 def gemm(a, b, out_dtype=None, out=None, workspace=None):
-    """C = A * B^T. a: QTensor (any quantized format, M x K; b of the same format) or a bf16 [M][K]
-    tensor (with an MXFP4 b: W4A16); b: QTensor stored N x K (MXFP4: row or
-    K-panel layout)."""
+    """C = A * B^T. a: QTensor (any quantized format, M x K; b of the same format,
+    or fp8_b128x128 for an fp8_b128 a) or a bf16 [M][K] tensor (with an MXFP4 b:
+    W4A16); b: QTensor stored N x K (MXFP4: row or K-panel layout)."""
     import torch
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
     od = MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16
     _check_qtensor(b, "gemm operand b")
+    if b.groups != 1:
+        raise ValueError("gemm takes one weight; a stack is gemm_grouped's")
     if isinstance(a, QTensor):
         _check_qtensor(a, "gemm operand a")
         fa, M, K = a.fmt, a.rows, a.cols
@@ -370,7 +454,88 @@ def gemm(a, b, out_dtype=None, out=None, workspace=None):
                           _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0),
                           _ptr(workspace), wsb, stream, la, b.layout), "mx_gemm_ex")
         return c
-    _check(mx_gemm(fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta, _ptr(b.codes),
-                   _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0),
-                   _ptr(workspace), wsb, stream), "mx_gemm")
+    _check(_on(dev, mx_gemm, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta, _ptr(b.codes),
+               _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0), _ptr(workspace), wsb,
+               stream), "mx_gemm")
     return c
+
+
+def gemm_grouped(a, b, offsets, out_dtype=None, out=None):
+    """C = A * B_g^T by expert. a: QTensor [M][K] (mxfp4 or fp8_b128), rows
+    sorted by expert; b: a stack of `groups` [N][K] weights (mxfp4 or
+    fp8_b128x128; quantize of a 3-D tensor); offsets: int32 device tensor of
+    groups + 1 nondecreasing row numbers, expert g's rows being offsets[g] ..
+    offsets[g + 1] - 1. The offsets are read on the device only. Rows of no
+    expert are left as `out` had them (undefined without `out`)."""
+    import torch
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    _check_qtensor(a, "gemm_grouped operand a")
+    _check_qtensor(b, "gemm_grouped operand b")
+    if a.layout != MX_LAYOUT_ROWS or b.layout != MX_LAYOUT_ROWS:
+        raise ValueError("gemm_grouped takes operands in the row layout")
+    if a.groups != 1:
+        raise ValueError("gemm_grouped operand a is one [M][K] tensor")
+    if b.cols != a.cols:
+        raise ValueError(f"K mismatch: A has {a.cols}, B has {b.cols}")
+    G, M, N, K = b.groups, a.rows, b.rows // b.groups, a.cols
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != G + 1 or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 tensor of {G + 1} row numbers")
+    dev = a.codes.device
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or out.dim() != 2 or tuple(out.shape) != (M, N) or out.stride(1) != 1:
+        raise ValueError(f"out must be a [{M}][{N}] {out_dtype} tensor with unit column stride")
+    stream = _stream(torch, dev, a.codes, a.scales, b.codes, b.scales, offsets, out)
+    _check(_on(dev, mx_gemm_grouped, a.fmt, b.fmt, b.block, MX_ROUND_RNE, G, M, N, K, _ptr(offsets),
+               _ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales),
+               MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, _ptr(out), out.stride(0),
+               stream), "mx_gemm_grouped")
+    return out
+
+
+def norm_quantize(x, weight, fmt, residual=None, gate=None, post_weight=None, alpha=1.0, eps=1e-6,
+                  layout="rows", out=None):
+    """The norms between two blocks, fused with the residual and the quantizer:
+    y = x, or its RMS norm times post_weight; h = residual + alpha * gate * y;
+    the RMS norm of h times weight, quantized to `fmt` (mxfp4, mxfp8 or
+    fp8_b128). x, residual: bf16 [rows][cols] with unit column stride; weight,
+    post_weight: bf16 [cols] (weight None: ones); gate: bf16 [cols] or [n][cols],
+    each of its rows for rows / n rows of x. Returns the QTensor and h (bf16;
+    `out` if given, which may be x or residual; None without a residual or out)."""
+    import torch
+    f = _fmt_id(fmt)
+    if f not in (MX_FMT_MXFP4, MX_FMT_MXFP8, MX_FMT_FP8_B128):
+        raise ValueError("norm_quantize gives mxfp4, mxfp8 or fp8_b128")
+    if x.dim() != 2:
+        raise ValueError("norm_quantize expects a 2-D bfloat16 tensor")
+    rows, cols = x.shape
+    for t, name in ((x, "x"), (residual, "residual"), (out, "out")):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != x.shape or t.stride(1) != 1):
+            raise ValueError(f"{name} must be a [{rows}][{cols}] bfloat16 tensor with unit column stride")
+    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (cols,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor of {cols} elements")
+    gate_rows = 0
+    if gate is not None:
+        n = 1 if gate.dim() == 1 else gate.shape[0]
+        if gate.dtype != torch.bfloat16 or gate.dim() > 2 or gate.shape[-1] != cols or not gate.is_contiguous():
+            raise ValueError(f"gate must be a contiguous bfloat16 tensor of rows of {cols}")
+        if n < 1 or rows % n != 0:
+            raise ValueError(f"{rows} rows do not divide among {n} gates")
+        gate_rows = rows // n
+    dev = x.device
+    if out is None and residual is not None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    codes = torch.empty((rows, code_cols(f, cols)), dtype=torch.uint8, device=dev)
+    scales = torch.empty(scale_shape(f, rows, cols), device=dev,
+                         dtype=torch.float32 if f == MX_FMT_FP8_B128 else torch.uint8)
+    lay = LAYOUTS[layout]
+    stream = _stream(torch, dev, x, residual, gate, post_weight, weight, out)
+    ld = lambda t: 0 if t is None else t.stride(0) if rows > 1 else cols  # noqa: E731
+    _check(_on(dev, mx_norm_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), ld(x),
+               _ptr(residual), ld(residual), _ptr(gate), gate_rows, _ptr(post_weight), alpha,
+               _ptr(weight), eps, _ptr(out), ld(out), _ptr(codes), _ptr(scales), stream, lay),
+           "mx_norm_quantize")
+    return QTensor(f, rows, cols, codes, scales, None, lay), out

@@ -1,0 +1,346 @@
+// Block-scaled GEMM C = A B^T on 16 x 16 x 128 matrix instructions, dense or
+// by expert (groups.h), for MXFP4 x MXFP4 and for FP8 x FP8 under fp32 scales
+// per 1 x 128 of A and 128 x 128 of B.
+//
+// FP8: a K step of 128 is one scale block, so the step's MFMA starts from
+// zero, and the vector ALU adds its partial sum times s_A(row) s_B(tile):
+//   C[i][j] = sum over blocks q of s_A[i][q] s_B[j / 128][q] P_q[i][j].
+// gfx950's FP8 MFMAs lose low bits inside their 128-term sum: of 8 products
+// added together, each loses less than 2^-13 of the largest (measured with one
+// large product and seven small ones; 1.4e-5 of the result on quantized normal
+// values). A bf16 result has an error of 1.7e-3 from its own rounding, so it
+// takes P from the FP8 MFMA, at twice the rate of the bf16 one. An fp32
+// result takes P from four bf16 MFMAs (EXACT): every E4M3 value is a bf16
+// value, and those return the rounded exact sum.
+// MXFP4: the MFMA applies both E8M0 scales and accumulates.
+//
+// Operands go HBM -> LDS directly (buffer_load ... lds), double-buffered over
+// K; the buffer view of a tile ends with the group's rows, so rows past the
+// end load as zeros. LDS rows hold a K step (128 or 64 bytes); the 16-byte
+// chunk c of row r sits in slot c ^ swz(r), so that the 16 lanes that read one
+// column of chunks hit distinct banks.
+//
+// B goes first into the MFMA: lane r + 16 g then holds C[row r][columns 4 g ..
+// 4 g + 3] of a tile, one row (one s_A) and a run of columns to store.
+#include <type_traits>
+
+#include "bf16.h"
+#include "groups.h"
+#include "mx_internal.h"
+
+namespace mx {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
+constexpr uint32_t kOOB = 0x80000000u;        // an offset past every buffer's range
+constexpr int kSegSteps = 48;                 // K steps per accumulation chain (fp32 results)
+
+// Tile geometry: waves of 16 TMW x 16 TNW, WM x WN of them.
+template <int FMT, int TMW_, int TNW_, int WM_, int WN_>
+struct Geo {
+  static constexpr int TMW = TMW_, TNW = TNW_, WM = WM_, WN = WN_;
+  static constexpr int BM = 16 * TMW * WM, BN = 16 * TNW * WN;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr bool kFp8 = FMT == kFP8B128;
+  static constexpr int kRow = kFp8 ? 128 : 64;  // LDS bytes of a row's K step
+  static constexpr int kCpr = kRow / 16;        // chunks per row
+  static constexpr int kRpb = 64 / kCpr;        // rows per 1 KB load of a wave
+  static constexpr int kOffB = BM * kRow;
+  static constexpr int kOffS = kOffB + BN * kRow;  // FP8: s_A [BM]; MXFP4: 4 E8M0 per row, A then B
+  static constexpr int kStage = kOffS + (kFp8 ? BM * 4 : (BM + BN) * 4);
+};
+
+template <bool FP8>
+__device__ __forceinline__ int swz(int row) {
+  return FP8 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
+
+// 8 E4M3 codes as bf16.
+__device__ __forceinline__ bf16x8 expand8(int lo, int hi) {
+  u32x4 o;
+  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, false));
+  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, true));
+  o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, false));
+  o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, true));
+  return __builtin_bit_cast(bf16x8, o);
+}
+
+struct Args {
+  const uint8_t *A, *SA, *B, *SB;
+  void* C;
+  const int* offsets;  // null: dense
+  int64_t ldc;
+  int groups, M, N, K, tiles_n;
+};
+
+template <int FMT, bool EXACT, int OUT, class G>
+__global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
+  constexpr bool FP8 = G::kFp8;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * G::kStage];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / G::WN, wn = wave % G::WN;
+  const int r = lane & 15, g = lane >> 4;
+
+  groups::Tile t;
+  if (!groups::tile_of<G::BM>(p.offsets, p.groups, p.M, p.tiles_n, blockIdx.x, t)) return;
+  const int n0 = t.tn * G::BN;
+  const int mrows = min(t.rows, G::BM), nrows = min(p.N - n0, G::BN);
+  const uint32_t rowbytes = (uint32_t)(FP8 ? p.K : p.K / 2);
+  const int nk = (p.K + 127) / 128;
+  const int kblocks = p.K / 32;                   // MXFP4: scales per row
+  const int64_t brow = (int64_t)t.group * p.N + n0;  // row of B among all weights
+
+  const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.A + (int64_t)t.row * rowbytes), 0, (int)((uint32_t)mrows * rowbytes), kRsrcFlags);
+  const __amdgpu_buffer_rsrc_t rB = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.B + brow * rowbytes), 0, (int)((uint32_t)nrows * rowbytes), kRsrcFlags);
+  const uint32_t sstride = (uint32_t)(FP8 ? nk * 4 : kblocks);  // scale bytes per row of A
+  const __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.SA + (int64_t)t.row * sstride), 0, (int)((uint32_t)mrows * sstride), kRsrcFlags);
+  const __amdgpu_buffer_rsrc_t rSB = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.SB + (FP8 ? 0 : brow * sstride)), 0, FP8 ? 0 : (int)((uint32_t)nrows * sstride), kRsrcFlags);
+  // FP8: the scales of this wave's 128 columns (its last tile past N: any).
+  const int nb = min(n0 + wn * 16 * G::TNW, p.N - 1) / 128;
+  const float* sb_row = (const float*)p.SB + ((int64_t)t.group * ((p.N + 127) / 128) + nb) * nk;
+
+  // Codes of step s (and s_A): 1 KB per instruction, kRpb rows.
+  auto issue = [&](int s, uint8_t* stage) {
+    constexpr int kA = G::BM / G::kRpb, kAll = (G::BM + G::BN) / G::kRpb;
+#pragma unroll
+    for (int i = 0; i < (kAll + G::kWaves - 1) / G::kWaves; i++) {
+      const int b = wave + i * G::kWaves;
+      if (kAll % G::kWaves != 0 && b >= kAll) break;
+      const bool isA = b < kA;
+      const int row = (isA ? b : b - kA) * G::kRpb + lane / G::kCpr;
+      const uint32_t kb = (uint32_t)s * G::kRow + (uint32_t)((lane % G::kCpr) ^ swz<FP8>(row)) * 16u;
+      uint32_t off = (uint32_t)row * rowbytes + kb;
+      if (!FP8) off = kb < rowbytes ? off : kOOB;  // (FP8: K is a multiple of 128)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rA : rB, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
+    }
+    if (FP8 && wave * 64 < G::BM)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rSA, (lds_ptr_t)(stage + G::kOffS + wave * 256), 4,
+                                               (uint32_t)(wave * 64 + lane) * sstride, 4 * s, 0, 0);
+  };
+  // MXFP4: the 4 scales of step s of one row, through a register (a row's
+  // scales are not aligned to 4 when K % 128 != 0; blocks past K: any scale,
+  // their codes are zero, but not a neighbour's NaN).
+  constexpr int kScaleRows = FP8 ? 1 : (G::BM + G::BN + G::kThreads - 1) / G::kThreads;
+  uint32_t sreg[kScaleRows];
+  auto load_scales = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < kScaleRows; i++) {
+      const int q = tid + i * G::kThreads;
+      const bool isA = q < G::BM;
+      const uint32_t off = (uint32_t)(isA ? q : q - G::BM) * sstride + (uint32_t)(4 * s);
+      if (kblocks % 4 == 0) {
+        const uint32_t a = __builtin_amdgcn_raw_buffer_load_b32(rSA, isA ? off : kOOB, 0, 0);
+        const uint32_t b = __builtin_amdgcn_raw_buffer_load_b32(rSB, isA ? kOOB : off, 0, 0);
+        sreg[i] = a | b;
+      } else {
+        sreg[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const bool in = 4 * s + j < kblocks;
+          const uint32_t a = __builtin_amdgcn_raw_buffer_load_b8(rSA, isA && in ? off + j : kOOB, 0, 0);
+          const uint32_t b = __builtin_amdgcn_raw_buffer_load_b8(rSB, !isA && in ? off + j : kOOB, 0, 0);
+          sreg[i] |= (a | b) << (8 * j);
+        }
+      }
+    }
+  };
+  auto store_scales = [&](uint8_t* stage) {
+#pragma unroll
+    for (int i = 0; i < kScaleRows; i++)
+      if (tid + i * G::kThreads < G::BM + G::BN)
+        *(uint32_t*)(stage + G::kOffS + (tid + i * G::kThreads) * 4) = sreg[i];
+  };
+
+  f32x4 acc[G::TMW][G::TNW], tot[OUT == kOutF32 ? G::TMW : 1][OUT == kOutF32 ? G::TNW : 1];
+#pragma unroll
+  for (int i = 0; i < G::TMW; i++)
+#pragma unroll
+    for (int j = 0; j < G::TNW; j++) {
+      acc[i][j] = f32x4{0, 0, 0, 0};
+      if (OUT == kOutF32) tot[i][j] = f32x4{0, 0, 0, 0};
+    }
+
+  float sb_next = FP8 ? sb_row[0] : 0.0f;
+  issue(0, smem);
+  if (!FP8) {
+    load_scales(0);
+    store_scales(smem);
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  for (int s = 0; s < nk; s++) {
+    const uint8_t* cur = smem + (s & 1) * G::kStage;
+    uint8_t* nxt = smem + ((s + 1) & 1) * G::kStage;
+    const float sb = sb_next;
+    if (s + 1 < nk) {
+      issue(s + 1, nxt);
+      if (!FP8) load_scales(s + 1);
+      if (FP8) sb_next = sb_row[s + 1];
+    }
+    if constexpr (FP8) {
+      // A lane's 32 bytes of the step: chunks g and g + 4 of its row (any
+      // order of K is right, if A's and B's are the same).
+      auto frag = [&](const uint8_t* rows, int row) {
+        const i32x4 lo = *(const i32x4*)(rows + row * 128 + ((g ^ swz<true>(row)) * 16));
+        const i32x4 hi = *(const i32x4*)(rows + row * 128 + (((g + 4) ^ swz<true>(row)) * 16));
+        return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      };
+      i32x8 bf[G::TNW];
+#pragma unroll
+      for (int j = 0; j < G::TNW; j++) bf[j] = frag(cur + G::kOffB, wn * 16 * G::TNW + j * 16 + r);
+      if constexpr (EXACT) {
+        bf16x8 be[G::TNW][4];
+#pragma unroll
+        for (int j = 0; j < G::TNW; j++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) be[j][q] = expand8(bf[j][2 * q], bf[j][2 * q + 1]);
+#pragma unroll
+        for (int i = 0; i < G::TMW; i++) {
+          const int row = wm * 16 * G::TMW + i * 16 + r;
+          const float f = *(const float*)(cur + G::kOffS + row * 4) * sb;
+          const i32x8 af = frag(cur, row);
+          bf16x8 ae[4];
+#pragma unroll
+          for (int q = 0; q < 4; q++) ae[q] = expand8(af[2 * q], af[2 * q + 1]);
+#pragma unroll
+          for (int j = 0; j < G::TNW; j++) {
+            f32x4 P = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; q++) P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(be[j][q], ae[q], P, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(P[e], f, acc[i][j][e]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < G::TMW; i++) {
+          const int row = wm * 16 * G::TMW + i * 16 + r;
+          const float f = *(const float*)(cur + G::kOffS + row * 4) * sb;
+          const i32x8 af = frag(cur, row);
+          f32x4 P[G::TNW];
+#pragma unroll
+          for (int j = 0; j < G::TNW; j++)
+            P[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, f32x4{0, 0, 0, 0}, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+          for (int j = 0; j < G::TNW; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(P[j][e], f, acc[i][j][e]);
+        }
+      }
+    } else {
+      // Lane (r, g) supplies K block g of its row and that block's scale.
+      auto frag = [&](const uint8_t* rows, int row) {
+        const i32x4 v = *(const i32x4*)(rows + row * 64 + ((g ^ swz<false>(row)) * 16));
+        return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      };
+      const uint8_t* sc = cur + G::kOffS;
+      i32x8 bf[G::TNW];
+      int sbb[G::TNW];
+#pragma unroll
+      for (int j = 0; j < G::TNW; j++) {
+        const int row = wn * 16 * G::TNW + j * 16 + r;
+        bf[j] = frag(cur + G::kOffB, row);
+        sbb[j] = sc[(G::BM + row) * 4 + g];
+      }
+#pragma unroll
+      for (int i = 0; i < G::TMW; i++) {
+        const int row = wm * 16 * G::TMW + i * 16 + r;
+        const i32x8 af = frag(cur, row);
+        const int sa = sc[row * 4 + g];
+#pragma unroll
+        for (int j = 0; j < G::TNW; j++)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, acc[i][j], 4, 4, 0, sbb[j], 0, sa);
+      }
+      if (s + 1 < nk) store_scales(nxt);
+    }
+    if constexpr (OUT == kOutF32) {
+      if ((s + 1) % kSegSteps == 0 && s + 1 < nk) {
+#pragma unroll
+        for (int i = 0; i < G::TMW; i++)
+#pragma unroll
+          for (int j = 0; j < G::TNW; j++) {
+            tot[i][j] += acc[i][j];
+            acc[i][j] = f32x4{0, 0, 0, 0};
+          }
+      }
+    }
+    // The next step's operands have arrived, and every wave is done with this
+    // step's buffer.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+
+  const bool vec_ok = p.ldc % 4 == 0;
+#pragma unroll
+  for (int i = 0; i < G::TMW; i++) {
+    const int lrow = wm * 16 * G::TMW + i * 16 + r;
+    if (lrow >= mrows) continue;
+#pragma unroll
+    for (int j = 0; j < G::TNW; j++) {
+      const int col = n0 + wn * 16 * G::TNW + j * 16 + 4 * g;
+      f32x4 v = acc[i][j];
+      if (OUT == kOutF32) v = nk > kSegSteps ? v + tot[i][j] : v;
+      const int64_t at = (int64_t)(t.row + lrow) * p.ldc + col;
+      if (vec_ok && col + 4 <= p.N) {
+        if (OUT == kOutF32)
+          *(f32x4*)((float*)p.C + at) = v;
+        else
+          *(u32x2*)((uint16_t*)p.C + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (col + e < p.N) {
+            if (OUT == kOutF32)
+              ((float*)p.C)[at + e] = v[e];
+            else
+              ((uint16_t*)p.C)[at + e] = bf16_bits(v[e]);
+          }
+      }
+    }
+  }
+}
+
+template <int FMT, bool EXACT, int OUT, class G>
+hipError_t launch(const Args& a, int64_t groups, hipStream_t s) {
+  Args p = a;
+  p.tiles_n = (int)((p.N + G::BN - 1) / G::BN);
+  const int64_t tm = p.offsets ? groups::max_row_tiles(p.M, groups, G::BM) : (p.M + G::BM - 1) / G::BM;
+  return launch_kernel(&gemm_block_kernel<FMT, EXACT, OUT, G>, dim3((unsigned)groups::grid_size(tm, p.tiles_n)),
+                       G::kThreads, 0, s, p);
+}
+
+}  // namespace
+
+// Whether the kernel's 32-bit offsets hold: 256 rows of codes and of scales,
+// and (for the smallest tiles) the grid.
+bool gemm_block_fits(int64_t M, int64_t N, int64_t K, int64_t groups) {
+  if (K > ((int64_t)1 << 22)) return false;
+  const int64_t tm = groups > 0 ? groups::max_row_tiles(M, groups, 128) : (M + 127) / 128;
+  return groups::grid_size(tm, (N + 127) / 128) < ((int64_t)1 << 31);
+}
+
+hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
+                      const void* b, const void* sb, const int32_t* offsets, int64_t groups,
+                      int out_dtype, void* c, int64_t ldc, hipStream_t s) {
+  const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
+               ldc, (int)groups, (int)M, (int)N, (int)K, 0};
+  const bool f32 = out_dtype == kOutF32;
+  if (fmt == kMXFP4) {
+    using G = Geo<kMXFP4, 4, 4, 2, 2>;
+    return f32 ? launch<kMXFP4, false, kOutF32, G>(p, groups, s) : launch<kMXFP4, false, kOutBF16, G>(p, groups, s);
+  }
+  using G = Geo<kFP8B128, 4, 4, 2, 2>;
+  return f32 ? launch<kFP8B128, true, kOutF32, G>(p, groups, s) : launch<kFP8B128, false, kOutBF16, G>(p, groups, s);
+}
+
+}  // namespace mx

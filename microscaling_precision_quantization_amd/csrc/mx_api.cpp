@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/mx.h"
@@ -18,19 +19,27 @@ bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 bool is_quant_fmt(int f) {
   return f == MX_FMT_MXFP4 || f == MX_FMT_MXFP8 || f == MX_FMT_NVFP4 || f == MX_FMT_MXFP8_E5M2 ||
-         f == MX_FMT_MXFP6_E3M2 || f == MX_FMT_MXFP4_MBS || f == MX_FMT_MXFP4_MBS16;
+         f == MX_FMT_MXFP6_E3M2 || f == MX_FMT_MXFP4_MBS || f == MX_FMT_MXFP4_MBS16 ||
+         f == MX_FMT_FP8_B128 || f == MX_FMT_FP8_B128X128;
 }
 bool is_mbs(int f) { return f == MX_FMT_MXFP4_MBS || f == MX_FMT_MXFP4_MBS16; }
-int block_of(int f) { return (f == MX_FMT_NVFP4 || f == MX_FMT_MXFP4_MBS16) ? 16 : 32; }
+bool is_fp8b(int f) { return f == MX_FMT_FP8_B128 || f == MX_FMT_FP8_B128X128; }
+int block_of(int f) {
+  if (is_fp8b(f)) return 128;
+  return (f == MX_FMT_NVFP4 || f == MX_FMT_MXFP4_MBS16) ? 16 : 32;
+}
+// fp32 scales need the alignment of a float, the others' bytes are read wide.
+bool scales_aligned(int f, const void* p) { return is_fp8b(f) ? aligned4(p) : aligned16(p); }
 // cols (and K) must be a multiple of this: the block, or the 128-element macro
 // block of MXFP4-MBS and MXFP4-MBS16.
-int granule_of(int f) { return is_mbs(f) ? 128 : block_of(f); }
+int granule_of(int f) { return is_mbs(f) ? 128 : block_of(f); }  // (the FP8 formats' block is 128)
 
 // Elements per tensor stay below 2^40 and every GEMM extent below 2^30 so that
 // the kernels' index arithmetic (int64 offsets, int extents) cannot overflow.
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxExtent = (int64_t)1 << 30;
 constexpr int64_t kW4A16MaxK = 65536;
+constexpr int64_t kMaxGroups = 65535;  // experts of a grouped GEMM (a grid dimension)
 
 mx_status hip_status(hipError_t e) {
   if (e == hipSuccess) return MX_OK;
@@ -44,7 +53,7 @@ int panel_width(int fmt) { return fmt == MX_FMT_MXFP4 ? 256 : 64; }
 
 // Code bytes of a row of cols elements.
 int64_t code_bytes(int fmt, int64_t cols) {
-  if (fmt == MX_FMT_MXFP8 || fmt == MX_FMT_MXFP8_E5M2) return cols;
+  if (fmt == MX_FMT_MXFP8 || fmt == MX_FMT_MXFP8_E5M2 || is_fp8b(fmt)) return cols;
   if (fmt == MX_FMT_MXFP6_E3M2) return cols * 3 / 4;
   return cols / 2;
 }
@@ -91,7 +100,7 @@ mx_status mx_quantize_layout(mx_format fmt, int block, mx_round rnd, int64_t row
   if (panel && !has_panel(fmt)) return MX_ERR_UNSUPPORTED;
   if (panel && !panel_shape_ok(fmt, rows, cols)) return MX_ERR_INVALID_ARG;
   if (!x || !codes || !scales) return MX_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MX_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !scales_aligned(fmt, scales)) return MX_ERR_INVALID_ARG;
   hipStream_t s = (hipStream_t)stream;
   if (fmt == MX_FMT_NVFP4) {
     if (!tensor_scale || !aligned4(tensor_scale)) return MX_ERR_INVALID_ARG;
@@ -101,6 +110,7 @@ mx_status mx_quantize_layout(mx_format fmt, int block, mx_round rnd, int64_t row
   }
   if (tensor_scale) return MX_ERR_INVALID_ARG;
   if (is_mbs(fmt)) return hip_status(mx::quant_mbs(rows, cols, x, codes, scales, s, block));
+  if (is_fp8b(fmt)) return hip_status(mx::quant_fp8(fmt, rows, cols, x, codes, scales, s));
   return hip_status(mx::quant_mx(fmt, rows, cols, x, codes, scales, s, false, false, panel));
 }
 
@@ -136,12 +146,14 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
   if (st != MX_OK) return st;
   if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return MX_ERR_UNSUPPORTED;
   if (!codes || !scales || !y) return MX_ERR_INVALID_ARG;
-  if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MX_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !scales_aligned(fmt, scales) || !aligned16(y)) return MX_ERR_INVALID_ARG;
   if (fmt == MX_FMT_NVFP4) {
     if (!tensor_scale || !aligned4(tensor_scale)) return MX_ERR_INVALID_ARG;
   } else if (tensor_scale) {
     return MX_ERR_INVALID_ARG;
   }
+  if (is_fp8b(fmt))
+    return hip_status(mx::dequant_fp8(fmt, rows, cols, codes, scales, out_dtype, y, (hipStream_t)stream));
   return hip_status(mx::dequant(fmt, rows, cols, codes, scales, tensor_scale, out_dtype, y,
                                 (hipStream_t)stream));
 }
@@ -171,7 +183,8 @@ mx_status gemm_impl(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, i
                    (fmt_a == MX_FMT_MXFP8_E5M2 || fmt_a == MX_FMT_MXFP6_E3M2);
   const bool mbs = (fmt_a == MX_FMT_MXFP4_MBS && fmt_b == MX_FMT_MXFP4_MBS && block == 32) ||
                    (fmt_a == MX_FMT_MXFP4_MBS16 && fmt_b == MX_FMT_MXFP4_MBS16 && block == 16);
-  if (!(w4a4 || w8a8 || nv || w4a16 || alt || mbs)) return MX_ERR_UNSUPPORTED;
+  const bool fp8b = fmt_a == MX_FMT_FP8_B128 && fmt_b == MX_FMT_FP8_B128X128 && block == 128;
+  if (!(w4a4 || w8a8 || nv || w4a16 || alt || mbs || fp8b)) return MX_ERR_UNSUPPORTED;
   // K-panel operands: the MXFP4 pair (either operand or both), or both
   // operands of the pairs on the 16-bit MFMAs.
   if ((panel_a || panel_b) && !w4a4 && !((w8a8 || nv || alt) && panel_a && panel_b))
@@ -182,8 +195,9 @@ mx_status gemm_impl(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, i
     return MX_ERR_INVALID_ARG;
   // K is a whole number of 32-element groups for every path (NVFP4 included:
   // its 16-blocks are staged in pairs).
-  if (K % 32 != 0 || (mbs && K % 128 != 0)) return MX_ERR_INVALID_ARG;
+  if (K % 32 != 0 || ((mbs || fp8b) && K % 128 != 0)) return MX_ERR_INVALID_ARG;
   if (ldc < N) return MX_ERR_INVALID_ARG;
+  if (fp8b && !mx::gemm_block_fits(M, N, K, 0)) return MX_ERR_INVALID_ARG;
   // Row tiles run along gridDim.y (at most 65535): 128 rows per tile for the
   // W4A4/W8A8 kernels, 16 for W4A16.
   if (M > (w4a16 ? 16 : 128) * (int64_t)65535) return MX_ERR_INVALID_ARG;
@@ -192,12 +206,12 @@ mx_status gemm_impl(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, i
   // 64 steps, the accumulation bound of mx.h.
   if (w4a16 && K > kW4A16MaxK) return MX_ERR_INVALID_ARG;
   if (!a || !b || !b_scales || !c) return MX_ERR_INVALID_ARG;
-  if (!aligned16(a) || !aligned16(b) || !aligned16(b_scales) || !aligned16(c))
+  if (!aligned16(a) || !aligned16(b) || !scales_aligned(fmt_b, b_scales) || !aligned16(c))
     return MX_ERR_INVALID_ARG;
   if (w4a16) {
     if (a_scales || a_ts || b_ts) return MX_ERR_INVALID_ARG;
   } else {
-    if (!a_scales || !aligned16(a_scales)) return MX_ERR_INVALID_ARG;
+    if (!a_scales || !scales_aligned(fmt_a, a_scales)) return MX_ERR_INVALID_ARG;
   }
   if (nv) {
     if (!a_ts || !b_ts || !aligned4(a_ts) || !aligned4(b_ts)) return MX_ERR_INVALID_ARG;
@@ -224,6 +238,8 @@ mx_status gemm_impl(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, i
   }
   if (w4a4)
     return hip_status(mx::gemm_mx(M, N, K, a, a_scales, b, b_scales, out_dtype, c, ldc, s));
+  if (fp8b)
+    return hip_status(mx::gemm_block(fmt_a, M, N, K, a, a_scales, b, b_scales, nullptr, 0, out_dtype, c, ldc, s));
   if (mbs)
     return hip_status(mx::gemm_mbs(M, N, K, a, a_scales, b, b_scales, out_dtype, c, ldc, s, block));
   if (w8a8 || nv)
@@ -281,6 +297,58 @@ mx_status mx_gemm_noalloc(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
   }
   return gemm_impl(fmt_a, fmt_b, block, rnd, M, N, K, a, a_scales, a_ts, b, b_scales, b_ts,
                    out_dtype, c, ldc, ws, need, stream, false, false);
+}
+
+mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, int64_t groups,
+                          int64_t M, int64_t N, int64_t K, const int32_t* offsets, const void* a,
+                          const void* a_scales, const void* b, const void* b_scales,
+                          mx_dtype out_dtype, void* c, int64_t ldc, void* stream) {
+  const bool w4a4 = fmt_a == MX_FMT_MXFP4 && fmt_b == MX_FMT_MXFP4 && block == 32;
+  const bool fp8b = fmt_a == MX_FMT_FP8_B128 && fmt_b == MX_FMT_FP8_B128X128 && block == 128;
+  if (!(w4a4 || fp8b)) return MX_ERR_UNSUPPORTED;
+  if (rnd != MX_ROUND_RNE) return MX_ERR_UNSUPPORTED;
+  if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return MX_ERR_UNSUPPORTED;
+  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxExtent || N > kMaxExtent || K > kMaxExtent)
+    return MX_ERR_INVALID_ARG;
+  if (groups <= 0 || groups > kMaxGroups || M > kMaxElems / K || groups * N > kMaxElems / K)
+    return MX_ERR_INVALID_ARG;
+  if (K % block != 0 || ldc < N) return MX_ERR_INVALID_ARG;
+  if (!mx::gemm_block_fits(M, N, K, groups)) return MX_ERR_INVALID_ARG;
+  if (!offsets || !aligned4(offsets)) return MX_ERR_INVALID_ARG;
+  if (!a || !a_scales || !b || !b_scales || !c) return MX_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(c)) return MX_ERR_INVALID_ARG;
+  if (!scales_aligned(fmt_a, a_scales) || !scales_aligned(fmt_b, b_scales)) return MX_ERR_INVALID_ARG;
+  return hip_status(mx::gemm_block(fmt_a, M, N, K, a, a_scales, b, b_scales, offsets, groups, out_dtype,
+                                   c, ldc, (hipStream_t)stream));
+}
+
+mx_status mx_norm_quantize(mx_format fmt, int block, mx_round rnd, int64_t rows, int64_t cols,
+                           const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                           const void* gate, int64_t gate_rows, const void* post_weight, float alpha,
+                           const void* weight, float eps, void* h, int64_t ldh, void* codes,
+                           void* scales, void* stream, mx_layout layout) {
+  if (fmt != MX_FMT_MXFP4 && fmt != MX_FMT_MXFP8 && fmt != MX_FMT_FP8_B128) return MX_ERR_UNSUPPORTED;
+  mx_status st = check_tensor(fmt, block, rnd, rows, cols);
+  if (st != MX_OK) return st;
+  if (layout != MX_LAYOUT_ROWS && layout != MX_LAYOUT_KPANEL) return MX_ERR_UNSUPPORTED;
+  const bool panel = layout == MX_LAYOUT_KPANEL;
+  if (panel && !has_panel(fmt)) return MX_ERR_UNSUPPORTED;
+  if (panel && !panel_shape_ok(fmt, rows, cols)) return MX_ERR_INVALID_ARG;
+  if (cols > mx::kNormMaxCols) return MX_ERR_INVALID_ARG;
+  // Rows are read and written 16 bytes at a time.
+  if (ldx < cols || ldx % 8 != 0 || rows > kMaxElems / ldx) return MX_ERR_INVALID_ARG;
+  if (residual && (ldr < cols || ldr % 8 != 0 || rows > kMaxElems / ldr)) return MX_ERR_INVALID_ARG;
+  if (h && (ldh < cols || ldh % 8 != 0 || rows > kMaxElems / ldh)) return MX_ERR_INVALID_ARG;
+  if (gate && gate_rows <= 0) return MX_ERR_INVALID_ARG;
+  // (negated, so that NaN fails too)
+  if (!(eps >= 0.0f && eps < HUGE_VALF) || !(alpha > -HUGE_VALF && alpha < HUGE_VALF)) return MX_ERR_INVALID_ARG;
+  if (!x || !codes || !scales) return MX_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !scales_aligned(fmt, scales)) return MX_ERR_INVALID_ARG;
+  if (!aligned16(residual) || !aligned16(gate) || !aligned16(post_weight) || !aligned16(weight) || !aligned16(h))
+    return MX_ERR_INVALID_ARG;
+  return hip_status(mx::norm_quantize(fmt, rows, cols, x, ldx, residual, ldr, gate, gate_rows, post_weight,
+                                      alpha, weight, eps, h, ldh, codes, scales, (hipStream_t)stream,
+                                      panel ? panel_width(fmt) : 0));
 }
 
 mx_status mx_pack(mx_format fmt, int block, int64_t rows, int64_t cols, const void* codes,

@@ -40,7 +40,7 @@ inline hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, siz
 
 // Format ids, kept equal to the public mx_format values.
 enum : int { kBF16 = 0, kMXFP4 = 1, kMXFP8 = 2, kNVFP4 = 3, kMXFP8E5M2 = 4, kMXFP6 = 5, kMXFP4MBS = 6,
-             kMXFP4MBS16 = 7 };
+             kMXFP4MBS16 = 7, kFP8B128 = 8, kFP8B128X128 = 9 };
 enum : int { kOutF32 = 0, kOutBF16 = 1 };
 
 // ---- quantize.hip
@@ -107,6 +107,29 @@ bool gemm_bf16x_large_fits(int fmt, int64_t M, int64_t N, int64_t K);
 hipError_t gemm_bf16x_large(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
                             const float* ta, const void* b, const void* sb, const float* tb,
                             int out_dtype, void* c, int64_t ldc, hipStream_t s, bool panel = false);
+
+// ---- fp8_block.hip: E4M3 codes under fp32 scales (kFP8B128: per 1 x 128,
+// scales [rows][cols/128]; kFP8B128X128: per 128 x 128, [ceil(rows/128)][cols/128])
+hipError_t quant_fp8(int fmt, int64_t rows, int64_t cols, const void* x, void* codes, void* scales,
+                     hipStream_t s);
+hipError_t dequant_fp8(int fmt, int64_t rows, int64_t cols, const void* codes, const void* scales,
+                       int out_dtype, void* y, hipStream_t s);
+
+// ---- gemm_block.hip: C = A B^T, dense (offsets null) or by expert (rows
+// offsets[g] .. offsets[g+1]-1 against weight g of `groups`, offsets on the
+// device). fmt: kMXFP4 (both operands) or kFP8B128 (B is kFP8B128X128).
+bool gemm_block_fits(int64_t M, int64_t N, int64_t K, int64_t groups);
+hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
+                      const void* b, const void* sb, const int32_t* offsets, int64_t groups,
+                      int out_dtype, void* c, int64_t ldc, hipStream_t s);
+
+// ---- norm_quantize.hip (kMXFP4, kMXFP8 or kFP8B128; cols at most kNormMaxCols;
+// panel: elements per K panel of the codes and scales, 0 for the row layout)
+constexpr int64_t kNormMaxCols = 32768;
+hipError_t norm_quantize(int fmt, int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                         const void* residual, int64_t ldr, const void* gate, int64_t gate_rows,
+                         const void* post_weight, float alpha, const void* weight, float eps, void* h,
+                         int64_t ldh, void* codes, void* scales, hipStream_t s, int panel);
 
 // ---- gemm_w4a16.hip: the library's own scratch for mx_gemm_noalloc (the
 // W4A16 split-K partials), a file-scope device array of this many bytes per

@@ -1,0 +1,105 @@
+"""Plain 64-bit forms of the block-scaled FP8 formats, the GEMM by expert and
+the fused norm + quantize, written from their definitions with numpy."""
+import numpy as np
+
+
+def e4m3_values():
+    c = np.arange(256)
+    e, m = (c >> 3) & 15, c & 7
+    v = np.where(e == 0, m * 2.0**-9, (8 + m) * 2.0 ** (e - 10.0))
+    v[(c & 127) == 127] = np.nan
+    return np.where(c & 128, -v, v)
+
+
+E4M3 = e4m3_values()
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6])
+
+
+def nearest_code(q, table):
+    """Code of the value of `table` (nonnegative, ascending) nearest |q|, ties
+    to the even code, saturating; and the sign."""
+    mid = (table[1:] + table[:-1]) / 2
+    lo = np.searchsorted(mid, np.abs(q), side="left")
+    hi = np.searchsorted(mid, np.abs(q), side="right")
+    return np.where(lo == hi, lo, lo + lo % 2), np.signbit(q)
+
+
+def e4m3_codes(q):
+    c, neg = nearest_code(q, E4M3[:127])
+    return (c + 128 * neg).astype(np.uint8)
+
+
+def near_border(q, table, tol):
+    """Whether |q| is within tol |q| of a midpoint of neighbouring values."""
+    mid = (table[1:] + table[:-1]) / 2
+    a = np.abs(q)
+    i = np.clip(np.searchsorted(mid, a), 1, len(mid) - 1)
+    return np.minimum(np.abs(a - mid[i]), np.abs(a - mid[i - 1])) <= tol * a
+
+
+def _fp8_blocks(v, axes):
+    """v: float64 holding the values exactly; amax over `axes`."""
+    with np.errstate(invalid="ignore", divide="ignore"):
+        amax = np.abs(v).max(axes, keepdims=True)
+        s = (amax.astype(np.float32) / np.float32(448)).astype(np.float32)
+        s = np.where(amax == 0, np.float32(1), s)
+        bad = ~np.isfinite(amax)
+        s = np.where(bad, np.float32(np.nan), s)
+        q = v / s.astype(np.float64)
+    return np.where(bad, 0, e4m3_codes(np.where(bad, 0.0, q))).astype(np.uint8), s
+
+
+def quantize_fp8(x, tall):
+    """Codes and fp32 scales of float64 [rows][cols]."""
+    rows, cols = x.shape
+    if not tall:
+        c, s = _fp8_blocks(x.reshape(rows, -1, 128), 2)
+        return c.reshape(rows, cols), s.reshape(rows, -1)
+    pad = np.concatenate([x, np.zeros((-rows % 128, cols))])
+    c, s = _fp8_blocks(pad.reshape(-1, 128, cols // 128, 128), (1, 3))
+    return c.reshape(-1, cols)[:rows], s.reshape(-1, cols // 128)
+
+
+def fp8_values(codes, scales, tall):
+    """float64 values (exact) of codes [rows][cols]."""
+    s = np.repeat(np.asarray(scales, np.float64), 128, 1)
+    if tall:
+        s = np.repeat(s, 128, 0)[: codes.shape[0]]
+    with np.errstate(invalid="ignore"):
+        return E4M3[codes] * s
+
+
+def mxfp4_values(codes, scales):
+    v = np.stack([E2M1[codes & 15], E2M1[codes >> 4]], -1).reshape(codes.shape[0], -1)
+    s = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    return v * np.repeat(s, 32, 1)
+
+
+def product(a, b):
+    """(A B^T, sum |a b|) in 64 bits."""
+    with np.errstate(invalid="ignore"):
+        return a @ b.T, np.abs(a) @ np.abs(b).T
+
+
+def grouped(a, b, offsets):
+    """a [M][K], b [G][N][K] values; rows of no group are NaN in S (unset)."""
+    c = np.zeros((a.shape[0], b.shape[1]))
+    s = np.full_like(c, np.nan)
+    for g in range(b.shape[0]):
+        r = slice(offsets[g], offsets[g + 1])
+        c[r], s[r] = product(a[r], b[g])
+    return c, s
+
+
+def norm_quantize_parts(x, weight, residual=None, gate=None, post=None, alpha=1.0, eps=1e-6):
+    """(h, n) in 64 bits."""
+    def norm(v, w):
+        return v / np.sqrt((v * v).mean(1, keepdims=True) + eps) * (1.0 if w is None else w)
+
+    with np.errstate(invalid="ignore", over="ignore"):
+        y = x if post is None else norm(x, post)
+        if gate is not None:
+            g = np.atleast_2d(gate)
+            y = y * np.repeat(g, x.shape[0] // g.shape[0], 0)
+        h = alpha * y + (0.0 if residual is None else residual)
+        return h, norm(h, weight)

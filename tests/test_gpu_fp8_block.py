@@ -1,0 +1,222 @@
+"""FP8 (E4M3) under fp32 scales per 1 x 128 and 128 x 128: codes and scales
+equal the definition's bit for bit, dequantized values their fp32 rounding,
+and every GEMM output lies within the bound of mx.h for its type."""
+import numpy as np
+import pytest
+import torch
+
+import llm_reference as ref
+import microscaling_precision_quantization_amd as mx
+from gpu_helpers import bf16_host_bits, dev_u8, host, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _bf16(a):
+    return torch.from_numpy(np.asarray(a, np.float32)).to(BF16)
+
+
+def _values(t):
+    return t.float().numpy().astype(np.float64)
+
+
+def _check_quantize(x, tall):
+    """x: bf16 host tensor."""
+    q = mx.quantize(x.cuda(), "fp8_b128x128" if tall else "fp8_b128")
+    codes, scales = ref.quantize_fp8(_values(x), tall)
+    assert q.scales.dtype == F32 and tuple(q.scales.shape) == scales.shape
+    assert np.array_equal(host(q.scales), scales, equal_nan=True)
+    assert np.array_equal(host(q.codes), codes)
+    return q
+
+
+def _mixed(rows, cols, seed):
+    """Normal values with large and tiny entries, zeros of both signs."""
+    r = np.random.RandomState(seed)
+    x = r.standard_normal((rows, cols)) * np.exp2(r.randint(-12, 6, (rows, cols)))
+    x[r.random_sample(x.shape) < 0.05] = 0.0
+    x[r.random_sample(x.shape) < 0.02] = -0.0
+    return _bf16(x)
+
+
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (1, 4096), (3, 256), (17, 1024), (127, 384), (128, 512),
+                                       (129, 640), (300, 1152)])
+def test_quantize_shapes(rows, cols, tall):
+    require_gpu()
+    _check_quantize(_mixed(rows, cols, rows + cols), tall)
+
+
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("power", [-133, -130, -126, -100, -70, -61, -60, -52, 0, 100, 118])
+def test_quantize_magnitudes(power, tall):
+    """Scales from the fp32 subnormals to near overflow, both sides of 2^-60."""
+    require_gpu()
+    r = np.random.RandomState(power + 200)
+    _check_quantize(_bf16(r.randint(-255, 256, (130, 256)) * 2.0**power), tall)
+
+
+@pytest.mark.parametrize("tall", [False, True])
+def test_quantize_ties(tall):
+    """amax = 448 * 2^k makes s a power of two: every midpoint of two E4M3
+    values is then an exact tie."""
+    require_gpu()
+    mid = (ref.E4M3[:126] + ref.E4M3[1:127]) / 2
+    row = np.concatenate([mid, [448.0, -448.0]])
+    x = np.stack([row, -row, row * 2.0**-20, row * 2.0**30])
+    _check_quantize(_bf16(x if not tall else np.concatenate([row[None], -row[None]])), tall)
+
+
+def test_quantize_every_bf16_value():
+    require_gpu()
+    bits = np.arange(1 << 16, dtype=np.uint32)
+    v = (bits << 16).astype(np.uint32).view(np.float32)
+    v = v[np.isfinite(v)]  # 65280 values: 510 blocks
+    _check_quantize(_bf16(v.reshape(-1, 128)), False)
+    r = np.random.RandomState(1)
+    _check_quantize(_bf16(r.permutation(v).reshape(-1, 128)), False)
+
+
+@pytest.mark.parametrize("tall", [False, True])
+def test_quantize_nonfinite_blocks(tall):
+    """A block with Inf or NaN: NaN scale, zero codes; its neighbours are not touched."""
+    require_gpu()
+    x = _mixed(260, 384, 5)
+    x[3, 130] = float("inf")
+    x[140, 5] = float("nan")
+    x[259, 383] = float("-inf")
+    q = _check_quantize(x, tall)
+    assert np.isnan(host(q.scales)).sum() == 3
+
+
+@pytest.mark.parametrize("fmt", ["fp8_b128", "fp8_b128x128"])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_dequantize(fmt, out):
+    require_gpu()
+    tall = fmt == "fp8_b128x128"
+    r = np.random.RandomState(3)
+    rows, cols = 131, 256
+    codes = r.randint(0, 256, (rows, cols)).astype(np.uint8)
+    shape = (2, 2) if tall else (rows, 2)
+    scales = np.exp2(r.uniform(-40, 40, shape)).astype(np.float32)
+    scales[0, 0] = np.nan
+    q = mx.QTensor(mx.FORMATS[fmt], rows, cols, dev_u8(codes), torch.from_numpy(scales).cuda())
+    y = mx.dequantize(q, out)
+    want = torch.from_numpy(ref.fp8_values(codes, scales, tall)).to(F32)
+    if out == F32:
+        assert np.array_equal(host(y), want.numpy(), equal_nan=True)
+    else:
+        w = want.to(BF16)
+        same = bf16_host_bits(y) == bf16_host_bits(w)
+        assert np.all(same | (np.isnan(want.numpy()) & np.isnan(host(y.float()))))
+
+
+def _operands(M, N, K, seed):
+    r = np.random.RandomState(seed)
+    a = _bf16(r.standard_normal((M, K)) * np.where(r.random_sample(K) < 0.01, 40, 1))
+    b = _bf16(r.standard_normal((N, K)) * 0.02)
+    return mx.quantize(a.cuda(), "fp8_b128"), mx.quantize(b.cuda(), "fp8_b128x128")
+
+
+def _val(q):
+    return ref.fp8_values(host(q.codes), host(q.scales), q.fmt == mx.MX_FMT_FP8_B128X128)
+
+
+def tolerance(c, s, out):
+    """mx.h: fp32 2^-18 sum|ab|; bf16 2^-10 sum|ab| from the FP8 MFMA, then half
+    a bf16 step (at most 2^-8 of the rounded value)."""
+    return 2.0**-18 * s if out == F32 else 2.0**-10 * s * (1 + 2.0**-8) + 2.0**-8 * np.abs(c)
+
+
+def check(got, c, s, out):
+    got = host(got.float()).astype(np.float64)
+    assert np.array_equal(np.isnan(got), np.isnan(c))
+    bad = np.abs(got - c) > tolerance(c, s, out)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], c[bad][:4])
+
+
+SHAPES = [(1, 1, 128), (1, 4096, 1024), (2, 17, 256), (7, 130, 640), (16, 512, 4096), (17, 129, 384),
+          (33, 255, 1152), (64, 64, 128), (100, 1000, 2432), (129, 257, 512), (300, 513, 1024),
+          (513, 385, 896)]
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gemm(M, N, K, out):
+    require_gpu()
+    a, b = _operands(M, N, K, M + N + K)
+    check(mx.gemm(a, b, out), *ref.product(_val(a), _val(b)), out)
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M", [3, 40, 260])
+def test_gemm_random_codes(M, out):
+    """Codes of every exponent, where the FP8 MFMA drops the most."""
+    require_gpu()
+    r = np.random.RandomState(M)
+    N, K = 150, 1024
+
+    def rand(rows, tall):
+        c = r.randint(0, 256, (rows, K)).astype(np.uint8)
+        c[(c & 127) == 127] = 0
+        s = np.exp2(r.uniform(-8, 8, (-(-rows // 128) if tall else rows, K // 128))).astype(np.float32)
+        return mx.QTensor(mx.FORMATS["fp8_b128x128" if tall else "fp8_b128"], rows, K, dev_u8(c), torch.from_numpy(s).cuda())
+
+    a, b = rand(M, False), rand(N, True)
+    check(mx.gemm(a, b, out), *ref.product(_val(a), _val(b)), out)
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M", [2, 200])
+def test_gemm_nan(M, out):
+    """A NaN scale of A reaches its row, one of B its 128 columns, a NaN code its row or column."""
+    require_gpu()
+    a, b = _operands(M, 200, 512, 9)
+    a.scales[1, 2] = float("nan")
+    b.scales[0, 3] = float("nan")
+    b.codes[150, 7] = 0x7F
+    c, s = ref.product(_val(a), _val(b))
+    assert np.isnan(c[0, :128]).all() and np.isnan(c[1]).all() and np.isnan(c[0, 150]) and np.isfinite(c[0, 151])
+    check(mx.gemm(a, b, out), c, s, out)
+
+
+@pytest.mark.parametrize("M,N,ld", [(5, 100, 104), (5, 100, 101), (150, 200, 333), (300, 260, 264)])
+def test_gemm_strided_out(M, N, ld):
+    """Only the M x N outputs are written."""
+    require_gpu()
+    a, b = _operands(M, N, 256, 11)
+    c, s = ref.product(_val(a), _val(b))
+    for out in (F32, BF16):
+        buf = torch.full((M + 2, ld), 7.0, dtype=out, device="cuda")
+        check(mx.gemm(a, b, out, out=buf[:M, :N]), c, s, out)
+        assert bool((buf[:, N:] == 7).all()) and bool((buf[M:] == 7).all())
+
+
+def test_gemm_long_chain_f32():
+    """Every product of one sign, K over one accumulation chain: still within 2^-18 sum|ab|."""
+    require_gpu()
+    r = np.random.RandomState(2)
+    K = 128 * 100
+    for M in (4, 140):
+        a = mx.quantize(_bf16(np.abs(r.standard_normal((M, K)))).cuda(), "fp8_b128")
+        b = mx.quantize(_bf16(np.abs(r.standard_normal((130, K)))).cuda(), "fp8_b128x128")
+        check(mx.gemm(a, b, F32), *ref.product(_val(a), _val(b)), F32)
+
+
+def test_gemm_repeats_and_streams():
+    """The same bits on every call, on any stream, two calls at once among them."""
+    require_gpu()
+    for M in (9, 150):
+        a, b = _operands(M, 300, 2048, 13)
+        first = mx.gemm(a, b, BF16)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        outs = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs += [mx.gemm(a, b, BF16) for _ in range(3)]
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o, first)

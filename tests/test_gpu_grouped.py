@@ -1,0 +1,179 @@
+"""GEMM by expert: every row against its expert's weight, within mx.h's bound;
+rows of no expert are left as they were."""
+import numpy as np
+import pytest
+import torch
+
+import llm_reference as ref
+import microscaling_precision_quantization_amd as mx
+from gpu_helpers import dev_u8, host, require_gpu
+from test_gpu_fp8_block import tolerance as fp8_tolerance
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _operands(fmt, M, G, N, K, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(M, K, generator=gen, device="cuda").to(BF16)
+    w = (torch.randn(G, N, K, generator=gen, device="cuda") * 0.02).to(BF16)
+    if fmt == "mxfp4":
+        return mx.quantize(x, "mxfp4"), mx.quantize(w, "mxfp4")
+    return mx.quantize(x, "fp8_b128"), mx.quantize(w, "fp8_b128x128")
+
+
+def _a_values(q):
+    c, s = host(q.codes), host(q.scales)
+    return ref.mxfp4_values(c, s) if q.fmt == mx.MX_FMT_MXFP4 else ref.fp8_values(c, s, False)
+
+
+def _b_values(q):
+    n = q.rows // q.groups
+    c, s = host(q.codes).reshape(q.groups, n, -1), host(q.scales).reshape(q.groups, -1, host(q.scales).shape[-1])
+    f = ref.mxfp4_values if q.fmt == mx.MX_FMT_MXFP4 else lambda c, s: ref.fp8_values(c, s, True)
+    return np.stack([f(c[g], s[g]) for g in range(q.groups)])
+
+
+def _tolerance(fmt, c, s, out):
+    if fmt == "fp8":
+        return fp8_tolerance(c, s, out)
+    return 2.0**-18 * s * (1 if out == F32 else 1 + 2.0**-8) + (0 if out == F32 else 2.0**-8 * np.abs(c))
+
+
+def _check(got, a, b, off, fmt, out):
+    c, s = ref.grouped(_a_values(a), _b_values(b), off)
+    rows = slice(off[0], off[-1])
+    err = np.abs(host(got.float()).astype(np.float64) - c)[rows]
+    bad = ~(err <= _tolerance(fmt, c, s, out)[rows])
+    assert not bad.any(), (np.argwhere(bad)[:4], err[bad][:4])
+
+
+def _offsets(sizes, start=0):
+    off = np.concatenate([[start], start + np.cumsum(sizes)]).astype(np.int32)
+    return off, torch.from_numpy(off).cuda()
+
+
+CASES = [  # sizes of the groups, N, K
+    ([1], 1, 128),
+    ([1], 300, 512),
+    ([0, 1, 0], 40, 256),
+    ([3, 0, 5, 1], 100, 384),
+    ([16, 17, 15, 0, 33], 130, 1024),
+    ([0, 0, 130, 1], 257, 640),
+    ([128, 129, 127], 128, 256),
+    ([200, 0, 300], 385, 512),
+    ([1] * 70, 48, 256),
+    ([0, 2, 1] * 50, 33, 128),
+    ([700], 260, 2048),
+]
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("sizes,N,K", CASES)
+def test_grouped(sizes, N, K, fmt, out):
+    require_gpu()
+    M = sum(sizes)
+    a, b = _operands(fmt, M, len(sizes), N, K, M + N)
+    off, d = _offsets(sizes)
+    _check(mx.gemm_grouped(a, b, d, out), a, b, off, fmt, out)
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("K", [32, 64, 96, 160, 224, 736, 1056, 2880])
+@pytest.mark.parametrize("sizes", [[2, 0, 3], [70, 150, 1]])
+def test_mxfp4_odd_k(K, sizes, out):
+    """K that is no multiple of a step. Every row's first scale byte is NaN but
+    the first block's codes are read only by their own row: a kernel that read
+    past a row's end would spread the NaN."""
+    require_gpu()
+    a, b = _operands("mxfp4", sum(sizes), len(sizes), 90, K, K)
+    off, d = _offsets(sizes)
+    _check(mx.gemm_grouped(a, b, d, out), a, b, off, "mxfp4", out)
+    a.scales[1::2, 0] = 255
+    got = mx.gemm_grouped(a, b, d, out)
+    assert bool(got[1::2].isnan().all()) and not bool(got[0::2].isnan().any())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("start,tail,sizes", [(0, 5, [4, 9]), (3, 0, [6, 0, 2]), (130, 140, [200, 31]),
+                                              (2, 300, [0, 0]), (0, 0, [300, 20])])
+def test_rows_of_no_group_are_left(fmt, start, tail, sizes):
+    require_gpu()
+    M, N, K = start + sum(sizes) + tail, 200, 256
+    a, b = _operands(fmt, M, len(sizes), N, K, 3)
+    off, d = _offsets(sizes, start)
+    for out, ld in ((F32, 200), (BF16, 203), (BF16, 208)):
+        buf = torch.full((M + 1, ld), 7.0, dtype=out, device="cuda")
+        got = mx.gemm_grouped(a, b, d, out, out=buf[:M, :N])
+        _check(got, a, b, off, fmt, out)
+        assert bool((buf[:start] == 7).all()) and bool((buf[start + sum(sizes):] == 7).all())
+        assert bool((buf[:, N:] == 7).all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+def test_offsets_past_the_end_are_clamped(fmt):
+    """Row numbers beyond [0, M] are read as 0 or M."""
+    require_gpu()
+    for M in (20, 400):
+        a, b = _operands(fmt, M, 3, 64, 256, 4)
+        d = torch.tensor([-5, M // 2, M // 2, M + 1000], dtype=torch.int32, device="cuda")
+        off = np.array([0, M // 2, M // 2, M])
+        _check(mx.gemm_grouped(a, b, d, BF16), a, b, off, fmt, BF16)
+
+
+def test_more_groups_than_a_wave():
+    """Row tiles are found by scanning the groups 64 at a time."""
+    require_gpu()
+    r = np.random.RandomState(0)
+    for fmt in ("mxfp4", "fp8"):
+        for G, M in ((64, 900), (65, 40), (200, 2000), (300, 7)):
+            sizes = r.multinomial(M, r.dirichlet(np.full(G, 0.3)))
+            a, b = _operands(fmt, M, G, 64, 128, G)
+            off, d = _offsets(sizes)
+            _check(mx.gemm_grouped(a, b, d, BF16), a, b, off, fmt, BF16)
+
+
+def test_equals_gemm_of_each_expert():
+    """With every group a whole dense product, the same result within both bounds; FP8 weights
+    whose rows are no multiple of 128 keep each expert's own tiles."""
+    require_gpu()
+    a, b = _operands("fp8", 96, 3, 100, 512, 8)
+    assert tuple(b.scales.shape) == (3, 1, 4)
+    off, d = _offsets([40, 30, 26])
+    got = mx.gemm_grouped(a, b, d, F32)
+    whole = mx.dequantize(b)
+    for g in range(3):
+        one = mx.QTensor(b.fmt, 100, 512, b.codes[100 * g:100 * (g + 1)], b.scales[g].contiguous())
+        assert torch.equal(mx.dequantize(one), whole[100 * g:100 * (g + 1)])
+        rows = slice(off[g], off[g + 1])
+        ag = mx.QTensor(a.fmt, rows.stop - rows.start, 512, a.codes[rows], a.scales[rows])
+        assert torch.allclose(mx.gemm(ag, one, F32), got[rows], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+def test_captured_with_new_offsets(fmt):
+    """A captured call follows the offsets of each replay: they are read on the device."""
+    require_gpu()
+    M, G, N, K = 150, 6, 256, 512
+    a, b = _operands(fmt, M, G, N, K, 6)
+    _, d = _offsets([25] * 6)
+    out = torch.zeros(M, N, dtype=BF16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mx.gemm_grouped(a, b, d, BF16, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.gemm_grouped(a, b, d, BF16, out=out)
+    for sizes in ([150, 0, 0, 0, 0, 0], [1, 2, 3, 4, 5, 135], [0, 0, 75, 0, 75, 0]):
+        off, new = _offsets(sizes)
+        d.copy_(new)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(out, a, b, off, fmt, BF16)
+        assert torch.equal(out, mx.gemm_grouped(a, b, new, BF16))
