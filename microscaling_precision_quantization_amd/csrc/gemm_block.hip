@@ -335,10 +335,15 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
   const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
   const bool f32 = out_dtype == kOutF32;
+  const int64_t per = offsets ? M / groups : M;
   if (fmt == kMXFP4) {
+    if (per >= 192 && gemm_mxfp4_fits(0, N, K))
+      return gemm_mxfp4_grouped(M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
     using G = Geo<kMXFP4, 4, 4, 2, 2>;
     return f32 ? launch<kMXFP4, false, kOutF32, G>(p, groups, s) : launch<kMXFP4, false, kOutBF16, G>(p, groups, s);
   }
+  if (!f32 && per >= 192)
+    return gemm_fp8_large(M, N, K, a, sa, b, sb, offsets, groups, c, ldc, s);
   using G = Geo<kFP8B128, 4, 4, 2, 2>;
   return f32 ? launch<kFP8B128, true, kOutF32, G>(p, groups, s) : launch<kFP8B128, false, kOutBF16, G>(p, groups, s);
 }

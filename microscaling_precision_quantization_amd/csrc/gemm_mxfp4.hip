@@ -48,6 +48,7 @@
 // of 4 consecutive columns of one row of C.
 #include <type_traits>
 
+#include "groups.h"
 #include "mx_internal.h"
 #include "tile256.h"
 
@@ -295,11 +296,14 @@ __device__ __forceinline__ void interleave_last() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int OUT, bool PANEL_A, bool PANEL_B>
+// GROUPED: by expert (groups.h; row layout). The pointers then move to the
+// tile's first row and its expert's weight, M to the rows left in the group.
+template <int OUT, bool PANEL_A, bool PANEL_B, bool GROUPED = false>
 __global__ __launch_bounds__(kThreads, 1) void gemm_mxfp4_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ SA, const uint8_t* __restrict__ B,
     const uint8_t* __restrict__ SB, void* __restrict__ C, int64_t ldc, int M, int N, int K,
-    int tiles_m, int tiles_n, int s_begin, int s_end, int fold) {
+    int tiles_m, int tiles_n, int s_begin, int s_end, int fold, const int* __restrict__ offsets,
+    int groups) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -307,7 +311,20 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mxfp4_kernel(
   const int r = lane & 31, g = lane >> 5;
 
   int tm, tn;
-  tile256::tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  if constexpr (GROUPED) {
+    groups::Tile t;
+    if (!groups::tile_of<BM>(offsets, groups, M, tiles_n, blockIdx.x, t)) return;
+    tm = 0;
+    tn = t.tn;
+    M = min(t.rows, BM);
+    A += (int64_t)t.row * (K / 2);
+    SA += (int64_t)t.row * (K / 32);
+    B += (int64_t)t.group * N * (K / 2);
+    SB += (int64_t)t.group * N * (K / 32);
+    C = (uint8_t*)C + t.row * ldc * (OUT == kOutF32 ? 4 : 2);
+  } else {
+    tile256::tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  }
   const int m0 = tm * BM, n0 = tn * BN;
 
   const uint32_t rowbytes = (uint32_t)(K / 2), scalebytes = (uint32_t)(K / 32);
@@ -466,13 +483,29 @@ hipError_t launch(dim3 grid, hipStream_t s, bool panel_a, bool panel_b, const ui
             const uint8_t* SA, const uint8_t* B, const uint8_t* SB, void* c, int64_t ldc, int m,
             int n, int k, int tm, int tn, int s0, int s1, int fold) {
   if (panel_a && panel_b)
-    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, true, true>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold));
+    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, true, true>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold, nullptr, 0));
   else if (panel_a)
-    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, true, false>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold));
+    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, true, false>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold, nullptr, 0));
   else if (panel_b)
-    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, false, true>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold));
+    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, false, true>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold, nullptr, 0));
   else
-    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, false, false>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold));
+    MX_TRY(launch_kernel(&gemm_mxfp4_kernel<OUT, false, false>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc, m, n, k, tm, tn, s0, s1, fold, nullptr, 0));
+  return hipSuccess;
+}
+
+// One launch, or (fp32 output) one per accumulation chain: run(first
+// super-step, end, fold bits).
+template <typename Run>
+hipError_t in_segments(int nsteps, int out_dtype, Run run) {
+  // fp32 accumulation chains of at most 48 MFMAs (tile256::fold_tile): K in
+  // segments of 12 super-steps, one launch each, every launch after the
+  // first adding its sums into C (launches on one stream run in order).
+  constexpr int kSeg = 12;
+  if (out_dtype != kOutF32 || nsteps <= kSeg) return run(0, nsteps, 0);
+  for (int s0 = 0; s0 < nsteps; s0 += kSeg) {
+    const int s1 = s0 + kSeg < nsteps ? s0 + kSeg : nsteps;
+    MX_TRY(run(s0, s1, 1 | (s0 == 0 ? 2 : 0) | (s1 == nsteps ? 4 : 0)));
+  }
   return hipSuccess;
 }
 
@@ -483,22 +516,27 @@ hipError_t gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* a, const void
   const dim3 grid((unsigned)(tm * tn));
   const uint8_t *A = (const uint8_t*)a, *SA = (const uint8_t*)sa, *B = (const uint8_t*)b,
                 *SB = (const uint8_t*)sb;
-  const int nsteps = (int)(K / kSuperK);
-  if (out_dtype == kOutF32) {
-    // fp32 accumulation chains of at most 48 MFMAs (tile256::fold_tile): K in
-    // segments of 12 super-steps, one launch each, every launch after the
-    // first adding its sums into C (launches on one stream run in order).
-    constexpr int kSeg = 12;
-    if (nsteps <= kSeg)
-      return launch<kOutF32>(grid, s, panel_a, panel_b, A, SA, B, SB, c, ldc, (int)M, (int)N, (int)K, tm, tn, 0, nsteps, 0);
-    for (int s0 = 0; s0 < nsteps; s0 += kSeg) {
-      const int s1 = s0 + kSeg < nsteps ? s0 + kSeg : nsteps;
-      const int fold = 1 | (s0 == 0 ? 2 : 0) | (s1 == nsteps ? 4 : 0);
-      MX_TRY(launch<kOutF32>(grid, s, panel_a, panel_b, A, SA, B, SB, c, ldc, (int)M, (int)N, (int)K, tm, tn, s0, s1, fold));
-    }
-    return hipSuccess;
-  }
-  return launch<kOutBF16>(grid, s, panel_a, panel_b, A, SA, B, SB, c, ldc, (int)M, (int)N, (int)K, tm, tn, 0, nsteps, 0);
+  return in_segments((int)(K / kSuperK), out_dtype, [&](int s0, int s1, int fold) {
+    if (out_dtype == kOutF32)
+      return launch<kOutF32>(grid, s, panel_a, panel_b, A, SA, B, SB, c, ldc, (int)M, (int)N, (int)K, tm, tn, s0, s1, fold);
+    return launch<kOutBF16>(grid, s, panel_a, panel_b, A, SA, B, SB, c, ldc, (int)M, (int)N, (int)K, tm, tn, s0, s1, fold);
+  });
+}
+
+hipError_t gemm_mxfp4_grouped(int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
+                              const void* b, const void* sb, const int32_t* offsets, int64_t groups,
+                              int out_dtype, void* c, int64_t ldc, hipStream_t s) {
+  const int tn = (int)((N + BN - 1) / BN);
+  const dim3 grid((unsigned)groups::grid_size(groups::max_row_tiles(M, groups, BM), tn));
+  const uint8_t *A = (const uint8_t*)a, *SA = (const uint8_t*)sa, *B = (const uint8_t*)b,
+                *SB = (const uint8_t*)sb;
+  return in_segments((int)(K / kSuperK), out_dtype, [&](int s0, int s1, int fold) {
+    if (out_dtype == kOutF32)
+      return launch_kernel(&gemm_mxfp4_kernel<kOutF32, false, false, true>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc,
+                           (int)M, (int)N, (int)K, 0, tn, s0, s1, fold, offsets, (int)groups);
+    return launch_kernel(&gemm_mxfp4_kernel<kOutBF16, false, false, true>, grid, kThreads, 0, s, A, SA, B, SB, c, ldc,
+                         (int)M, (int)N, (int)K, 0, tn, s0, s1, fold, offsets, (int)groups);
+  });
 }
 
 }  // namespace mx

@@ -20,8 +20,8 @@ inline int64_t max_row_tiles(int64_t M, int64_t n, int64_t bm) {
 }
 
 // Workgroups of a 1-D grid for that many row tiles and tiles_n column tiles:
-// a multiple of 8, for tile_of below.
-inline int64_t grid_size(int64_t row_tiles, int64_t tiles_n) { return (row_tiles * tiles_n + 7) / 8 * 8; }
+// two multiples of 8 (whole and partly filled tiles), for tile_of below.
+inline int64_t grid_size(int64_t row_tiles, int64_t tiles_n) { return (row_tiles * tiles_n + 14) / 8 * 8; }
 
 struct Tile {
   int group;         // weight
@@ -35,62 +35,83 @@ __device__ __forceinline__ void rows_of(const int* offsets, int M, int g, int& l
   hi = max(min(offsets[g + 1], M), lo);
 }
 
-// Inclusive sum of v over the lanes up to this one.
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// v of another lane by DPP, 0 where there is none (or ROWS leaves the row out).
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp0(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+
+// Inclusive sum of v over the lanes up to this one: within rows of 16 lanes
+// (row_shr 1, 2, 4, 8), then the last lane of row 0 and 2 into the next row
+// (row_bcast 15) and that of the first two rows into the last two (row_bcast 31).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += dpp0<0x111>(v);
+  v += dpp0<0x112>(v);
+  v += dpp0<0x114>(v);
+  v += dpp0<0x118>(v);
+  v += dpp0<0x142, 0xA>(v);
+  v += dpp0<0x143, 0xC>(v);
   return v;
 }
 
 // Tile of workgroup `bid`; false: there is none. offsets null: one group of
-// all M rows. Workgroup ids go round-robin over the 8 XCDs; XCD x gets tiles
-// [x c, (x + 1) c) of the tiles that there are, rastered in groups of 4 row
-// tiles, so that its L2 holds the rows and columns its tiles share.
+// all M rows. Whole tiles come first, partly filled ones, which take less
+// time, last, so that they even out the end of the launch. Workgroup ids go
+// round-robin over the 8 XCDs; XCD x gets an eighth of each kind in a row,
+// rastered in groups of 4 row tiles, so that its L2 holds the rows and
+// columns its tiles share.
 template <int BM>
 __device__ __forceinline__ bool tile_of(const int* offsets, int n, int M, int tiles_n, int bid, Tile& t) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
-  int lo = 0, hi = 0, scan = 0;
+  // Each lane's group (of 64 at a time), and the scan of the whole tiles times
+  // 128 plus the partly filled ones, at most 64 in a wave.
+  int lo = 0, hi = 0, scan = 0, whole = 0, part = 0;
+  auto look = [&](int c) {
+    lo = hi = 0;
+    if (c + lane < n) rows_of(offsets, M, c + lane, lo, hi);
+    scan = wave_scan((hi - lo) / BM * 128 + ((hi - lo) % BM != 0));
+    return __builtin_amdgcn_readlane(scan, 63);
+  };
   if (!offsets) {
-    total = (M + BM - 1) / BM;
+    whole = M / BM;
+    part = M % BM != 0;
   } else {
     for (int c = 0; c < n; c += 64) {
-      lo = hi = 0;
-      if (c + lane < n) rows_of(offsets, M, c + lane, lo, hi);
-      scan = wave_scan((hi - lo + BM - 1) / BM, lane);
-      total += __builtin_amdgcn_readlane(scan, 63);
+      const int all = look(c);
+      whole += all / 128;
+      part += all % 128;
     }
   }
-  const int tiles = total * tiles_n, share = (tiles + 7) / 8;
-  const int i = bid / 8, id = (bid % 8) * share + i;
-  if (i >= share || id >= tiles) return false;
+  const int i = bid / 8, x = bid % 8;
+  const int share = (whole * tiles_n + 7) / 8, share2 = (part * tiles_n + 7) / 8;
+  const bool first = i < share;
+  const int id = first ? x * share + i : x * share2 + i - share;
+  const int rows = first ? whole : part;
+  if (i >= share + share2 || id >= rows * tiles_n) return false;
   constexpr int GM = 4;
-  const int first = id / (GM * tiles_n) * GM, width = min(total - first, GM);
+  const int top = id / (GM * tiles_n) * GM, width = min(rows - top, GM);
   const int within = id % (GM * tiles_n);
-  int tm = first + within % width;
+  int tm = top + within % width;
   t.tn = within / width;
   if (!offsets) {
     t.group = 0;
-    t.row = tm * BM;
+    t.row = first ? tm * BM : whole * BM;
     t.rows = M - t.row;
     return true;
   }
   for (int c = 0; c < n; c += 64) {
-    if (n > 64) {  // (otherwise the values are those of the loop above)
-      lo = hi = 0;
-      if (c + lane < n) rows_of(offsets, M, c + lane, lo, hi);
-      scan = wave_scan((hi - lo + BM - 1) / BM, lane);
-    }
-    const int sum = __builtin_amdgcn_readlane(scan, 63);
+    if (n > 64) look(c);  // (otherwise the values are those of the loop above)
+    const int upto = first ? scan / 128 : scan % 128;
+    const int sum = __builtin_amdgcn_readlane(upto, 63);
     if (tm < sum) {
-      const int l = __builtin_ctzll(__ballot(scan > tm));
-      const int before = l ? __builtin_amdgcn_readlane(scan, l - 1) : 0;
-      t.group = c + l;
-      t.row = __builtin_amdgcn_readlane(lo, l) + (tm - before) * BM;
-      t.rows = __builtin_amdgcn_readlane(hi, l) - t.row;
+      const int l = __builtin_ctzll(__ballot(upto > tm));
+      const int before = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0;
+      const int glo = __builtin_amdgcn_readlane(lo, l), ghi = __builtin_amdgcn_readlane(hi, l);
+      // (Uniform as they are; said so, for the compiler to keep them in scalars.)
+      t.group = __builtin_amdgcn_readfirstlane(c + l);
+      t.row = __builtin_amdgcn_readfirstlane(first ? glo + (tm - before) * BM : glo + (ghi - glo) / BM * BM);
+      t.rows = __builtin_amdgcn_readfirstlane(ghi - t.row);
+      t.tn = __builtin_amdgcn_readfirstlane(t.tn);
       return true;
     }
     tm -= sum;

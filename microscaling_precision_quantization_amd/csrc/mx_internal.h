@@ -90,6 +90,11 @@ hipError_t gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void* a, const void
                       const void* b, const void* sb, int out_dtype, void* c, int64_t ldc,
                       hipStream_t s, bool panel_a, bool panel_b);
 
+// By expert (gemm_block's arguments), row layout.
+hipError_t gemm_mxfp4_grouped(int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
+                              const void* b, const void* sb, const int32_t* offsets, int64_t groups,
+                              int out_dtype, void* c, int64_t ldc, hipStream_t s);
+
 // ---- pack.hip (codes and scales into the K-panel layout): `panels` panels,
 // wb code bytes (a multiple of 16) and sb scale bytes (8, 4 or 2) per row
 // and panel.
@@ -122,6 +127,11 @@ bool gemm_block_fits(int64_t M, int64_t N, int64_t K, int64_t groups);
 hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
                       const void* b, const void* sb, const int32_t* offsets, int64_t groups,
                       int out_dtype, void* c, int64_t ldc, hipStream_t s);
+
+// ---- gemm_fp8_large.hip (256 x 256 tiles, bf16 result; gemm_block's FP8 shapes)
+hipError_t gemm_fp8_large(int64_t M, int64_t N, int64_t K, const void* a, const void* sa, const void* b,
+                          const void* sb, const int32_t* offsets, int64_t groups, void* c, int64_t ldc,
+                          hipStream_t s);
 
 // ---- norm_quantize.hip (kMXFP4, kMXFP8 or kFP8B128; cols at most kNormMaxCols;
 // panel: elements per K panel of the codes and scales, 0 for the row layout)
