@@ -336,6 +336,8 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
   const bool f32 = out_dtype == kOutF32;
   const int64_t per = offsets ? M / groups : M;
+  if (per <= 64 && gemm_few_rows_fits(K, out_dtype))
+    return gemm_few_rows(fmt, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
   if (fmt == kMXFP4) {
     if (per >= 192 && gemm_mxfp4_fits(0, N, K))
       return gemm_mxfp4_grouped(M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);

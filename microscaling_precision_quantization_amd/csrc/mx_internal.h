@@ -133,6 +133,13 @@ hipError_t gemm_fp8_large(int64_t M, int64_t N, int64_t K, const void* a, const 
                           const void* sb, const int32_t* offsets, int64_t groups, void* c, int64_t ldc,
                           hipStream_t s);
 
+// ---- gemm_few_rows.hip (few rows of A, or few per expert: weights streamed
+// once per 16, 32 or 64 rows; gemm_block's shapes and arguments)
+bool gemm_few_rows_fits(int64_t K, int out_dtype);
+hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
+                         const void* b, const void* sb, const int32_t* offsets, int64_t groups,
+                         int out_dtype, void* c, int64_t ldc, hipStream_t s);
+
 // ---- norm_quantize.hip (kMXFP4, kMXFP8 or kFP8B128; cols at most kNormMaxCols;
 // panel: elements per K panel of the codes and scales, 0 for the row layout)
 constexpr int64_t kNormMaxCols = 32768;
