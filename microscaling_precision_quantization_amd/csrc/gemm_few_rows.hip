@@ -5,16 +5,25 @@
 //
 // Bound by HBM: every weight byte is read once and meets 16 MT rows of A, so
 // the kernel is a stream of weights from HBM through VGPRs to the matrix core.
-//  * A workgroup takes 16 NT weight rows of one expert; its waves split K step by
-//    step, so that together they read 128 kWaves contiguous bytes of a row, and
-//    their sums meet in LDS at the end, in a fixed order.
-//  * A step is 128 bytes of a row (128 K of FP8, 256 K of MXFP4): lane (r, g) =
-//    (l % 16, l / 16) reads bytes 16 g and 64 + 16 g of row r of each tile, 64
-//    contiguous bytes a row and load; the same order of K in A. Operands and
-//    scales go through a ring of kDepth steps in VGPRs.
+//  * A workgroup takes T tiles of 16 weight rows of one expert. K goes to its
+//    waves in chunks of W S steps of 128 bytes (128 K of FP8, 256 K of
+//    MXFP4), S consecutive steps each. A wave keeps A's fragments (and scales) of
+//    its S steps in VGPRs and runs tile by tile: its loads are 16 rows x 128 S
+//    contiguous bytes, which keeps DRAM pages open, and A's cost is shared
+//    by T tiles. The waves' sums meet in LDS at the end, in a fixed order.
+//  * Weights go HBM -> LDS directly, whole 128-byte lines, 8 rows a load, into a
+//    ring of D steps of the wave's own: no barrier, D - 1 steps in flight, and no
+//    VGPRs for them. The loads are non-temporal (38 us instead of 43). (Loading fragments, 64 bytes of 16 rows a load, into VGPRs
+//    reached 4.5-5.2 TB/s at 16 x 28672 x 8192; this does 6.1.) The chunk swizzle of
+//    LDS rows is gemm_block.hip's.
+//  * In a step lane (r, g) = (l % 16, l / 16) takes chunks g and g + 4 of row r of
+//    the tile; the same order of K in A.
 //  * Loads are range-checked buffer loads without a branch: rows past the
 //    group's or N, steps past K and 32-element blocks past K read as zeros.
 //  * A group with more than 16 MT rows takes further passes over the weights.
+#include <type_traits>
+#include <utility>
+
 #include "bf16.h"
 #include "groups.h"
 #include "mx_internal.h"
@@ -31,7 +40,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
 constexpr uint32_t kOOB = 0x80000000u;        // an offset past every buffer's range
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+constexpr int kNonTemporal = 2;                // cache policy of a load: streamed
 
 struct Args {
   const uint8_t *A, *SA, *B, *SB;
@@ -51,39 +61,84 @@ __device__ __forceinline__ bf16x8 expand8(int lo, int hi) {
   return __builtin_bit_cast(bf16x8, o);
 }
 
-// A lane's share of one step: 32 bytes of MT rows of A and NT of B, and the
-// scales. FP8: s_A of the row (sa[m][0]), s_B (sb[0][0]). MXFP4: dwords 0 and 1
-// hold the scales of the step's blocks 0..3 and 4..7 of the row.
-template <int MT, int NT>
-struct Step {
-  i32x4 a[MT][2], b[NT][2];
-  u32x2 sa[MT], sb[NT];
-};
+template <typename F, int... K>
+__device__ __forceinline__ void unroll_at(F&& f, std::integer_sequence<int, K...>) {
+  (f(std::integral_constant<int, K>{}), ...);
+}
+// f(0), f(1), ..., f(N - 1), each with its number as a constant.
+template <int N, typename F>
+__device__ __forceinline__ void unroll(F&& f) {
+  unroll_at(std::forward<F>(f), std::make_integer_sequence<int, N>{});
+}
 
 // ALIGNED: a row's MXFP4 scales start on dwords (K % 128 = 0).
-template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int MT, int NT, int DEPTH>
-__global__ __launch_bounds__(kThreads) void gemm_few_rows_kernel(Args p) {
-  __shared__ float part[kWaves][MT][NT][4][64];
+// W: waves.
+template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int MT, int S, int T, int D>
+__global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
+  constexpr int kWaves = W;
+  constexpr int kSlot = 2048, kRing = kWaves * D * kSlot, kSums = kWaves * MT * T * 4 * 64 * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing > kSums ? kRing : kSums];
+  float(*part)[MT][T][4][64] = (float(*)[MT][T][4][64])smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * (16 * NT), group = blockIdx.y;
+  const int n0 = blockIdx.x * (16 * T), group = blockIdx.y;
   int lo = 0, hi = p.M;
   if (p.offsets) groups::rows_of(p.offsets, p.M, group, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
   if (lo >= hi) return;
 
-  const int nrows = min(p.N - n0, 16 * NT);
+  const int nrows = min(p.N - n0, 16 * T);
   const uint32_t rowbytes = (uint32_t)(FP8 ? p.K : p.K / 2);
   const int nk = (int)((rowbytes + 127) / 128);
-  const int steps = (nk + kWaves - 1) / kWaves;  // of each wave
-  // Scale bytes per row, and the weights' first scale.
-  const uint32_t sstride = FP8 ? (uint32_t)(nk * 4) : (uint32_t)(p.K / 32);
+  const uint32_t sstride = FP8 ? (uint32_t)(nk * 4) : (uint32_t)(p.K / 32);  // scale bytes per row
   const int64_t brow = (int64_t)group * p.N + n0;
   const __amdgpu_buffer_rsrc_t rB = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(p.B + brow * rowbytes), 0, (int)((uint32_t)nrows * rowbytes), kRsrcFlags);
+  // FP8: the scale rows of this workgroup's 128-row blocks (they may be two or more).
+  const int nb0 = n0 / 128, nbs = (p.N + 127) / 128;
   const __amdgpu_buffer_rsrc_t rSB =
-      FP8 ? __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(p.SB + ((int64_t)group * ((p.N + 127) / 128) + n0 / 128) * sstride), 0, (int)sstride, kRsrcFlags)
+      FP8 ? __builtin_amdgcn_make_buffer_rsrc((void*)(p.SB + ((int64_t)group * nbs + nb0) * sstride), 0,
+                                              (int)((uint32_t)(nbs - nb0) * sstride), kRsrcFlags)
           : __builtin_amdgcn_make_buffer_rsrc((void*)(p.SB + brow * sstride), 0, (int)((uint32_t)nrows * sstride), kRsrcFlags);
+  // Lane offsets within a tile, for A's fragments (row r, chunks g and g + 4)
+  // and for the weights' loads (row l / 8 + 8 h, the chunk that belongs into slot
+  // l % 8): the step and the tile go into the scalar offset, which the range
+  // check counts too. In the last step of an MXFP4 row that is no multiple
+  // of 256 K long, chunks past its end are left out.
+  const uint32_t left = rowbytes - 128u * (uint32_t)(nk - 1);
+  uint32_t va[2], va_last[2], vb[2], vb_last[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const uint32_t ca = 16u * (uint32_t)(g + 4 * h), cb = 16u * (uint32_t)((lane & 7) ^ (4 * h + (lane >> 4)));
+    va[h] = (uint32_t)r * rowbytes + ca;
+    vb[h] = (uint32_t)(8 * h + (lane >> 3)) * rowbytes + cb;
+    va_last[h] = FP8 || ca < left ? va[h] : kOOB;
+    vb_last[h] = FP8 || cb < left ? vb[h] : kOOB;
+  }
+  const uint32_t soff = (uint32_t)r * sstride;
+  const int chunks = (nk + kWaves * S - 1) / (kWaves * S);
+  uint8_t* ring = smem + wave * (D * kSlot);
+  const int frag0 = r * 128 + ((g ^ (r >> 1)) & 7) * 16, frag1 = r * 128 + (((g + 4) ^ (r >> 1)) & 7) * 16;
+
+  auto step_at = [&](uint32_t row, int s) __attribute__((always_inline)) {
+    return (int)(s < nk ? row + (uint32_t)s * 128u : kOOB);
+  };
+  // MXFP4: the scales of step s, blocks 0..3 and 4..7 (this lane uses byte g of
+  // each dword). Bytes past the row's end are left out: they are another
+  // row's and might be NaN.
+  auto load_scales = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, int s) __attribute__((always_inline)) {
+    const uint32_t so = s < nk ? row + (uint32_t)s * 8u : kOOB;
+    if (ALIGNED) {
+      u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, soff, (int)so, 0));
+      if (s * 8 + 4 >= (int)sstride) v.y = 0;  // (K % 256 = 128)
+      return v;
+    }
+    const uint32_t b = (uint32_t)s * 8u + (uint32_t)g;
+    const uint32_t x = __builtin_amdgcn_raw_buffer_load_b8(rs, b < sstride ? soff + g : kOOB, (int)so, 0);
+    const uint32_t y = __builtin_amdgcn_raw_buffer_load_b8(rs, b + 4u < sstride ? soff + 4u + g : kOOB, (int)so, 0);
+    return u32x2{x << (8 * g), y << (8 * g)};
+  };
 
   for (int m0 = lo; m0 < hi; m0 += 16 * MT) {
     const int mrows = min(hi - m0, 16 * MT);
@@ -91,121 +146,131 @@ __global__ __launch_bounds__(kThreads) void gemm_few_rows_kernel(Args p) {
         (void*)(p.A + (int64_t)m0 * rowbytes), 0, (int)((uint32_t)mrows * rowbytes), kRsrcFlags);
     const __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(p.SA + (int64_t)m0 * sstride), 0, (int)((uint32_t)mrows * sstride), kRsrcFlags);
-
-    // Two dwords of MXFP4 scales of a row at step s; bytes past the row's end
-    // (they are another row's) do not matter, their codes being zeros, unless
-    // they are NaN: those are left out.
-    auto scales4 = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, int s, bool in) __attribute__((always_inline)) {
-      const uint32_t off = row + (uint32_t)s * 8u;
-      if (ALIGNED) {
-        // (a row's last step may hold one dword of it: K % 256 = 128)
-        const uint32_t x = __builtin_amdgcn_raw_buffer_load_b32(rs, in ? off : kOOB, 0, 0);
-        const uint32_t y = __builtin_amdgcn_raw_buffer_load_b32(rs, in && s * 8 + 4 < (int)sstride ? off + 4u : kOOB, 0, 0);
-        return u32x2{x, y};
-      }
-      // Bytes g and 4 + g, all that this lane uses.
-      const uint32_t x = __builtin_amdgcn_raw_buffer_load_b8(rs, in && s * 8 + g < (int)sstride ? off + g : kOOB, 0, 0);
-      const uint32_t y = __builtin_amdgcn_raw_buffer_load_b8(rs, in && s * 8 + 4 + g < (int)sstride ? off + 4u + g : kOOB, 0, 0);
-      return u32x2{x << (8 * g), y << (8 * g)};
-    };
-    auto load = [&](Step<MT, NT>& q, int i) __attribute__((always_inline)) {
-      const int s = i * kWaves + wave;
-      const bool in = s < nk;
-      const uint32_t k0 = (uint32_t)s * 128u + 16u * g, k1 = k0 + 64u;
-#pragma unroll
-      for (int t = 0; t < NT; t++) {
-        const uint32_t row = (uint32_t)(16 * t + r) * rowbytes;
-        q.b[t][0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rB, k0 < rowbytes ? row + k0 : kOOB, 0, 0));
-        q.b[t][1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rB, k1 < rowbytes ? row + k1 : kOOB, 0, 0));
-        if (!FP8) q.sb[t] = scales4(rSB, (uint32_t)(16 * t + r) * sstride, s, in);
-      }
-      if (FP8) q.sb[0].x = __builtin_amdgcn_raw_buffer_load_b32(rSB, in ? (uint32_t)s * 4u : kOOB, 0, 0);
-#pragma unroll
-      for (int t = 0; t < MT; t++) {
-        const uint32_t row = (uint32_t)(16 * t + r) * rowbytes;
-        q.a[t][0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, k0 < rowbytes ? row + k0 : kOOB, 0, 0));
-        q.a[t][1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, k1 < rowbytes ? row + k1 : kOOB, 0, 0));
-        const uint32_t srow = (uint32_t)(16 * t + r) * sstride;
-        if (FP8)
-          q.sa[t].x = __builtin_amdgcn_raw_buffer_load_b32(rSA, in ? srow + (uint32_t)s * 4u : kOOB, 0, 0);
-        else
-          q.sa[t] = scales4(rSA, srow, s, in);
-      }
-    };
-
-    f32x4 acc[MT][NT];
+    f32x4 acc[MT][T];
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
-      for (int j = 0; j < NT; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-    auto compute = [&](const Step<MT, NT>& q) __attribute__((always_inline)) {
-      if constexpr (FP8) {
-        const float sb = __builtin_bit_cast(float, q.sb[0].x);
+      for (int j = 0; j < T; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    for (int c = 0; c < chunks; c++) {
+      const int s0 = (c * kWaves + wave) * S;
+      // The ring's first weights, then A of all S steps, then (FP8) the
+      // weights' scales: lane l's is step s0 + l's.
+      u32x2 wsc[D];  // MXFP4: the ring's scales
+      auto load = [&](int k) __attribute__((always_inline)) {
+        const int t = k / S, s = s0 + k % S;
+        const int so = step_at((uint32_t)(16 * t) * rowbytes, s);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(ring + (k % D) * kSlot + h * 1024), 16,
+                                                   FP8 || s < nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
+        if (!FP8) wsc[k % D] = load_scales(rSB, (uint32_t)(16 * t) * sstride, s);
+      };
+#pragma unroll
+      for (int k = 0; k < D - 1; k++)
+        if (k < T * S) load(k);
+      i32x8 a[MT][S];
+      float sa[MT][S];
+      u32x2 sc[MT][S];
+#pragma unroll
+      for (int s = 0; s < S; s++)
 #pragma unroll
         for (int i = 0; i < MT; i++) {
-          const float f = __builtin_bit_cast(float, q.sa[i].x) * sb;
-          const i32x8 av = {q.a[i][0].x, q.a[i][0].y, q.a[i][0].z, q.a[i][0].w,
-                            q.a[i][1].x, q.a[i][1].y, q.a[i][1].z, q.a[i][1].w};
+          const int so = step_at((uint32_t)(16 * i) * rowbytes, s0 + s);
+          const bool full = FP8 || s0 + s < nk - 1;
+          const i32x4 x = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[0] : va_last[0], so, 0));
+          const i32x4 y = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[1] : va_last[1], so, 0));
+          a[i][s] = i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          if (FP8)
+            sa[i][s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                rSA, soff, (int)(s0 + s < nk ? (uint32_t)(16 * i) * sstride + (uint32_t)(s0 + s) * 4u : kOOB), 0));
+          else
+            sc[i][s] = load_scales(rSA, (uint32_t)(16 * i) * sstride, s0 + s);
+        }
+      float sb[T];
+      if (FP8) {
 #pragma unroll
-          for (int j = 0; j < NT; j++) {
-            const i32x8 bv = {q.b[j][0].x, q.b[j][0].y, q.b[j][0].z, q.b[j][0].w,
-                              q.b[j][1].x, q.b[j][1].y, q.b[j][1].z, q.b[j][1].w};
+        for (int t = 0; t < T; t++) {
+          const uint32_t nb = (uint32_t)((n0 + 16 * t) / 128 - nb0);  // (a tile past N: out of range)
+          sb[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+              rSB, s0 + lane < nk ? (uint32_t)lane * 4u : kOOB, (int)(nb * sstride + (uint32_t)s0 * 4u), 0));
+        }
+      }
+      // Step k + 1's fragments are read before step k's MFMAs. Loads end in
+      // order: step k + 1's have arrived when only the later steps' are out
+      // (the first time, A's too, which came last).
+      constexpr int kLoads = FP8 ? 2 : ALIGNED ? 3 : 4;  // of a step
+      auto arrived = [&](auto n) __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"i"(decltype(n)::value) : "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto read = [&](int k) __attribute__((always_inline)) {
+        const i32x4 x = *(const i32x4*)(ring + (k % D) * kSlot + frag0), y = *(const i32x4*)(ring + (k % D) * kSlot + frag1);
+        return i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      };
+      arrived(std::integral_constant<int, 0>{});
+      i32x8 next = read(0);
+      unroll<T * S>([&](auto kk) __attribute__((always_inline)) {
+        constexpr int k = decltype(kk)::value, t = k / S, s = k % S;
+        const i32x8 bv = next;
+        if (k + D - 1 < T * S) load(k + D - 1);
+        if constexpr (k + 1 < T * S) {
+          // Steps loaded behind k + 1 (the first D - 1 have all arrived).
+          constexpr int last = k + D - 1 < T * S ? k + D - 1 : T * S - 1;
+          constexpr int behind = last - (k + 1);
+          if constexpr (k + 1 >= D - 1) arrived(std::integral_constant<int, behind * kLoads>{});
+          next = read(k + 1);
+        }
+        const u32x2 wscale = wsc[k % D];
+        if constexpr (FP8) {
+          const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb[t]), s));
+#pragma unroll
+          for (int i = 0; i < MT; i++) {
+            const float f = sa[i][s] * w;
             f32x4 P = f32x4{0, 0, 0, 0};
             if (EXACT) {
 #pragma unroll
               for (int h = 0; h < 4; h++)
                 P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
-                                                            expand8(av[2 * h], av[2 * h + 1]), P, 0, 0, 0);
+                                                            expand8(a[i][s][2 * h], a[i][s][2 * h + 1]), P, 0, 0, 0);
             } else {
-              P = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, P, 0, 0, 0, 127, 0, 127);
+              P = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, a[i][s], P, 0, 0, 0, 127, 0, 127);
             }
 #pragma unroll
-            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(P[e], f, acc[i][j][e]);
+            for (int e = 0; e < 4; e++) acc[i][t][e] = __builtin_fmaf(P[e], f, acc[i][t][e]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const i32x8 bh = {bv[4 * h], bv[4 * h + 1], bv[4 * h + 2], bv[4 * h + 3], 0, 0, 0, 0};
+            const int wb = (int)((wscale[h] >> (8 * g)) & 0xFFu);
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+              const i32x8 av = {a[i][s][4 * h], a[i][s][4 * h + 1], a[i][s][4 * h + 2], a[i][s][4 * h + 3], 0, 0, 0, 0};
+              const int wa = (int)((sc[i][s][h] >> (8 * g)) & 0xFFu);
+              acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bh, av, acc[i][t], 4, 4, 0, wb, 0, wa);
+            }
           }
         }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int i = 0; i < MT; i++) {
-            const i32x8 av = {q.a[i][h].x, q.a[i][h].y, q.a[i][h].z, q.a[i][h].w, 0, 0, 0, 0};
-            const int sa = (int)((q.sa[i][h] >> (8 * g)) & 0xFFu);
-#pragma unroll
-            for (int j = 0; j < NT; j++) {
-              const i32x8 bv = {q.b[j][h].x, q.b[j][h].y, q.b[j][h].z, q.b[j][h].w, 0, 0, 0, 0};
-              const int sb = (int)((q.sb[j][h] >> (8 * g)) & 0xFFu);
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[i][j], 4, 4, 0, sb, 0, sa);
-            }
-          }
-      }
-    };
-
-    Step<MT, NT> ring[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH - 1; d++) load(ring[d], d);
-    for (int i = 0; i < steps; i += DEPTH) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; d++) {
-        if (i + d >= steps) break;
-        load(ring[(d + DEPTH - 1) % DEPTH], i + d + DEPTH - 1);
-        compute(ring[d]);
-      }
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
 
     // The waves' sums, added in their order. acc[i][j][e] of lane (r, g) is row
     // 16 i + r, column 16 j + 4 g + e.
-    if (m0 != lo) __syncthreads();  // (the last pass's sums have been read)
+    __syncthreads();  // (every ring has been read)
 #pragma unroll
     for (int i = 0; i < MT; i++)
 #pragma unroll
-      for (int j = 0; j < NT; j++)
+      for (int j = 0; j < T; j++)
 #pragma unroll
         for (int e = 0; e < 4; e++) part[wave][i][j][e][lane] = acc[i][j][e];
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < (MT * NT + kWaves - 1) / kWaves; u++) {
-      const int ij = u * kWaves + wave, i = ij / NT, j = ij % NT;
-      if (ij >= MT * NT) break;
+    for (int u = 0; u < (MT * T + kWaves - 1) / kWaves; u++) {
+      const int ij = u * kWaves + wave, i = ij / T, j = ij % T;
+      if (ij >= MT * T) break;
       f32x4 v;
 #pragma unroll
       for (int e = 0; e < 4; e++) {
@@ -235,17 +300,34 @@ __global__ __launch_bounds__(kThreads) void gemm_few_rows_kernel(Args p) {
   }
 }
 
-template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int MT, int NT, int DEPTH>
+template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int MT, int S, int T, int D>
 hipError_t launch(const Args& p, int64_t groups, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N + 16 * NT - 1) / (16 * NT)), (unsigned)groups);
-  return launch_kernel(&gemm_few_rows_kernel<FP8, EXACT, ALIGNED, OUT, MT, NT, DEPTH>, grid, kThreads, 0, s, p);
+  const dim3 grid((unsigned)((p.N + 16 * T - 1) / (16 * T)), (unsigned)groups);
+  return launch_kernel(&gemm_few_rows_kernel<FP8, EXACT, ALIGNED, OUT, W, MT, S, T, D>, grid, 64 * W, 0, s, p);
 }
 
+// per: rows of A per group, groups that have rows taken as min(groups, M).
+// Times in us at 16 rows, FP8, N x K (by expert: experts used x N x K).
 template <bool FP8, bool EXACT, bool ALIGNED, int OUT>
 hipError_t dispatch(const Args& p, int64_t groups, int64_t per, hipStream_t s) {
-  if (per <= 16) return launch<FP8, EXACT, ALIGNED, OUT, 1, 4, 3>(p, groups, s);
-  if (per <= 32) return launch<FP8, EXACT, ALIGNED, OUT, 2, 4, 2>(p, groups, s);
-  return launch<FP8, EXACT, ALIGNED, OUT, 4, 4, 2>(p, groups, s);
+  if (per > 32) return launch<FP8, EXACT, ALIGNED, OUT, 4, 4, 4, 2, 8>(p, groups, s);
+  if (per > 16) return launch<FP8, EXACT, ALIGNED, OUT, 4, 2, 4, 2, 8>(p, groups, s);
+  if constexpr (FP8) {
+    const int64_t tiles = (p.N + 15) / 16 * (p.offsets && p.M < groups ? p.M : groups);
+    const int nk = p.K / 128;
+    // Long rows, many of them: one workgroup of 8 waves a CU and 7 tiles
+    // share A (28672 x 8192: 38.2, T = 4 41.3, T = 2 53.5).
+    if (nk >= 48 && p.N >= 7 * 16 * 32 && tiles >= 7 * 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 1, 8, 7, 8>(p, groups, s);
+    // Dense, enough tiles for every CU (14336 x 4096: 14.3, T = 2 15.1, T = 1
+    // 20.1). By expert, fewer tiles spread better (8 x 2048 x 4096: T = 2
+    // 12.2, T = 4 16.3).
+    if (!p.offsets && nk > 16 && tiles >= 640) return launch<FP8, EXACT, ALIGNED, OUT, 4, 1, 8, 4, 9>(p, groups, s);
+    if (nk > 16 && tiles >= 512) return launch<FP8, EXACT, ALIGNED, OUT, 4, 1, 8, 2, 8>(p, groups, s);
+  }
+  // Few tiles or short rows (4096 x 4096: 7.4, T = 2 7.9; 4096 x 14336: 15.6 and
+  // 21.7; 8192 x 1024: 5.2 and 6.0), and MXFP4, whose rows are half as long
+  // (32 x 2048 x 2048: 14.8, T = 2 20.9, S = 8 30.6).
+  return launch<FP8, EXACT, ALIGNED, OUT, 4, 1, 4, 1, 5>(p, groups, s);
 }
 
 template <bool ALIGNED>
@@ -259,7 +341,7 @@ hipError_t mxfp4(const Args& p, int64_t groups, int64_t per, bool f32, hipStream
 // fp32 results: accumulation chains of at most 48 matrix instructions or scale
 // blocks, of 128 K, in a wave.
 bool gemm_few_rows_fits(int64_t K, int out_dtype) {
-  return out_dtype != kOutF32 || K <= (int64_t)48 * 128 * kWaves;
+  return out_dtype != kOutF32 || K <= (int64_t)48 * 128 * 4;
 }
 
 hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
