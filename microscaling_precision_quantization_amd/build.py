@@ -26,10 +26,11 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-ffp-contract=
           "-Wall", "-Wno-unused-function", "-I" + os.path.join(ROOT, "include")]
 
 
-# Per-source flags. gemm_mbs.hip, gemm_few_rows.hip: the MFMA partial sums feed vector-ALU
+# Per-source flags. gemm_mbs.hip, gemm_block.hip, gemm_few_rows.hip: the MFMA partial sums feed vector-ALU
 # arithmetic, so select the MFMA forms that write VGPRs (the default puts them
 # in AGPRs and adds one v_accvgpr_read per element).
 EXTRA = {"gemm_mbs.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+         "gemm_block.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
          "gemm_few_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 

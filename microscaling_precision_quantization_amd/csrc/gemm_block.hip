@@ -14,11 +14,12 @@
 // value, and those return the rounded exact sum.
 // MXFP4: the MFMA applies both E8M0 scales and accumulates.
 //
-// Operands go HBM -> LDS directly (buffer_load ... lds), double-buffered over
-// K; the buffer view of a tile ends with the group's rows, so rows past the
-// end load as zeros. LDS rows hold a K step (128 or 64 bytes); the 16-byte
-// chunk c of row r sits in slot c ^ swz(r), so that the 16 lanes that read one
-// column of chunks hit distinct banks.
+// Operands and A's (MXFP4: both) scales go HBM -> LDS directly (buffer_load ...
+// lds) into a ring of NS stages, a K step each, NS - 1 of them in flight: with few tiles the
+// loads' latency is what a step takes. The buffer view of a tile ends with
+// the group's rows, so rows past the end load as zeros. LDS rows hold a K step
+// (128 or 64 bytes); the 16-byte chunk c of row r sits in slot c ^ swz(r), so that
+// the 16 lanes that read one column of chunks hit distinct banks.
 //
 // B goes first into the MFMA: lane r + 16 g then holds C[row r][columns 4 g ..
 // 4 g + 3] of a tile, one row (one s_A) and a run of columns to store.
@@ -43,10 +44,13 @@ constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
 constexpr uint32_t kOOB = 0x80000000u;        // an offset past every buffer's range
 constexpr int kSegSteps = 48;                 // K steps per accumulation chain (fp32 results)
 
-// Tile geometry: waves of 16 TMW x 16 TNW, WM x WN of them.
-template <int FMT, int TMW_, int TNW_, int WM_, int WN_>
+// Tile geometry: waves of 16 TMW x 16 TNW, WM x WN of them; NS stages. ALIGNED: a
+// row's MXFP4 scales start on dwords (K % 128 = 0), so that a step's four are
+// one load; otherwise they are four loads of a byte, which LDS holds as a dword.
+template <int FMT, int TMW_, int TNW_, int WM_, int WN_, int NS_, bool ALIGNED_ = true>
 struct Geo {
-  static constexpr int TMW = TMW_, TNW = TNW_, WM = WM_, WN = WN_;
+  static constexpr int TMW = TMW_, TNW = TNW_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr bool kAligned = ALIGNED_;
   static constexpr int BM = 16 * TMW * WM, BN = 16 * TNW * WN;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr bool kFp8 = FMT == kFP8B128;
@@ -54,8 +58,20 @@ struct Geo {
   static constexpr int kCpr = kRow / 16;        // chunks per row
   static constexpr int kRpb = 64 / kCpr;        // rows per 1 KB load of a wave
   static constexpr int kOffB = BM * kRow;
-  static constexpr int kOffS = kOffB + BN * kRow;  // FP8: s_A [BM]; MXFP4: 4 E8M0 per row, A then B
-  static constexpr int kStage = kOffS + (kFp8 ? BM * 4 : (BM + BN) * 4);
+  // Scales, a dword a row, loaded 64 rows at a time: FP8 s_A of A's rows; MXFP4
+  // the step's four of A's and then of B's rows, or (not ALIGNED) that four
+  // times, a byte of each.
+  static constexpr int kOffS = kOffB + BN * kRow;
+  static constexpr int kScaleA = (BM + 63) / 64, kScaleGroups = kFp8 ? kScaleA : kScaleA + (BN + 63) / 64;
+  static constexpr int kScaleLoads = kScaleGroups * (kAligned ? 1 : 4);
+  static constexpr int kCodeLoads = (BM + BN) / kRpb;
+  // Loads of a wave and step: every wave the same number, so that a count of
+  // outstanding loads means the same steps in all (the rest go nowhere: out of
+  // range, into LDS that nobody reads).
+  static constexpr int kLoads = (kCodeLoads + kScaleLoads + kWaves - 1) / kWaves;
+  static constexpr int kStage = kOffS + kScaleLoads * 256;
+  static constexpr int kDummy = NS * kStage, kSmem = kDummy + 1024;
+  static_assert(kSmem <= 160 * 1024 && (NS - 1) * kLoads < 64, "tile");
 };
 
 template <bool FP8>
@@ -84,7 +100,7 @@ struct Args {
 template <int FMT, bool EXACT, int OUT, class G>
 __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
   constexpr bool FP8 = G::kFp8;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * G::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[G::kSmem];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / G::WN, wn = wave % G::WN;
   const int r = lane & 15, g = lane >> 4;
@@ -111,56 +127,39 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
   const int nb = min(n0 + wn * 16 * G::TNW, p.N - 1) / 128;
   const float* sb_row = (const float*)p.SB + ((int64_t)t.group * ((p.N + 127) / 128) + nb) * nk;
 
-  // Codes of step s (and s_A): 1 KB per instruction, kRpb rows.
-  auto issue = [&](int s, uint8_t* stage) {
-    constexpr int kA = G::BM / G::kRpb, kAll = (G::BM + G::BN) / G::kRpb;
+  // Loads of step s into its stage: codes, 1 KB (kRpb rows) each, then scales,
+  // 64 rows each. Steps past the last load nothing, but are counted.
+  auto issue = [&](int s, uint8_t* stage) __attribute__((always_inline)) {
+    constexpr int kA = G::BM / G::kRpb;
+    const bool in = s < nk;
 #pragma unroll
-    for (int i = 0; i < (kAll + G::kWaves - 1) / G::kWaves; i++) {
+    for (int i = 0; i < G::kLoads; i++) {
       const int b = wave + i * G::kWaves;
-      if (kAll % G::kWaves != 0 && b >= kAll) break;
-      const bool isA = b < kA;
-      const int row = (isA ? b : b - kA) * G::kRpb + lane / G::kCpr;
-      const uint32_t kb = (uint32_t)s * G::kRow + (uint32_t)((lane % G::kCpr) ^ swz<FP8>(row)) * 16u;
-      uint32_t off = (uint32_t)row * rowbytes + kb;
-      if (!FP8) off = kb < rowbytes ? off : kOOB;  // (FP8: K is a multiple of 128)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rA : rB, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
-    }
-    if (FP8 && wave * 64 < G::BM)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rSA, (lds_ptr_t)(stage + G::kOffS + wave * 256), 4,
-                                               (uint32_t)(wave * 64 + lane) * sstride, 4 * s, 0, 0);
-  };
-  // MXFP4: the 4 scales of step s of one row, through a register (a row's
-  // scales are not aligned to 4 when K % 128 != 0; blocks past K: any scale,
-  // their codes are zero, but not a neighbour's NaN).
-  constexpr int kScaleRows = FP8 ? 1 : (G::BM + G::BN + G::kThreads - 1) / G::kThreads;
-  uint32_t sreg[kScaleRows];
-  auto load_scales = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < kScaleRows; i++) {
-      const int q = tid + i * G::kThreads;
-      const bool isA = q < G::BM;
-      const uint32_t off = (uint32_t)(isA ? q : q - G::BM) * sstride + (uint32_t)(4 * s);
-      if (kblocks % 4 == 0) {
-        const uint32_t a = __builtin_amdgcn_raw_buffer_load_b32(rSA, isA ? off : kOOB, 0, 0);
-        const uint32_t b = __builtin_amdgcn_raw_buffer_load_b32(rSB, isA ? kOOB : off, 0, 0);
-        sreg[i] = a | b;
+      if ((i + 1) * G::kWaves <= G::kCodeLoads || b < G::kCodeLoads) {
+        const bool isA = b < kA;
+        const int row = (isA ? b : b - kA) * G::kRpb + lane / G::kCpr;
+        const uint32_t kb = (uint32_t)s * G::kRow + (uint32_t)((lane % G::kCpr) ^ swz<FP8>(row)) * 16u;
+        const uint32_t off = kb < rowbytes ? (uint32_t)row * rowbytes + kb : kOOB;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rA : rB, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
+        continue;
+      }
+      const int q = b - G::kCodeLoads;  // scale load
+      const bool real = in && q < G::kScaleLoads;
+      uint8_t* dst = real ? stage + G::kOffS + q * 256 : smem + G::kDummy;
+      if (FP8) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rSA, (lds_ptr_t)dst, 4, (uint32_t)(q * 64 + lane) * sstride,
+                                                 real ? 4 * s : (int)kOOB, 0, 0);
       } else {
-        sreg[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const bool in = 4 * s + j < kblocks;
-          const uint32_t a = __builtin_amdgcn_raw_buffer_load_b8(rSA, isA && in ? off + j : kOOB, 0, 0);
-          const uint32_t b = __builtin_amdgcn_raw_buffer_load_b8(rSB, !isA && in ? off + j : kOOB, 0, 0);
-          sreg[i] |= (a | b) << (8 * j);
-        }
+        const int grp = q % G::kScaleGroups, j = q / G::kScaleGroups;  // j: the step's block (not ALIGNED)
+        const bool isA = grp < G::kScaleA;
+        const uint32_t off = (uint32_t)((isA ? grp : grp - G::kScaleA) * 64 + lane) * sstride;
+        const uint32_t so = real && 4 * s + j < kblocks ? (uint32_t)(4 * s + j) : kOOB;
+        if (G::kAligned)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rSA : rSB, (lds_ptr_t)dst, 4, off, (int)so, 0, 0);
+        else
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rSA : rSB, (lds_ptr_t)dst, 1, off, (int)so, 0, 0);
       }
     }
-  };
-  auto store_scales = [&](uint8_t* stage) {
-#pragma unroll
-    for (int i = 0; i < kScaleRows; i++)
-      if (tid + i * G::kThreads < G::BM + G::BN)
-        *(uint32_t*)(stage + G::kOffS + (tid + i * G::kThreads) * 4) = sreg[i];
   };
 
   f32x4 acc[G::TMW][G::TNW], tot[OUT == kOutF32 ? G::TMW : 1][OUT == kOutF32 ? G::TNW : 1];
@@ -172,22 +171,20 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
       if (OUT == kOutF32) tot[i][j] = f32x4{0, 0, 0, 0};
     }
 
-  float sb_next = FP8 ? sb_row[0] : 0.0f;
-  issue(0, smem);
-  if (!FP8) {
-    load_scales(0);
-    store_scales(smem);
-  }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  // FP8: s_B of this wave's columns, 64 steps at a time, lane l's step s0 + l.
+  float sbs = 0.0f;
+#pragma unroll
+  for (int d = 0; d < G::NS - 1; d++) issue(d, smem + d * G::kStage);
+  int at = 0;  // step s's stage
   for (int s = 0; s < nk; s++) {
-    const uint8_t* cur = smem + (s & 1) * G::kStage;
-    uint8_t* nxt = smem + ((s + 1) & 1) * G::kStage;
-    const float sb = sb_next;
-    if (s + 1 < nk) {
-      issue(s + 1, nxt);
-      if (!FP8) load_scales(s + 1);
-      if (FP8) sb_next = sb_row[s + 1];
-    }
+    if (FP8 && s % 64 == 0) sbs = s + lane < nk ? sb_row[s + lane] : 0.0f;
+    // Step s has arrived (the later steps' loads may still be out), and every
+    // wave is done with step s - 1, whose stage takes step s + NS - 1.
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((G::NS - 2) * G::kLoads) : "memory");
+    const uint8_t* cur = smem + at * G::kStage;
+    issue(s + G::NS - 1, smem + (at == 0 ? G::NS - 1 : at - 1) * G::kStage);
+    at = at == G::NS - 1 ? 0 : at + 1;
+    const float sb = FP8 ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sbs), s & 63)) : 0.0f;
     if constexpr (FP8) {
       // A lane's 32 bytes of the step: chunks g and g + 4 of its row (any
       // order of K is right, if A's and B's are the same).
@@ -244,25 +241,26 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
         const i32x4 v = *(const i32x4*)(rows + row * 64 + ((g ^ swz<false>(row)) * 16));
         return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
       };
-      const uint8_t* sc = cur + G::kOffS;
+      auto scale = [&](int at) {  // at: row of A, or 64 kScaleA + row of B
+        return (int)cur[G::kOffS + (G::kAligned ? at * 4 + g : (g * (64 * G::kScaleGroups) + at) * 4)];
+      };
       i32x8 bf[G::TNW];
       int sbb[G::TNW];
 #pragma unroll
       for (int j = 0; j < G::TNW; j++) {
         const int row = wn * 16 * G::TNW + j * 16 + r;
         bf[j] = frag(cur + G::kOffB, row);
-        sbb[j] = sc[(G::BM + row) * 4 + g];
+        sbb[j] = scale(64 * G::kScaleA + row);
       }
 #pragma unroll
       for (int i = 0; i < G::TMW; i++) {
         const int row = wm * 16 * G::TMW + i * 16 + r;
         const i32x8 af = frag(cur, row);
-        const int sa = sc[row * 4 + g];
+        const int sa = scale(row);
 #pragma unroll
         for (int j = 0; j < G::TNW; j++)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, acc[i][j], 4, 4, 0, sbb[j], 0, sa);
       }
-      if (s + 1 < nk) store_scales(nxt);
     }
     if constexpr (OUT == kOutF32) {
       if ((s + 1) % kSegSteps == 0 && s + 1 < nk) {
@@ -275,9 +273,6 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
           }
       }
     }
-    // The next step's operands have arrived, and every wave is done with this
-    // step's buffer.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 
   const bool vec_ok = p.ldc % 4 == 0;
@@ -310,23 +305,45 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
   }
 }
 
+// Row tiles times column tiles (by expert: the most that M rows can need).
+int64_t tiles(const Args& p, int bm, int bn) {
+  const int64_t tm = p.offsets ? groups::max_row_tiles(p.M, p.groups, bm) : (p.M + bm - 1) / bm;
+  return tm * ((p.N + bn - 1) / bn);
+}
+
 template <int FMT, bool EXACT, int OUT, class G>
-hipError_t launch(const Args& a, int64_t groups, hipStream_t s) {
+hipError_t launch(const Args& a, hipStream_t s) {
   Args p = a;
   p.tiles_n = (int)((p.N + G::BN - 1) / G::BN);
-  const int64_t tm = p.offsets ? groups::max_row_tiles(p.M, groups, G::BM) : (p.M + G::BM - 1) / G::BM;
-  return launch_kernel(&gemm_block_kernel<FMT, EXACT, OUT, G>, dim3((unsigned)groups::grid_size(tm, p.tiles_n)),
+  const int64_t n = tiles(p, G::BM, G::BN) / p.tiles_n;
+  return launch_kernel(&gemm_block_kernel<FMT, EXACT, OUT, G>, dim3((unsigned)groups::grid_size(n, p.tiles_n)),
                        G::kThreads, 0, s, p);
+}
+
+// The tile: a CU takes its operands at 35-45 bytes a ns whatever the tile, so
+// while tiles are fewer than CUs, smaller ones, spread over more CUs, are faster;
+// with enough tiles larger ones are, which read less for their outputs. Times
+// in us of 32 / 64 / 128 square tiles, M x N x K:
+//   fp8, bf16 result: 128 x 4096 x 4096 11.8 / 14.8 / 29, 64 x 14336 x 4096 21.8 / 15.3,
+//   20 x 14336 x 4096 12.6 / 15.0, 777 x 8192 x 4096 - / 59 / 58, 1500 x 8192 x 4096
+//   - / 100 / 87; mxfp4, 800 rows over 8 x 2048 x 4096 - / 28 / 22, 3000 over
+//   4 x 600 x 992 - / 7.6 / 10.3.
+template <int FMT, bool EXACT, int OUT, bool ALIGNED>
+hipError_t by_tile(const Args& p, hipStream_t s) {
+  if (tiles(p, 128, 128) >= (FMT == kMXFP4 ? 200 : 700))
+    return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 4, ALIGNED>>(p, s);
+  if (p.M > 32 && tiles(p, 64, 64) >= 200) return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 2, 4, ALIGNED>>(p, s);
+  return launch<FMT, EXACT, OUT, Geo<FMT, 1, 1, 2, 2, 6, ALIGNED>>(p, s);
 }
 
 }  // namespace
 
-// Whether the kernel's 32-bit offsets hold: 256 rows of codes and of scales,
-// and (for the smallest tiles) the grid.
+// Whether the kernels' 32-bit offsets hold (256 rows of codes and of scales)
+// and the grid of 128 x 128 tiles (smaller ones are for few) its 2^32 threads.
 bool gemm_block_fits(int64_t M, int64_t N, int64_t K, int64_t groups) {
   if (K > ((int64_t)1 << 22)) return false;
   const int64_t tm = groups > 0 ? groups::max_row_tiles(M, groups, 128) : (M + 127) / 128;
-  return groups::grid_size(tm, (N + 127) / 128) < ((int64_t)1 << 31);
+  return groups::grid_size(tm, (N + 127) / 128) < ((int64_t)1 << 24);
 }
 
 hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
@@ -335,19 +352,26 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
   const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
   const bool f32 = out_dtype == kOutF32;
-  const int64_t per = offsets ? M / groups : M;
-  if (per <= 64 && gemm_few_rows_fits(K, out_dtype))
+  // Few rows of A: a stream of weights. (16 rows against 4096 x 4096 fp8 7.4 us,
+  // 32 x 32 tiles 10; 512 rows over 64 x 2048 x 4096 mxfp4 65, tiles 79; 1024
+  // rows 106 and 92.)
+  if ((offsets ? M <= 8 * groups : M <= 16) && gemm_few_rows_fits(N, K, out_dtype))
     return gemm_few_rows(fmt, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
+  // Tiles of 256 x 256 for at least two thirds of the CUs. (Times of 256 / 128
+  // square tiles: fp8 1500 x 8192 x 4096 53 / 87, 777 x 8192 x 4096 (128 tiles) 44 / 58,
+  // 300 x 8192 x 4096 (64) 43 / 30; mxfp4 2400 rows over 16 x 2048 x 2048 (200) 20 /
+  // 22, 800 over 8 x 2048 x 4096 (88) 28 / 22.)
+  const int64_t large = tiles(p, 256, 256);
   if (fmt == kMXFP4) {
-    if (per >= 192 && gemm_mxfp4_fits(0, N, K))
+    if (large >= 160 && gemm_mxfp4_fits(0, N, K))
       return gemm_mxfp4_grouped(M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
-    using G = Geo<kMXFP4, 4, 4, 2, 2>;
-    return f32 ? launch<kMXFP4, false, kOutF32, G>(p, groups, s) : launch<kMXFP4, false, kOutBF16, G>(p, groups, s);
+    if (K % 128 != 0)
+      return f32 ? by_tile<kMXFP4, false, kOutF32, false>(p, s) : by_tile<kMXFP4, false, kOutBF16, false>(p, s);
+    return f32 ? by_tile<kMXFP4, false, kOutF32, true>(p, s) : by_tile<kMXFP4, false, kOutBF16, true>(p, s);
   }
-  if (!f32 && per >= 192)
-    return gemm_fp8_large(M, N, K, a, sa, b, sb, offsets, groups, c, ldc, s);
-  using G = Geo<kFP8B128, 4, 4, 2, 2>;
-  return f32 ? launch<kFP8B128, true, kOutF32, G>(p, groups, s) : launch<kFP8B128, false, kOutBF16, G>(p, groups, s);
+  if (f32) return by_tile<kFP8B128, true, kOutF32, true>(p, s);
+  if (large >= 128) return gemm_fp8_large(M, N, K, a, sa, b, sb, offsets, groups, c, ldc, s);
+  return by_tile<kFP8B128, false, kOutBF16, true>(p, s);
 }
 
 }  // namespace mx

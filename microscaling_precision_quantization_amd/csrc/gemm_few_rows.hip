@@ -3,7 +3,7 @@
 // of B. (The mathematics and the choice between the FP8 and the bf16 MFMA are
 // gemm_block.hip's.)
 //
-// Bound by HBM: every weight byte is read once and meets 16 MT rows of A, so
+// Bound by HBM: every weight byte is read once and meets 16 rows of A, so
 // the kernel is a stream of weights from HBM through VGPRs to the matrix core.
 //  * A workgroup takes T tiles of 16 weight rows of one expert. K goes to its
 //    waves in chunks of W S steps of 128 bytes (128 K of FP8, 256 K of
@@ -20,7 +20,7 @@
 //    the tile; the same order of K in A.
 //  * Loads are range-checked buffer loads without a branch: rows past the
 //    group's or N, steps past K and 32-element blocks past K read as zeros.
-//  * A group with more than 16 MT rows takes further passes over the weights.
+//  * A group with more than 16 rows takes further passes over the weights.
 #include <type_traits>
 #include <utility>
 
@@ -39,7 +39,9 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
-constexpr uint32_t kOOB = 0x80000000u;        // an offset past every buffer's range
+// Lane and scalar offsets past every buffer's range (256 rows of at most 2^22
+// bytes); their sum is one too.
+constexpr uint32_t kOOB = 0x80000000u, kScalarOOB = 0x40000000u;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int kNonTemporal = 2;                // cache policy of a load: streamed
 
@@ -73,12 +75,12 @@ __device__ __forceinline__ void unroll(F&& f) {
 
 // ALIGNED: a row's MXFP4 scales start on dwords (K % 128 = 0).
 // W: waves.
-template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int MT, int S, int T, int D>
+template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int S, int T, int D>
 __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   constexpr int kWaves = W;
-  constexpr int kSlot = 2048, kRing = kWaves * D * kSlot, kSums = kWaves * MT * T * 4 * 64 * 4;
+  constexpr int kSlot = 2048, kRing = kWaves * D * kSlot, kSums = kWaves * T * 4 * 64 * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing > kSums ? kRing : kSums];
-  float(*part)[MT][T][4][64] = (float(*)[MT][T][4][64])smem;
+  float(*part)[T][4][64] = (float(*)[T][4][64])smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * (16 * T), group = blockIdx.y;
@@ -122,13 +124,13 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   const int frag0 = r * 128 + ((g ^ (r >> 1)) & 7) * 16, frag1 = r * 128 + (((g + 4) ^ (r >> 1)) & 7) * 16;
 
   auto step_at = [&](uint32_t row, int s) __attribute__((always_inline)) {
-    return (int)(s < nk ? row + (uint32_t)s * 128u : kOOB);
+    return (int)(s < nk ? row + (uint32_t)s * 128u : kScalarOOB);
   };
   // MXFP4: the scales of step s, blocks 0..3 and 4..7 (this lane uses byte g of
   // each dword). Bytes past the row's end are left out: they are another
   // row's and might be NaN.
   auto load_scales = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, int s) __attribute__((always_inline)) {
-    const uint32_t so = s < nk ? row + (uint32_t)s * 8u : kOOB;
+    const uint32_t so = s < nk ? row + (uint32_t)s * 8u : kScalarOOB;
     if (ALIGNED) {
       u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, soff, (int)so, 0));
       if (s * 8 + 4 >= (int)sstride) v.y = 0;  // (K % 256 = 128)
@@ -140,17 +142,16 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
     return u32x2{x << (8 * g), y << (8 * g)};
   };
 
-  for (int m0 = lo; m0 < hi; m0 += 16 * MT) {
-    const int mrows = min(hi - m0, 16 * MT);
+  for (int m0 = lo; m0 < hi; m0 += 16) {
+    if (m0 != lo) __syncthreads();  // (the last pass's sums, where the rings are, have been read)
+    const int mrows = min(hi - m0, 16);
     const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(p.A + (int64_t)m0 * rowbytes), 0, (int)((uint32_t)mrows * rowbytes), kRsrcFlags);
     const __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(p.SA + (int64_t)m0 * sstride), 0, (int)((uint32_t)mrows * sstride), kRsrcFlags);
-    f32x4 acc[MT][T];
+    f32x4 acc[T];
 #pragma unroll
-    for (int i = 0; i < MT; i++)
-#pragma unroll
-      for (int j = 0; j < T; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < T; j++) acc[j] = f32x4{0, 0, 0, 0};
 
     for (int c = 0; c < chunks; c++) {
       const int s0 = (c * kWaves + wave) * S;
@@ -169,24 +170,22 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
 #pragma unroll
       for (int k = 0; k < D - 1; k++)
         if (k < T * S) load(k);
-      i32x8 a[MT][S];
-      float sa[MT][S];
-      u32x2 sc[MT][S];
+      i32x8 a[S];
+      float sa[S];
+      u32x2 sc[S];
 #pragma unroll
-      for (int s = 0; s < S; s++)
-#pragma unroll
-        for (int i = 0; i < MT; i++) {
-          const int so = step_at((uint32_t)(16 * i) * rowbytes, s0 + s);
-          const bool full = FP8 || s0 + s < nk - 1;
-          const i32x4 x = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[0] : va_last[0], so, 0));
-          const i32x4 y = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[1] : va_last[1], so, 0));
-          a[i][s] = i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          if (FP8)
-            sa[i][s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                rSA, soff, (int)(s0 + s < nk ? (uint32_t)(16 * i) * sstride + (uint32_t)(s0 + s) * 4u : kOOB), 0));
-          else
-            sc[i][s] = load_scales(rSA, (uint32_t)(16 * i) * sstride, s0 + s);
-        }
+      for (int s = 0; s < S; s++) {
+        const int so = step_at(0, s0 + s);
+        const bool full = FP8 || s0 + s < nk - 1;
+        const i32x4 x = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[0] : va_last[0], so, 0));
+        const i32x4 y = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[1] : va_last[1], so, 0));
+        a[s] = i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        if (FP8)
+          sa[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+              rSA, soff, (int)(s0 + s < nk ? (uint32_t)(s0 + s) * 4u : kScalarOOB), 0));
+        else
+          sc[s] = load_scales(rSA, 0, s0 + s);
+      }
       float sb[T];
       if (FP8) {
 #pragma unroll
@@ -225,62 +224,54 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
         const u32x2 wscale = wsc[k % D];
         if constexpr (FP8) {
           const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb[t]), s));
+          const float f = sa[s] * w;
+          f32x4 P = f32x4{0, 0, 0, 0};
+          if (EXACT) {
 #pragma unroll
-          for (int i = 0; i < MT; i++) {
-            const float f = sa[i][s] * w;
-            f32x4 P = f32x4{0, 0, 0, 0};
-            if (EXACT) {
-#pragma unroll
-              for (int h = 0; h < 4; h++)
-                P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
-                                                            expand8(a[i][s][2 * h], a[i][s][2 * h + 1]), P, 0, 0, 0);
-            } else {
-              P = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, a[i][s], P, 0, 0, 0, 127, 0, 127);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; e++) acc[i][t][e] = __builtin_fmaf(P[e], f, acc[i][t][e]);
+            for (int h = 0; h < 4; h++)
+              P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
+                                                          expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
+          } else {
+            P = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, a[s], P, 0, 0, 0, 127, 0, 127);
           }
+#pragma unroll
+          for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; h++) {
             const i32x8 bh = {bv[4 * h], bv[4 * h + 1], bv[4 * h + 2], bv[4 * h + 3], 0, 0, 0, 0};
             const int wb = (int)((wscale[h] >> (8 * g)) & 0xFFu);
-#pragma unroll
-            for (int i = 0; i < MT; i++) {
-              const i32x8 av = {a[i][s][4 * h], a[i][s][4 * h + 1], a[i][s][4 * h + 2], a[i][s][4 * h + 3], 0, 0, 0, 0};
-              const int wa = (int)((sc[i][s][h] >> (8 * g)) & 0xFFu);
-              acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bh, av, acc[i][t], 4, 4, 0, wb, 0, wa);
-            }
+            const i32x8 av = {a[s][4 * h], a[s][4 * h + 1], a[s][4 * h + 2], a[s][4 * h + 3], 0, 0, 0, 0};
+            const int wa = (int)((sc[s][h] >> (8 * g)) & 0xFFu);
+            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bh, av, acc[t], 4, 4, 0, wb, 0, wa);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       });
     }
 
-    // The waves' sums, added in their order. acc[i][j][e] of lane (r, g) is row
-    // 16 i + r, column 16 j + 4 g + e.
+    // The waves' sums, added in their order. acc[j][e] of lane (r, g) is row r,
+    // column 16 j + 4 g + e.
     __syncthreads();  // (every ring has been read)
 #pragma unroll
-    for (int i = 0; i < MT; i++)
+    for (int j = 0; j < T; j++)
 #pragma unroll
-      for (int j = 0; j < T; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) part[wave][i][j][e][lane] = acc[i][j][e];
+      for (int e = 0; e < 4; e++) part[wave][j][e][lane] = acc[j][e];
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < (MT * T + kWaves - 1) / kWaves; u++) {
-      const int ij = u * kWaves + wave, i = ij / T, j = ij % T;
-      if (ij >= MT * T) break;
+    for (int u = 0; u < (T + kWaves - 1) / kWaves; u++) {
+      const int j = u * kWaves + wave;
+      if (j >= T) break;
       f32x4 v;
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        v[e] = part[0][i][j][e][lane];
+        v[e] = part[0][j][e][lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; w++) v[e] += part[w][i][j][e][lane];
+        for (int w = 1; w < kWaves; w++) v[e] += part[w][j][e][lane];
       }
-      const int row = 16 * i + r, col = n0 + 16 * j + 4 * g;
-      if (row >= mrows) continue;
-      const int64_t at = (int64_t)(m0 + row) * p.ldc + col;
+      const int col = n0 + 16 * j + 4 * g;
+      if (r >= mrows) continue;
+      const int64_t at = (int64_t)(m0 + r) * p.ldc + col;
       if (p.ldc % 4 == 0 && col + 4 <= p.N) {
         if (OUT == kOutF32)
           *(f32x4*)((float*)p.C + at) = v;
@@ -300,47 +291,46 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   }
 }
 
-template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int MT, int S, int T, int D>
+template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int S, int T, int D>
 hipError_t launch(const Args& p, int64_t groups, hipStream_t s) {
   const dim3 grid((unsigned)((p.N + 16 * T - 1) / (16 * T)), (unsigned)groups);
-  return launch_kernel(&gemm_few_rows_kernel<FP8, EXACT, ALIGNED, OUT, W, MT, S, T, D>, grid, 64 * W, 0, s, p);
+  return launch_kernel(&gemm_few_rows_kernel<FP8, EXACT, ALIGNED, OUT, W, S, T, D>, grid, 64 * W, 0, s, p);
 }
 
-// per: rows of A per group, groups that have rows taken as min(groups, M).
-// Times in us at 16 rows, FP8, N x K (by expert: experts used x N x K).
+// Experts that have rows are taken as min(groups, M). Times in us at 16 rows,
+// FP8, N x K (by expert: experts used x N x K).
 template <bool FP8, bool EXACT, bool ALIGNED, int OUT>
-hipError_t dispatch(const Args& p, int64_t groups, int64_t per, hipStream_t s) {
-  if (per > 32) return launch<FP8, EXACT, ALIGNED, OUT, 4, 4, 4, 2, 8>(p, groups, s);
-  if (per > 16) return launch<FP8, EXACT, ALIGNED, OUT, 4, 2, 4, 2, 8>(p, groups, s);
+hipError_t dispatch(const Args& p, int64_t groups, hipStream_t s) {
   if constexpr (FP8) {
     const int64_t tiles = (p.N + 15) / 16 * (p.offsets && p.M < groups ? p.M : groups);
     const int nk = p.K / 128;
     // Long rows, many of them: one workgroup of 8 waves a CU and 7 tiles
     // share A (28672 x 8192: 38.2, T = 4 41.3, T = 2 53.5).
-    if (nk >= 48 && p.N >= 7 * 16 * 32 && tiles >= 7 * 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 1, 8, 7, 8>(p, groups, s);
+    if (nk >= 48 && p.N >= 7 * 16 * 32 && tiles >= 7 * 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
     // Dense, enough tiles for every CU (14336 x 4096: 14.3, T = 2 15.1, T = 1
     // 20.1). By expert, fewer tiles spread better (8 x 2048 x 4096: T = 2
     // 12.2, T = 4 16.3).
-    if (!p.offsets && nk > 16 && tiles >= 640) return launch<FP8, EXACT, ALIGNED, OUT, 4, 1, 8, 4, 9>(p, groups, s);
-    if (nk > 16 && tiles >= 512) return launch<FP8, EXACT, ALIGNED, OUT, 4, 1, 8, 2, 8>(p, groups, s);
+    if (!p.offsets && nk > 16 && tiles >= 640) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 4, 9>(p, groups, s);
+    if (nk > 16 && tiles >= 512) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
   }
   // Few tiles or short rows (4096 x 4096: 7.4, T = 2 7.9; 4096 x 14336: 15.6 and
   // 21.7; 8192 x 1024: 5.2 and 6.0), and MXFP4, whose rows are half as long
   // (32 x 2048 x 2048: 14.8, T = 2 20.9, S = 8 30.6).
-  return launch<FP8, EXACT, ALIGNED, OUT, 4, 1, 4, 1, 5>(p, groups, s);
+  return launch<FP8, EXACT, ALIGNED, OUT, 4, 4, 1, 5>(p, groups, s);
 }
 
 template <bool ALIGNED>
-hipError_t mxfp4(const Args& p, int64_t groups, int64_t per, bool f32, hipStream_t s) {
-  if (f32) return dispatch<false, false, ALIGNED, kOutF32>(p, groups, per, s);
-  return dispatch<false, false, ALIGNED, kOutBF16>(p, groups, per, s);
+hipError_t mxfp4(const Args& p, int64_t groups, bool f32, hipStream_t s) {
+  if (f32) return dispatch<false, false, ALIGNED, kOutF32>(p, groups, s);
+  return dispatch<false, false, ALIGNED, kOutBF16>(p, groups, s);
 }
 
 }  // namespace
 
 // fp32 results: accumulation chains of at most 48 matrix instructions or scale
 // blocks, of 128 K, in a wave.
-bool gemm_few_rows_fits(int64_t K, int out_dtype) {
+bool gemm_few_rows_fits(int64_t N, int64_t K, int out_dtype) {
+  if (N > ((int64_t)1 << 27)) return false;  // (16 columns a workgroup: the grid)
   return out_dtype != kOutF32 || K <= (int64_t)48 * 128 * 4;
 }
 
@@ -349,11 +339,10 @@ hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a
                          int out_dtype, void* c, int64_t ldc, hipStream_t s) {
   const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
                ldc, (int)M, (int)N, (int)K};
-  const int64_t per = offsets ? (M + groups - 1) / groups : M;
   const int64_t g = offsets ? groups : 1;
   const bool f32 = out_dtype == kOutF32;
-  if (fmt == kMXFP4) return K % 128 == 0 ? mxfp4<true>(p, g, per, f32, s) : mxfp4<false>(p, g, per, f32, s);
-  return f32 ? dispatch<true, true, true, kOutF32>(p, g, per, s) : dispatch<true, false, true, kOutBF16>(p, g, per, s);
+  if (fmt == kMXFP4) return K % 128 == 0 ? mxfp4<true>(p, g, f32, s) : mxfp4<false>(p, g, f32, s);
+  return f32 ? dispatch<true, true, true, kOutF32>(p, g, s) : dispatch<true, false, true, kOutBF16>(p, g, s);
 }
 
 }  // namespace mx
