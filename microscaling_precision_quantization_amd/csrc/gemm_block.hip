@@ -305,9 +305,13 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
   }
 }
 
-// Row tiles times column tiles (by expert: the most that M rows can need).
+// Experts that have rows, and rows each, as far as the host can know.
+int64_t used(const Args& p) { return !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M; }
+int64_t rows_each(const Args& p) { return p.M / used(p); }
+
+// Tiles to expect: an expert's last row tile half full.
 int64_t tiles(const Args& p, int bm, int bn) {
-  const int64_t tm = p.offsets ? groups::max_row_tiles(p.M, p.groups, bm) : (p.M + bm - 1) / bm;
+  const int64_t tm = p.offsets ? (p.M + used(p) * (bm / 2)) / bm : (p.M + bm - 1) / bm;
   return tm * ((p.N + bn - 1) / bn);
 }
 
@@ -315,7 +319,7 @@ template <int FMT, bool EXACT, int OUT, class G>
 hipError_t launch(const Args& a, hipStream_t s) {
   Args p = a;
   p.tiles_n = (int)((p.N + G::BN - 1) / G::BN);
-  const int64_t n = tiles(p, G::BM, G::BN) / p.tiles_n;
+  const int64_t n = p.offsets ? groups::max_row_tiles(p.M, p.groups, G::BM) : (p.M + G::BM - 1) / G::BM;
   return launch_kernel(&gemm_block_kernel<FMT, EXACT, OUT, G>, dim3((unsigned)groups::grid_size(n, p.tiles_n)),
                        G::kThreads, 0, s, p);
 }
@@ -324,15 +328,17 @@ hipError_t launch(const Args& a, hipStream_t s) {
 // while tiles are fewer than CUs, smaller ones, spread over more CUs, are faster;
 // with enough tiles larger ones are, which read less for their outputs. Times
 // in us of 32 / 64 / 128 square tiles, M x N x K:
-//   fp8, bf16 result: 128 x 4096 x 4096 11.8 / 14.8 / 29, 64 x 14336 x 4096 21.8 / 15.3,
-//   20 x 14336 x 4096 12.6 / 15.0, 777 x 8192 x 4096 - / 59 / 58, 1500 x 8192 x 4096
-//   - / 100 / 87; mxfp4, 800 rows over 8 x 2048 x 4096 - / 28 / 22, 3000 over
-//   4 x 600 x 992 - / 7.6 / 10.3.
+//   fp8, bf16 result: 17 x 28672 x 4096 34 / 27 / 31, 32 x 14336 x 4096 12.4 / 15.0 / 28,
+//   64 x 14336 x 4096 22 / 15 / 29, 128 x 4096 x 4096 11.8 / 14.8 / 29, 128 x 28672 x
+//   4096 - / 54 / 37, 256 x 14336 x 4096 - / 35 / 31, 1500 x 8192 x 4096 - / 100 / 87,
+//   800 rows over 8 x 2048 x 4096 - / 22 / 31;
+//   mxfp4: 800 rows over 8 x 2048 x 4096 - / 28 / 22, 1920 over 64 x 2048 x 4096 - / 108 / 80,
+//   3000 over 4 x 600 x 992 - / 7.6 / 10.3.
 template <int FMT, bool EXACT, int OUT, bool ALIGNED>
 hipError_t by_tile(const Args& p, hipStream_t s) {
-  if (tiles(p, 128, 128) >= (FMT == kMXFP4 ? 200 : 700))
+  if ((p.offsets || p.M > 48) && tiles(p, 128, 128) >= (FMT == kMXFP4 ? 150 : 200))
     return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 4, ALIGNED>>(p, s);
-  if (p.M > 32 && tiles(p, 64, 64) >= 200) return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 2, 4, ALIGNED>>(p, s);
+  if (tiles(p, 64, 64) >= (p.M > 32 ? 200 : 300)) return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 2, 4, ALIGNED>>(p, s);
   return launch<FMT, EXACT, OUT, Geo<FMT, 1, 1, 2, 2, 6, ALIGNED>>(p, s);
 }
 
@@ -357,20 +363,22 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
   // rows 106 and 92.)
   if ((offsets ? M <= 8 * groups : M <= 16) && gemm_few_rows_fits(N, K, out_dtype))
     return gemm_few_rows(fmt, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
-  // Tiles of 256 x 256 for at least two thirds of the CUs. (Times of 256 / 128
-  // square tiles: fp8 1500 x 8192 x 4096 53 / 87, 777 x 8192 x 4096 (128 tiles) 44 / 58,
-  // 300 x 8192 x 4096 (64) 43 / 30; mxfp4 2400 rows over 16 x 2048 x 2048 (200) 20 /
-  // 22, 800 over 8 x 2048 x 4096 (88) 28 / 22.)
-  const int64_t large = tiles(p, 256, 256);
+  // Tiles of 256 x 256, for almost half of the CUs or more, where most are more than half full.
+  // (Times of 256 / the best of the smaller tiles: fp8 1500 x 8192 x 4096 (192 tiles)
+  // 53 / 87, 777 x 8192 x 4096 (128) 44 / 58, 256 x 28672 x 4096 (112) 60 / 63, 300 x
+  // 8192 x 4096 (64) 43 / 30, 128 x 28672 x 4096 (112, half full) 54 / 37; mxfp4 2400 rows
+  // over 16 x 2048 x 2048 (139) 20 / 22, 800 over 8 x 2048 x 4096 (57) 28 / 22; fp8 1600
+  // rows over 16 x 2048 x 2048 25 / 35.)
+  const bool large = rows_each(p) > (offsets ? 64 : 128) && tiles(p, 256, 256) >= 110;
   if (fmt == kMXFP4) {
-    if (large >= 160 && gemm_mxfp4_fits(0, N, K))
+    if (large && gemm_mxfp4_fits(0, N, K))
       return gemm_mxfp4_grouped(M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
     if (K % 128 != 0)
       return f32 ? by_tile<kMXFP4, false, kOutF32, false>(p, s) : by_tile<kMXFP4, false, kOutBF16, false>(p, s);
     return f32 ? by_tile<kMXFP4, false, kOutF32, true>(p, s) : by_tile<kMXFP4, false, kOutBF16, true>(p, s);
   }
   if (f32) return by_tile<kFP8B128, true, kOutF32, true>(p, s);
-  if (large >= 128) return gemm_fp8_large(M, N, K, a, sa, b, sb, offsets, groups, c, ldc, s);
+  if (large) return gemm_fp8_large(M, N, K, a, sa, b, sb, offsets, groups, c, ldc, s);
   return by_tile<kFP8B128, false, kOutBF16, true>(p, s);
 }
 
