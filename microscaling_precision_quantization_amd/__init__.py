@@ -269,11 +269,11 @@ def _stream(torch, device, *tensors):
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"all tensors must be on {device}; got one on {t.device}")
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device.index)  # (1.8 us less than by a Stream object)
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check(status, what):
@@ -342,7 +342,7 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
         wsb = mx_quantize_workspace_bytes(f, rows, cols)
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
     if lay == MX_LAYOUT_ROWS:
-        _check(_on(dev, mx_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
+        _check(_on(dev, lib().mx_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
                    _ptr(scales), _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x)), "mx_quantize")
     else:
         _check(mx_quantize_layout(f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
@@ -454,7 +454,7 @@ def gemm(a, b, out_dtype=None, out=None, workspace=None):
                           _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0),
                           _ptr(workspace), wsb, stream, la, b.layout), "mx_gemm_ex")
         return c
-    _check(_on(dev, mx_gemm, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta, _ptr(b.codes),
+    _check(_on(dev, lib().mx_gemm, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta, _ptr(b.codes),
                _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0), _ptr(workspace), wsb,
                stream), "mx_gemm")
     return c
@@ -488,7 +488,7 @@ def gemm_grouped(a, b, offsets, out_dtype=None, out=None):
     elif out.dtype != out_dtype or out.dim() != 2 or tuple(out.shape) != (M, N) or out.stride(1) != 1:
         raise ValueError(f"out must be a [{M}][{N}] {out_dtype} tensor with unit column stride")
     stream = _stream(torch, dev, a.codes, a.scales, b.codes, b.scales, offsets, out)
-    _check(_on(dev, mx_gemm_grouped, a.fmt, b.fmt, b.block, MX_ROUND_RNE, G, M, N, K, _ptr(offsets),
+    _check(_on(dev, lib().mx_gemm_grouped, a.fmt, b.fmt, b.block, MX_ROUND_RNE, G, M, N, K, _ptr(offsets),
                _ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales),
                MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, _ptr(out), out.stride(0),
                stream), "mx_gemm_grouped")
@@ -510,32 +510,36 @@ def norm_quantize(x, weight, fmt, residual=None, gate=None, post_weight=None, al
         raise ValueError("norm_quantize gives mxfp4, mxfp8 or fp8_b128")
     if x.dim() != 2:
         raise ValueError("norm_quantize expects a 2-D bfloat16 tensor")
-    rows, cols = x.shape
+    rows, cols = shape = x.shape
+    bf16 = torch.bfloat16
     for t, name in ((x, "x"), (residual, "residual"), (out, "out")):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape != x.shape or t.stride(1) != 1):
+        if t is not None and (t.dtype != bf16 or t.shape != shape or t.stride(1) != 1):
             raise ValueError(f"{name} must be a [{rows}][{cols}] bfloat16 tensor with unit column stride")
     for t, name in ((weight, "weight"), (post_weight, "post_weight")):
-        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != (cols,) or not t.is_contiguous()):
+        if t is not None and (t.dtype != bf16 or t.dim() != 1 or t.numel() != cols or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous bfloat16 tensor of {cols} elements")
     gate_rows = 0
     if gate is not None:
         n = 1 if gate.dim() == 1 else gate.shape[0]
-        if gate.dtype != torch.bfloat16 or gate.dim() > 2 or gate.shape[-1] != cols or not gate.is_contiguous():
+        if gate.dtype != bf16 or gate.dim() > 2 or gate.shape[-1] != cols or not gate.is_contiguous():
             raise ValueError(f"gate must be a contiguous bfloat16 tensor of rows of {cols}")
         if n < 1 or rows % n != 0:
             raise ValueError(f"{rows} rows do not divide among {n} gates")
         gate_rows = rows // n
     dev = x.device
     if out is None and residual is not None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=bf16, device=dev)
     codes = torch.empty((rows, code_cols(f, cols)), dtype=torch.uint8, device=dev)
     scales = torch.empty(scale_shape(f, rows, cols), device=dev,
                          dtype=torch.float32 if f == MX_FMT_FP8_B128 else torch.uint8)
     lay = LAYOUTS[layout]
     stream = _stream(torch, dev, x, residual, gate, post_weight, weight, out)
-    ld = lambda t: 0 if t is None else t.stride(0) if rows > 1 else cols  # noqa: E731
-    _check(_on(dev, mx_norm_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), ld(x),
-               _ptr(residual), ld(residual), _ptr(gate), gate_rows, _ptr(post_weight), alpha,
-               _ptr(weight), eps, _ptr(out), ld(out), _ptr(codes), _ptr(scales), stream, lay),
+    # (The row stride of a single row says nothing.)
+    ldx = x.stride(0) if rows > 1 else cols
+    ldr = residual.stride(0) if residual is not None and rows > 1 else cols
+    ldh = out.stride(0) if out is not None and rows > 1 else cols
+    _check(_on(dev, lib().mx_norm_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), ldx,
+               _ptr(residual), ldr, _ptr(gate), gate_rows, _ptr(post_weight), alpha, _ptr(weight), eps,
+               _ptr(out), ldh, _ptr(codes), _ptr(scales), stream, lay),
            "mx_norm_quantize")
     return QTensor(f, rows, cols, codes, scales, None, lay), out

@@ -7,10 +7,10 @@
 // The quotient never reaches 464, where E4M3 would overflow: s is within
 // half an fp32 step of amax / 448, at worst 2^-8 of it among the subnormals.
 //
-// Deciding the code without a division per element: v = x' rcp(s') is within
-// 2^-21 of the quotient (x' and s' are scaled by 2^64 when s < 2^-60, so that
-// neither the reciprocal overflows nor v underflows), so the quotient lies
-// between v (1 - 2^-20) and v (1 + 2^-20). Where both convert to the same code,
+// Deciding the code without a division per element: x' rcp(s') is within 2^-21 of
+// the quotient (x' and s' are scaled by 2^64 when s < 2^-60, so that neither the
+// reciprocal overflows nor the product underflows), so the quotient lies between
+// x' times rcp(s') (1 - 2^-20) and x' times rcp(s') (1 + 2^-20). Where both convert to the same code,
 // that is the code. Otherwise one midpoint m of two neighbouring E4M3 values
 // lies between them, and the sign of |x'| - m s', exact in one fma (m has 5
 // bits), decides.
@@ -77,25 +77,29 @@ __global__ __launch_bounds__(kThreads) void quant_fp8_rows_kernel(const u32x4* _
   }
 }
 
-// 128 x 128 tiles: a workgroup of 16 waves takes 128 rows x 512 columns (4
-// tiles), a wave 8 of the rows, so that one load instruction reads 1 KB of one
-// row and the tile stays in registers between its amax and its codes. The
+// 128 x 128 tiles: a workgroup of 8 waves takes 128 rows x 256 columns (two
+// tiles; 28672 x 8192: 118 us = 6.0 TB/s, one tile 129, four 127), a load instruction two
+// rows of them, and the tile stays in registers between its amax and its codes. The
 // tiles' amax come from the waves' through LDS. Rows past the end belong to no
-// tile; a tile at the end is shorter.
-constexpr int kTileWaves = 16;
-__global__ __launch_bounds__(64 * kTileWaves) void quant_fp8_tiles_kernel(
+// tile; a tile at the end is shorter. Codes are not read again soon: non-temporal
+// stores (plain ones: 125 us).
+constexpr int W = 8;
+__global__ __launch_bounds__(64 * W) void quant_fp8_tiles_kernel(
     const u32x4* __restrict__ x, u32x2* __restrict__ codes, float* __restrict__ scales, int64_t rows,
     int64_t cpr) {
-  __shared__ uint32_t part[kTileWaves][4];
+  constexpr int kC = 4 * W, kTiles = W / 4;  // chunks of a row, tiles
+  constexpr int kR = 64 / kC;                // rows of a load
+  __shared__ uint32_t part[kTiles][W * kR];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t across = (cpr + 63) / 64, strip = blockIdx.x / across;  // strip: 128 rows
-  const int64_t c = (int64_t)(blockIdx.x % across) * 64 + lane;         // chunk of the row
-  const int64_t r0 = strip * 128 + wave * 8;
+  const int64_t across = (cpr + kC - 1) / kC, strip = blockIdx.x / across;  // strip: 128 rows
+  const int tile = lane % kC / 16;
+  const int64_t c = (int64_t)(blockIdx.x % across) * kC + lane % kC;         // chunk of the row
+  const int64_t r0 = strip * 128 + wave * (8 * kR) + lane / kC;
   const bool in = c < cpr;
   u32x4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; i++)
-    v[i] = in && r0 + i < rows ? __builtin_nontemporal_load(x + (r0 + i) * cpr + c) : u32x4{0, 0, 0, 0};
+    v[i] = in && r0 + i * kR < rows ? __builtin_nontemporal_load(x + (r0 + i * kR) * cpr + c) : u32x4{0, 0, 0, 0};
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
@@ -103,17 +107,18 @@ __global__ __launch_bounds__(64 * kTileWaves) void quant_fp8_tiles_kernel(
     m = m > a ? m : a;
   }
   m = fp8::row16_max(m);
-  if ((lane & 15) == 0) part[wave][lane >> 4] = m;
+  if ((lane & 15) == 0) part[tile][wave * kR + lane / kC] = m;
   __syncthreads();
-  m = fp8::row16_max(part[lane & 15][lane >> 4]);
+  static_assert(W * kR == 16, "a tile's partial maxima fill a DPP row");
+  m = fp8::row16_max(part[tile][lane & 15]);
   const fp8::Scale s = fp8::scale_of(__builtin_bit_cast(float, m << 16));
-  if (wave == 0 && (lane & 15) == 0 && in) scales[strip * (cpr / 16) + (c >> 4)] = s.value;
+  if (wave == 0 && lane < kC && (lane & 15) == 0 && in) scales[strip * (cpr / 16) + (c >> 4)] = s.value;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     float e[8];
     unpack8(v[i], e);
     const uint2 q = fp8::encode8(e, s);
-    if (in && r0 + i < rows) codes[(r0 + i) * cpr + c] = u32x2{q.x, q.y};
+    if (in && r0 + i * kR < rows) __builtin_nontemporal_store(u32x2{q.x, q.y}, codes + (r0 + i * kR) * cpr + c);
   }
 }
 
@@ -152,9 +157,9 @@ hipError_t quant_fp8(int fmt, int64_t rows, int64_t cols, const void* x, void* c
     return launch_kernel(&quant_fp8_rows_kernel, dim3((unsigned)((n + per - 1) / per)), kThreads, 0, s,
                          (const u32x4*)x, (u32x2*)codes, (float*)scales, n);
   }
-  const dim3 grid((unsigned)((cpr + 63) / 64 * ((rows + 127) / 128)));
-  return launch_kernel(&quant_fp8_tiles_kernel, grid, 64 * kTileWaves, 0, s, (const u32x4*)x,
-                       (u32x2*)codes, (float*)scales, rows, cpr);
+  const dim3 grid((unsigned)((cpr + 4 * W - 1) / (4 * W) * ((rows + 127) / 128)));
+  return launch_kernel(&quant_fp8_tiles_kernel, grid, 64 * W, 0, s, (const u32x4*)x, (u32x2*)codes,
+                       (float*)scales, rows, cpr);
 }
 
 hipError_t dequant_fp8(int fmt, int64_t rows, int64_t cols, const void* codes, const void* scales,

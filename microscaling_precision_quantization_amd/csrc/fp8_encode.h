@@ -21,10 +21,11 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return v;
 }
 
-// A block's scale: the stored value, and what encode8 works with (lift 2^64
-// for s < 2^-60, else 1).
+// A block's scale: the stored value, and what encode8 works with: the scale
+// times `lift` (2^64 for s < 2^-60, else 1), and its reciprocal a little
+// lowered and raised.
 struct Scale {
-  float value, lifted, inv, lift;
+  float value, lifted, lift, down, up;
   bool finite;
 };
 
@@ -36,7 +37,9 @@ __device__ __forceinline__ Scale scale_of(float amax) {
   s.value = s.finite ? v : __builtin_nanf("");
   s.lift = v < 0x1p-60f ? 0x1p64f : 1.0f;
   s.lifted = v * s.lift;
-  s.inv = __builtin_amdgcn_rcpf(s.lifted);
+  const float inv = __builtin_amdgcn_rcpf(s.lifted);
+  s.down = inv * (1.0f - 0x1p-20f);
+  s.up = inv * (1.0f + 0x1p-20f);
   return s;
 }
 
@@ -64,18 +67,19 @@ __device__ __forceinline__ uint32_t settle(uint32_t lo, uint32_t hi, float x, co
 
 // Codes of 8 elements of a block with scale s (zero if it is not finite).
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], const Scale& s) {
-  constexpr float kDown = 1.0f - 0x1p-20f, kUp = 1.0f + 0x1p-20f;
-  float y[8], v[8];
+  float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    y[i] = x[i] * s.lift;
-    v[i] = y[i] * s.inv;
+  for (int i = 0; i < 8; i++) y[i] = x[i];
+  if (s.lift != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[i] *= s.lift;
   }
   uint32_t lo[2], hi[2];
 #pragma unroll
   for (int h = 0; h < 2; h++) {
-    lo[h] = pack4(v[4 * h] * kDown, v[4 * h + 1] * kDown, v[4 * h + 2] * kDown, v[4 * h + 3] * kDown);
-    hi[h] = pack4(v[4 * h] * kUp, v[4 * h + 1] * kUp, v[4 * h + 2] * kUp, v[4 * h + 3] * kUp);
+    const float* v = y + 4 * h;
+    lo[h] = pack4(v[0] * s.down, v[1] * s.down, v[2] * s.down, v[3] * s.down);
+    hi[h] = pack4(v[0] * s.up, v[1] * s.up, v[2] * s.up, v[3] * s.up);
   }
   if (((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) != 0) {
 #pragma unroll

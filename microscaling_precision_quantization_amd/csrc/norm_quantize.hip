@@ -69,61 +69,74 @@ __global__ __launch_bounds__(T) void norm_quantize_kernel(NormArgs p) {
   __shared__ float part[4][16];
   const int tid = threadIdx.x;
   const int chunks = p.cols / 8;
-  u32x4 w[CH], pw[CH], gt[CH];
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-  for (int i = 0; i < CH; i++) {
+  auto chunk_of = [&](const uint16_t* v, int i) __attribute__((always_inline)) {
     const int c = i * T + tid;
-    w[i] = p.weight && c < chunks ? ((const u32x4*)p.weight)[c] : ones;
-    pw[i] = p.post && c < chunks ? ((const u32x4*)p.post)[c] : ones;
+    return v && c < chunks ? ((const u32x4*)v)[c] : ones;
+  };
+  // Rows of up to 4 chunks a thread have no VGPRs for them: the weights come from the
+  // caches for every row, and no row is loaded ahead.
+  constexpr bool kKeep = CH < 4;
+  u32x4 w[CH], pw[CH], gt[CH];
+#pragma unroll
+  for (int i = 0; i < CH && kKeep; i++) {
+    w[i] = chunk_of(p.weight, i);
+    pw[i] = chunk_of(p.post, i);
     gt[i] = ones;
   }
   int64_t gate_at = -1;
   const float inv = 1.0f / (float)p.cols;
   int slot = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, slot ^= 2) {
-    u32x4 vx[CH], vr[CH];
+  // The next row's inputs are loaded while a row is computed. (x and residual of
+  // a row are read before h, which may be the same memory, is written for it.)
+  u32x4 nx[CH], nr[CH];
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < CH; i++) {
       const int c = i * T + tid;
-      vx[i] = c < chunks ? ((const u32x4*)(p.x + row * p.ldx))[c] : u32x4{0, 0, 0, 0};
-      vr[i] = p.residual && c < chunks ? ((const u32x4*)(p.residual + row * p.ldr))[c] : u32x4{0, 0, 0, 0};
+      const bool in = c < chunks && row < p.rows;
+      nx[i] = in ? __builtin_nontemporal_load((const u32x4*)(p.x + row * p.ldx) + c) : u32x4{0, 0, 0, 0};
+      nr[i] = p.residual && in ? __builtin_nontemporal_load((const u32x4*)(p.residual + row * p.ldr) + c) : u32x4{0, 0, 0, 0};
     }
-    if (p.gate && row / p.gate_rows != gate_at) {
-      gate_at = row / p.gate_rows;
-#pragma unroll
-      for (int i = 0; i < CH; i++) {
-        const int c = i * T + tid;
-        if (c < chunks) gt[i] = ((const u32x4*)(p.gate + gate_at * p.cols))[c];
-      }
-    }
+  };
+  if (kKeep) fetch(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, slot ^= 2) {
+    if (!kKeep) fetch(row);
+    u32x4 vr[CH];
     float h[CH][8];
 #pragma unroll
-    for (int i = 0; i < CH; i++) unpack8(vx[i], h[i]);
+    for (int i = 0; i < CH; i++) {
+      unpack8(nx[i], h[i]);
+      vr[i] = nr[i];
+    }
+    if (kKeep) fetch(row + gridDim.x);
+    const uint16_t* gate = p.gate ? p.gate + row / p.gate_rows * p.cols : nullptr;
+    if (kKeep && gate && row / p.gate_rows != gate_at) {
+      gate_at = row / p.gate_rows;
+#pragma unroll
+      for (int i = 0; i < CH; i++) gt[i] = chunk_of(gate, i);
+    }
+    float ry = p.alpha;  // what the products x post_weight gate are multiplied by
     if (p.post) {
       float ss = 0.0f;
 #pragma unroll
       for (int i = 0; i < CH; i++)
 #pragma unroll
         for (int e = 0; e < 8; e++) ss = __builtin_fmaf(h[i][e], h[i][e], ss);
-      const float rs = 1.0f / sqrtf(block_sum<T>(ss, part[slot]) * inv + p.eps);
-#pragma unroll
-      for (int i = 0; i < CH; i++) {
-        float f[8];
-        unpack8(pw[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; e++) h[i][e] = h[i][e] * rs * f[e];
-      }
+      ry = p.alpha / sqrtf(block_sum<T>(ss, part[slot]) * inv + p.eps);
     }
+    // x post_weight gate has at most 24 significant bits and is exact, so h
+    // rounds once per element.
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-      float f[8], r[8];
-      unpack8(gt[i], f);
+      float f[8], q[8], r[8];
+      unpack8(kKeep ? gt[i] : chunk_of(gate, i), f);
+      unpack8(kKeep ? pw[i] : chunk_of(p.post, i), q);
       unpack8(vr[i], r);
 #pragma unroll
       for (int e = 0; e < 8; e++) {
-        h[i][e] = __builtin_fmaf(p.alpha, h[i][e] * f[e], r[e]);
+        h[i][e] = __builtin_fmaf(h[i][e] * q[e] * f[e], ry, r[e]);
         ss = __builtin_fmaf(h[i][e], h[i][e], ss);
       }
     }
@@ -131,9 +144,11 @@ __global__ __launch_bounds__(T) void norm_quantize_kernel(NormArgs p) {
 #pragma unroll
       for (int i = 0; i < CH; i++) {
         const int c = i * T + tid;
-        if (c < chunks)
-          ((u32x4*)(p.h + row * p.ldh))[c] = u32x4{pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]),
-                                                   pack_bf16x2(h[i][4], h[i][5]), pack_bf16x2(h[i][6], h[i][7])};
+        if (c >= chunks) continue;
+        const u32x4 v = {pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]), pack_bf16x2(h[i][4], h[i][5]),
+                         pack_bf16x2(h[i][6], h[i][7])};
+        u32x4* dst = (u32x4*)(p.h + row * p.ldh) + c;
+        __builtin_nontemporal_store(v, dst);
       }
     }
     const float rs = 1.0f / sqrtf(block_sum<T>(ss, part[slot + 1]) * inv + p.eps);
@@ -141,11 +156,11 @@ __global__ __launch_bounds__(T) void norm_quantize_kernel(NormArgs p) {
     for (int i = 0; i < CH; i++) {
       const int c = i * T + tid;
       float f[8], n[8];
-      unpack8(w[i], f);
+      unpack8(kKeep ? w[i] : chunk_of(p.weight, i), f);
       uint32_t m = 0;  // amax as bits: a larger magnitude has larger bits
 #pragma unroll
       for (int e = 0; e < 8; e++) {
-        n[e] = h[i][e] * rs * f[e];
+        n[e] = h[i][e] * f[e] * rs;
         m = umax(m, __builtin_bit_cast(uint32_t, n[e]) & 0x7FFFFFFFu);
       }
       // Where this chunk's codes go, in elements from the tensor's start.
