@@ -66,6 +66,14 @@ CASES = [  # sizes of the groups, N, K
     ([1] * 70, 48, 256),
     ([0, 2, 1] * 50, 33, 128),
     ([700], 260, 2048),
+    # few rows per expert on average, more than 16 in one: further passes over its weight
+    ([0, 40, 1, 0, 0, 0, 17, 0, 3, 0], 200, 1024),
+    ([1] * 12 + [60] + [0] * 30, 2100, 512),
+    # enough for tiles of 64, of 128 and of 256 square
+    ([33, 100, 1, 70], 2500, 256),
+    ([130, 255, 3, 129, 400], 3300, 384),
+    ([300, 511, 0, 700, 1], 4100, 512),
+    ([257, 64, 65, 128, 129, 1000], 4200, 768),
 ]
 
 
@@ -82,13 +90,12 @@ def test_grouped(sizes, N, K, fmt, out):
 
 @pytest.mark.parametrize("out", [F32, BF16])
 @pytest.mark.parametrize("K", [32, 64, 96, 160, 224, 736, 1056, 2880])
-@pytest.mark.parametrize("sizes", [[2, 0, 3], [70, 150, 1]])
+@pytest.mark.parametrize("sizes", [[2, 0, 3], [1, 18, 0, 0], [70, 150, 1], [300, 250, 600]])
 def test_mxfp4_odd_k(K, sizes, out):
-    """K that is no multiple of a step. Every row's first scale byte is NaN but
-    the first block's codes are read only by their own row: a kernel that read
-    past a row's end would spread the NaN."""
+    """K that is no multiple of a step. Then every second row's first scale is made
+    NaN: read past the end of the row before it, it would spread there."""
     require_gpu()
-    a, b = _operands("mxfp4", sum(sizes), len(sizes), 90, K, K)
+    a, b = _operands("mxfp4", sum(sizes), len(sizes), 90 if sum(sizes) < 1000 else 2000, K, K)
     off, d = _offsets(sizes)
     _check(mx.gemm_grouped(a, b, d, out), a, b, off, "mxfp4", out)
     a.scales[1::2, 0] = 255
@@ -123,14 +130,28 @@ def test_offsets_past_the_end_are_clamped(fmt):
         _check(mx.gemm_grouped(a, b, d, BF16), a, b, off, fmt, BF16)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("sizes,N,K", [([3, 0, 2], 200, 3584), ([60, 80], 300, 6400), ([700, 0, 900], 3900, 3328)])
+def test_long_chains_f32(sizes, N, K, fmt):
+    """Every product of one sign and K over one accumulation chain: within 2^-18 sum|ab|."""
+    require_gpu()
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.rand(sum(sizes), K, generator=gen, device="cuda").to(BF16)
+    w = torch.rand(len(sizes), N, K, generator=gen, device="cuda").to(BF16)
+    a = mx.quantize(x, "mxfp4" if fmt == "mxfp4" else "fp8_b128")
+    b = mx.quantize(w, "mxfp4" if fmt == "mxfp4" else "fp8_b128x128")
+    off, d = _offsets(sizes)
+    _check(mx.gemm_grouped(a, b, d, F32), a, b, off, fmt, F32)
+
+
 def test_more_groups_than_a_wave():
     """Row tiles are found by scanning the groups 64 at a time."""
     require_gpu()
     r = np.random.RandomState(0)
     for fmt in ("mxfp4", "fp8"):
-        for G, M in ((64, 900), (65, 40), (200, 2000), (300, 7)):
+        for G, M in ((64, 900), (65, 40), (200, 2000), (300, 7), (130, 9000)):
             sizes = r.multinomial(M, r.dirichlet(np.full(G, 0.3)))
-            a, b = _operands(fmt, M, G, 64, 128, G)
+            a, b = _operands(fmt, M, G, 64 if M < 9000 else 700, 128 if M < 9000 else 256, G)
             off, d = _offsets(sizes)
             _check(mx.gemm_grouped(a, b, d, BF16), a, b, off, fmt, BF16)
 
@@ -152,13 +173,14 @@ def test_equals_gemm_of_each_expert():
         assert torch.allclose(mx.gemm(ag, one, F32), got[rows], rtol=1e-5, atol=1e-5)
 
 
+@pytest.mark.parametrize("M,N", [(150, 256), (40, 100), (2400, 2600)])
 @pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
-def test_captured_with_new_offsets(fmt):
+def test_captured_with_new_offsets(fmt, M, N):
     """A captured call follows the offsets of each replay: they are read on the device."""
     require_gpu()
-    M, G, N, K = 150, 6, 256, 512
+    G, K = 6, 512
     a, b = _operands(fmt, M, G, N, K, 6)
-    _, d = _offsets([25] * 6)
+    _, d = _offsets([M // 6] * 6)
     out = torch.zeros(M, N, dtype=BF16, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -169,7 +191,7 @@ def test_captured_with_new_offsets(fmt):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         mx.gemm_grouped(a, b, d, BF16, out=out)
-    for sizes in ([150, 0, 0, 0, 0, 0], [1, 2, 3, 4, 5, 135], [0, 0, 75, 0, 75, 0]):
+    for sizes in ([M, 0, 0, 0, 0, 0], [1, 2, 3, 4, 5, M - 15], [0, 0, M // 2, 0, M - M // 2, 0]):
         off, new = _offsets(sizes)
         d.copy_(new)
         out.zero_()
