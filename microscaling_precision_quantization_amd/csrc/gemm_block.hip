@@ -336,8 +336,21 @@ hipError_t launch(const Args& a, hipStream_t s) {
 //   3000 over 4 x 600 x 992 - / 7.6 / 10.3.
 template <int FMT, bool EXACT, int OUT, bool ALIGNED>
 hipError_t by_tile(const Args& p, hipStream_t s) {
-  if ((p.offsets || p.M > 48) && tiles(p, 128, 128) >= (FMT == kMXFP4 ? 150 : 200))
-    return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 4, ALIGNED>>(p, s);
+  if ((p.offsets || p.M > 48) && tiles(p, 128, 128) >= (FMT == kMXFP4 ? 150 : 200)) {
+    if constexpr (EXACT) {
+      // Expanding codes is as much work as the MFMAs: 8 waves, so that a SIMD's
+      // second wave does one beside the other (2000 x 2000 x 2432 34 us with 4
+      // waves, 28 with 8), and, where rounds of CUs allow, 256 x 128 tiles, which expand less
+      // (8192 cubed 1480 / 1255 / 1100; a tile of 256 x 128 takes 2.15 us a step, of
+      // 128 x 128 1.25).
+      auto rounds = [](int64_t n) { return (n + 255) / 256; };
+      if (7 * rounds(tiles(p, 256, 128)) < 4 * rounds(tiles(p, 128, 128)))
+        return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 4, 2, 3, ALIGNED>>(p, s);
+      return launch<FMT, EXACT, OUT, Geo<FMT, 4, 2, 2, 4, 3, ALIGNED>>(p, s);
+    } else {
+      return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 4, ALIGNED>>(p, s);
+    }
+  }
   if (tiles(p, 64, 64) >= (p.M > 32 ? 200 : 300)) return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 2, 4, ALIGNED>>(p, s);
   return launch<FMT, EXACT, OUT, Geo<FMT, 1, 1, 2, 2, 6, ALIGNED>>(p, s);
 }
