@@ -237,20 +237,21 @@ def _check_qtensor(q, what):
     """The kernels read exactly the bytes a QTensor's shape implies: refuse
     buffers of another size, type or layout in memory."""
     import torch
-    if q.fmt not in BLOCK or q.fmt == MX_FMT_BF16 or q.cols % BLOCK[q.fmt] != 0:
+    fmt, codes, scales = q.fmt, q.codes, q.scales
+    if fmt not in BLOCK or fmt == MX_FMT_BF16 or q.cols % BLOCK[fmt] != 0:
         raise ValueError(f"{what}: not a quantized tensor of a supported format")
     if q.groups < 1 or q.rows % q.groups != 0:
         raise ValueError(f"{what}: {q.rows} rows are not a stack of {q.groups} weights")
-    need_c = q.rows * code_cols(q.fmt, q.cols)
+    need_c = q.rows * code_cols(fmt, q.cols)
     need_s = q.groups
-    for d in scale_shape(q.fmt, q.rows // q.groups, q.cols):
+    for d in scale_shape(fmt, q.rows // q.groups, q.cols):
         need_s *= d
-    if q.codes.dtype != torch.uint8 or not q.codes.is_contiguous() or q.codes.numel() != need_c:
+    if codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.numel() != need_c:
         raise ValueError(f"{what}: codes must be a contiguous uint8 tensor of {need_c} bytes")
-    st, name = (torch.float32, "float32") if q.fmt in FP8_BLOCK_FORMATS else (torch.uint8, "uint8")
-    if q.scales.dtype != st or not q.scales.is_contiguous() or q.scales.numel() != need_s:
+    st, name = (torch.float32, "float32") if fmt in FP8_BLOCK_FORMATS else (torch.uint8, "uint8")
+    if scales.dtype != st or not scales.is_contiguous() or scales.numel() != need_s:
         raise ValueError(f"{what}: scales must be a contiguous {name} tensor of {need_s} elements")
-    if q.fmt == MX_FMT_NVFP4:
+    if fmt == MX_FMT_NVFP4:
         ts = q.tensor_scale
         if ts is None or ts.dtype != torch.float32 or ts.numel() < 1:
             raise ValueError(f"{what}: NVFP4 needs a float32 tensor scale")
@@ -324,9 +325,9 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
         rows, cols = x.shape
         codes = torch.empty((rows, code_cols(f, cols)), dtype=torch.uint8, device=x.device)
         scales = torch.empty(scale_shape(f, rows, cols), dtype=torch.uint8, device=x.device)
-        _check(mx_quantize_ex(f, BLOCK[f], MX_ROUND_RNE, SCALE_RULES[scale_rule], ROTATIONS[rotation], rows,
-                              cols, _ptr(x), _ptr(codes), _ptr(scales), _stream(torch, x.device, x), lay),
-               "mx_quantize_ex")
+        _check(_on(x.device, mx_quantize_ex, f, BLOCK[f], MX_ROUND_RNE, SCALE_RULES[scale_rule],
+                   ROTATIONS[rotation], rows, cols, _ptr(x), _ptr(codes), _ptr(scales),
+                   _stream(torch, x.device, x), lay), "mx_quantize_ex")
         return QTensor(f, rows, cols, codes, scales, None, lay)
     if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("quantize expects a contiguous 2-D bfloat16 tensor")
@@ -345,8 +346,8 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
         _check(_on(dev, lib().mx_quantize, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
                    _ptr(scales), _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x)), "mx_quantize")
     else:
-        _check(mx_quantize_layout(f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
-                                  _ptr(scales), _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x), lay),
+        _check(_on(dev, mx_quantize_layout, f, BLOCK[f], MX_ROUND_RNE, rows, cols, _ptr(x), _ptr(codes),
+                   _ptr(scales), _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x), lay),
                "mx_quantize_layout")
     return QTensor(f, rows, cols, codes, scales, ts, lay)
 
@@ -403,8 +404,8 @@ def pack(q):
         raise ValueError("pack() takes one weight, not a stack")
     codes = torch.empty_like(q.codes)
     scales = torch.empty_like(q.scales)
-    _check(mx_pack(q.fmt, q.block, q.rows, q.cols, _ptr(q.codes), _ptr(q.scales), _ptr(codes),
-                   _ptr(scales), _stream(torch, q.codes.device, q.codes, q.scales)), "mx_pack")
+    _check(_on(q.codes.device, mx_pack, q.fmt, q.block, q.rows, q.cols, _ptr(q.codes), _ptr(q.scales),
+               _ptr(codes), _ptr(scales), _stream(torch, q.codes.device, q.codes, q.scales)), "mx_pack")
     return QTensor(q.fmt, q.rows, q.cols, codes, scales, q.tensor_scale, MX_LAYOUT_KPANEL)
 
 
@@ -439,7 +440,7 @@ def gemm(a, b, out_dtype=None, out=None, workspace=None):
                 or out.stride(1) != 1):
             raise ValueError(f"out must be a [{M}][{N}] {out_dtype} tensor with unit column stride")
     c = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=dev)
-    wsb = mx_gemm_workspace_bytes(fa, b.fmt, M, N, K)
+    wsb = mx_gemm_workspace_bytes(fa, b.fmt, M, N, K) if fa == MX_FMT_BF16 else 0  # (no other pair has one)
     if wsb and workspace is None:
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
     if workspace is not None:
@@ -450,9 +451,9 @@ def gemm(a, b, out_dtype=None, out=None, workspace=None):
     a_parts = (a.codes, a.scales, a.tensor_scale) if isinstance(a, QTensor) else (a,)
     stream = _stream(torch, dev, *a_parts, b.codes, b.scales, b.tensor_scale, c, workspace)
     if la != MX_LAYOUT_ROWS or b.layout != MX_LAYOUT_ROWS:
-        _check(mx_gemm_ex(fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta, _ptr(b.codes),
-                          _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0),
-                          _ptr(workspace), wsb, stream, la, b.layout), "mx_gemm_ex")
+        _check(_on(dev, lib().mx_gemm_ex, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta,
+                   _ptr(b.codes), _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0),
+                   _ptr(workspace), wsb, stream, la, b.layout), "mx_gemm_ex")
         return c
     _check(_on(dev, lib().mx_gemm, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta, _ptr(b.codes),
                _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0), _ptr(workspace), wsb,
