@@ -282,7 +282,8 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
  * A bf16 output rounds an fp32 value once more (within 2^-8 * |C_ij|); on the
  * 256 x 256-tile kernels that value is one chain over all of K (K / 64 steps
  * for MXFP4, K / 16 for the 16-bit paths, K / 128 for MBS), so before that
- * rounding it errs by at most (steps + c) * 2^-24 * S_ij. The FP8 pair: an
+ * rounding it errs by at most (steps + c) * 2^-24 * S_ij. The FP8 pair (the
+ * products s_A s_B within fp32's range): an
  * fp32 result has chains of 48 blocks of 128 K, each block adding at most 6
  * roundings of its own (c = 6); a bf16 result takes its P from the FP8 MFMA,
  * which drops low bits of a 128-term sum (measured: of 8 products that it adds
@@ -399,7 +400,8 @@ mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   residual's own memory, with the same stride; other overlaps are not allowed.
  * gate (NULL: 1): bf16 [ceil(rows / gate_rows)][cols]; row r takes gate row
  *   r / gate_rows. post_weight, weight (NULL: 1): bf16 [cols].
- * alpha finite; eps finite and >= 0.
+ * alpha finite; eps finite and >= 0. The sums of squares of x and h have to stay
+ * in fp32's range; with eps = 0 a row of zeros gives NaN, as the formula does.
  * codes, scales: as mx_quantize_layout writes them in `layout`
  *   (MX_LAYOUT_KPANEL: MXFP4 and MXFP8, with its conditions).
  */
