@@ -3,7 +3,8 @@
 // so the grid is made for the most tiles that any offsets of M rows can need,
 // and each workgroup finds its tile by itself: every wave scans the groups'
 // tile counts, 64 groups at a time. Offsets are clamped to [0, M], so that no
-// value of theirs leads outside A or C.
+// value of theirs leads outside A or C; where they then fall, groups overlap and
+// their tiles may be more than the grid and the counts hold: no tile is done.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -66,9 +67,14 @@ __device__ __forceinline__ bool tile_of(const int* offsets, int n, int M, int ti
   // Each lane's group (of 64 at a time), and the scan of the whole tiles times
   // 128 plus the partly filled ones, at most 64 in a wave.
   int lo = 0, hi = 0, scan = 0, whole = 0, part = 0;
+  bool falls = false;
   auto look = [&](int c) {
     lo = hi = 0;
-    if (c + lane < n) rows_of(offsets, M, c + lane, lo, hi);
+    if (c + lane < n) {
+      lo = min(max(offsets[c + lane], 0), M);
+      hi = min(max(offsets[c + lane + 1], 0), M);
+    }
+    falls |= __ballot(hi < lo) != 0;
     scan = wave_scan((hi - lo) / BM * 128 + ((hi - lo) % BM != 0));
     return __builtin_amdgcn_readlane(scan, 63);
   };
@@ -81,6 +87,7 @@ __device__ __forceinline__ bool tile_of(const int* offsets, int n, int M, int ti
       whole += all / 128;
       part += all % 128;
     }
+    if (falls) return false;
   }
   const int i = bid / 8, x = bid % 8;
   const int share = (whole * tiles_n + 7) / 8, share2 = (part * tiles_n + 7) / 8;

@@ -131,6 +131,51 @@ def test_offsets_past_the_end_are_clamped(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("M,N", [(20, 64), (400, 200), (1500, 2600), (3000, 4000)])
+def test_offsets_out_of_order(M, N, fmt):
+    """Undefined rows of C, but nothing outside C; and the next call is right."""
+    require_gpu()
+    a, b = _operands(fmt, M, 5, N, 256, 6)
+    for bad in ([0, M, 0, M, 0, M], [M, 0, 0, M, 3, 1], [2**31 - 1, -2**31, 5, 4, 3, M]):
+        d = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        for out in (F32, BF16):
+            buf = torch.full((M + 2, N + 8), 7.0, dtype=out, device="cuda")
+            mx.gemm_grouped(a, b, d, out, out=buf[1:M + 1, :N])
+            assert bool((buf[0] == 7).all()) and bool((buf[M + 1] == 7).all()) and bool((buf[:, N:] == 7).all())
+    off, d = _offsets([M // 5] * 4 + [M - M // 5 * 4])
+    _check(mx.gemm_grouped(a, b, d, BF16), a, b, off, fmt, BF16)
+
+
+def test_one_row_into_any_stride():
+    """The row stride of a single row says nothing."""
+    require_gpu()
+    a, b = _operands("fp8", 1, 2, 100, 256, 7)
+    off, d = _offsets([0, 1])
+    out = torch.empty(100, 1, dtype=BF16, device="cuda").t()
+    assert out.stride() == (1, 1)
+    _check(mx.gemm_grouped(a, b, d, BF16, out=out), a, b, off, "fp8", BF16)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_stack_past_32_bits(rows):
+    """A stack of more than 2^32 code bytes: the last expert is its own."""
+    require_gpu()
+    G, N, K = 17, 16384, 16384
+    one = mx.quantize((torch.arange(N * K, device="cuda") % 251 - 125).to(BF16).view(N, K), "fp8_b128x128")
+    codes = torch.zeros(G * N, K, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(G, N // 128, K // 128, device="cuda")
+    codes[-N:].copy_(one.codes)
+    scales[-1].copy_(one.scales)
+    b = mx.QTensor(one.fmt, G * N, K, codes, scales, groups=G)
+    a = mx.quantize((torch.arange(rows * K, device="cuda") % 127 - 63).to(BF16).view(rows, K), "fp8_b128")
+    d = torch.tensor([0] * G + [rows], dtype=torch.int32, device="cuda")
+    got, want = mx.gemm_grouped(a, b, d, F32), mx.gemm(a, one, F32)
+    # Both are within 2^-18 sum|ab|, which Cauchy-Schwarz bounds by the rows' norms.
+    bound = 2.0**-17 * mx.dequantize(a).norm(dim=1, keepdim=True) * mx.dequantize(one).norm(dim=1)[None, :]
+    assert bool(((got - want).abs() <= bound).all()) and bool((want != 0).any())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
 @pytest.mark.parametrize("sizes,N,K", [([3, 0, 2], 200, 3584), ([60, 80], 300, 6400), ([700, 0, 900], 3900, 3328)])
 def test_long_chains_f32(sizes, N, K, fmt):
     """Every product of one sign and K over one accumulation chain: within 2^-18 sum|ab|."""
