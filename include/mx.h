@@ -252,9 +252,10 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
  *                       base blocks two MFMAs per 32 K, one per half) and the
  *                       vector ALU adds P * f_A * f_B (f_A f_B exact in fp32)
  *                       to the accumulator
- *   (FP8_B128, FP8_B128X128, 128)  K a multiple of 128, at most 2^22: per 128 K
- *                       the matrix core's partial sum P, plus P * fl32(s_A s_B)
- *                       on the vector ALU. For an fp32 result P comes from bf16
+ *   (FP8_B128, FP8_B128X128, 128)  K a multiple of 128, at most 2^22, and fewer
+ *                       than 2^23 tiles of 128 x 128 of C: per 128 K the
+ *                       matrix core's partial sum P, plus P * fl32(s_A s_B) on
+ *                       the vector ALU. For an fp32 result P comes from bf16
  *                       MFMAs on the exactly expanded codes; for a bf16 result
  *                       from the FP8 MFMA
  *   (BF16,  MXFP4, 32)  W4A16: bf16 activations times MXFP4 weights expanded
@@ -378,7 +379,8 @@ mx_status mx_gemm_noalloc(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   rows; b_scales: MXFP4 [groups][N][K/32], FP8_B128X128
  *   [groups][ceil(N/128)][K/128] (each weight quantized by itself).
  * c: [M][ldc] fp32 or bf16. Limits: M, N <= 2^30, K <= 2^22, groups <= 65535,
- * M K and groups N K <= 2^40. No workspace. Accuracy as mx_gemm's for the pair.
+ * M K and groups N K <= 2^40, and (M / 128 + min(groups, M)) * N / 128 tiles
+ * below 2^23. No workspace. Accuracy as mx_gemm's for the pair.
  */
 mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, int64_t groups,
                           int64_t M, int64_t N, int64_t K, const int32_t* offsets, const void* a,
@@ -400,8 +402,8 @@ mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   residual's own memory, with the same stride; other overlaps are not allowed.
  * gate (NULL: 1): bf16 [ceil(rows / gate_rows)][cols]; row r takes gate row
  *   r / gate_rows. post_weight, weight (NULL: 1): bf16 [cols].
- * alpha finite; eps finite and >= 0. The sums of squares of x and h have to stay
- * in fp32's range; with eps = 0 a row of zeros gives NaN, as the formula does.
+ * alpha finite; eps finite and >= 0. The sums of squares of x and h and the products
+ * x * post_weight * gate and h * weight have to stay in fp32's range; with eps = 0 a row of zeros gives NaN, as the formula does.
  * codes, scales: as mx_quantize_layout writes them in `layout`
  *   (MX_LAYOUT_KPANEL: MXFP4 and MXFP8, with its conditions).
  */

@@ -491,8 +491,8 @@ def gemm_grouped(a, b, offsets, out_dtype=None, out=None):
     stream = _stream(torch, dev, a.codes, a.scales, b.codes, b.scales, offsets, out)
     _check(_on(dev, lib().mx_gemm_grouped, a.fmt, b.fmt, b.block, MX_ROUND_RNE, G, M, N, K, _ptr(offsets),
                _ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales),
-               MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, _ptr(out), out.stride(0),
-               stream), "mx_gemm_grouped")
+               MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, _ptr(out),
+               out.stride(0) if M > 1 else N, stream), "mx_gemm_grouped")
     return out
 
 
@@ -501,7 +501,8 @@ def norm_quantize(x, weight, fmt, residual=None, gate=None, post_weight=None, al
     """The norms between two blocks, fused with the residual and the quantizer:
     y = x, or its RMS norm times post_weight; h = residual + alpha * gate * y;
     the RMS norm of h times weight, quantized to `fmt` (mxfp4, mxfp8 or
-    fp8_b128). x, residual: bf16 [rows][cols] with unit column stride; weight,
+    fp8_b128). x, residual: bf16 [rows][cols] with unit column stride and rows
+    that start on 16 bytes; weight,
     post_weight: bf16 [cols] (weight None: ones); gate: bf16 [cols] or [n][cols],
     each of its rows for rows / n rows of x. Returns the QTensor and h (bf16;
     `out` if given, which may be x or residual; None without a residual or out)."""
@@ -521,9 +522,10 @@ def norm_quantize(x, weight, fmt, residual=None, gate=None, post_weight=None, al
             raise ValueError(f"{name} must be a contiguous bfloat16 tensor of {cols} elements")
     gate_rows = 0
     if gate is not None:
-        n = 1 if gate.dim() == 1 else gate.shape[0]
-        if gate.dtype != bf16 or gate.dim() > 2 or gate.shape[-1] != cols or not gate.is_contiguous():
+        if (gate.dtype != bf16 or gate.dim() not in (1, 2) or gate.shape[-1] != cols
+                or not gate.is_contiguous()):
             raise ValueError(f"gate must be a contiguous bfloat16 tensor of rows of {cols}")
+        n = 1 if gate.dim() == 1 else gate.shape[0]
         if n < 1 or rows % n != 0:
             raise ValueError(f"{rows} rows do not divide among {n} gates")
         gate_rows = rows // n

@@ -358,11 +358,12 @@ hipError_t by_tile(const Args& p, hipStream_t s) {
 }  // namespace
 
 // Whether the kernels' 32-bit offsets hold (256 rows of codes and of scales)
-// and the grid of 128 x 128 tiles (smaller ones are for few) its 2^32 threads.
+// and the grid its 2^32 threads: 128 x 128 tiles of 512; smaller tiles are for
+// few, or for at most 48 rows, where 64 x 64 ones of 256 are twice as many.
 bool gemm_block_fits(int64_t M, int64_t N, int64_t K, int64_t groups) {
   if (K > ((int64_t)1 << 22)) return false;
   const int64_t tm = groups > 0 ? groups::max_row_tiles(M, groups, 128) : (M + 127) / 128;
-  return groups::grid_size(tm, (N + 127) / 128) < ((int64_t)1 << 24);
+  return groups::grid_size(tm, (N + 127) / 128) < ((int64_t)1 << 23);
 }
 
 hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,

@@ -113,6 +113,32 @@ def test_dequantize(fmt, out):
         assert np.all(same | (np.isnan(want.numpy()) & np.isnan(host(y.float()))))
 
 
+def test_dequantize_past_one_grid():
+    """More chunks than threads of a grid, and byte offsets past 32 bits (52 GB)."""
+    require_gpu()
+    rows, cols = (1 << 17) + 128, 1 << 17
+    codes = torch.zeros(rows, cols, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(rows // 128, cols // 128, device="cuda")
+    for r, c in ((0, 5), (70000, 3), (1 << 17, 0), (rows - 1, cols - 1)):
+        codes[r, c] = 0x38  # 1
+    scales[-1, -1] = 3.0
+    y = mx.dequantize(mx.QTensor(mx.MX_FMT_FP8_B128X128, rows, cols, codes, scales), BF16)
+    assert y[0, 5] == 1 and y[70000, 3] == 1 and y[1 << 17, 0] == 1 and y[-1, -1] == 3
+    assert y[-128:].float().sum().item() == 4 and y[:128].float().sum().item() == 1
+
+
+def test_gemm_without_allocation():
+    """mx_gemm_noalloc gives mx_gemm's bits: the pair needs no scratch."""
+    require_gpu()
+    a, b = _operands(20, 300, 512, 12)
+    want = mx.gemm(a, b, BF16)
+    got = torch.empty_like(want)
+    assert mx.mx_gemm_noalloc(a.fmt, b.fmt, 128, 0, 20, 300, 512, a.codes.data_ptr(), a.scales.data_ptr(), None,
+                              b.codes.data_ptr(), b.scales.data_ptr(), None, mx.MX_OUT_BF16, got.data_ptr(), 300,
+                              torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(got, want)
+
+
 def _operands(M, N, K, seed):
     r = np.random.RandomState(seed)
     a = _bf16(r.standard_normal((M, K)) * np.where(r.random_sample(K) < 0.01, 40, 1))
@@ -173,11 +199,11 @@ def test_gemm_random_codes(M, out):
 
 
 @pytest.mark.parametrize("out", [F32, BF16])
-@pytest.mark.parametrize("M", [2, 200])
-def test_gemm_nan(M, out):
+@pytest.mark.parametrize("M,N", [(2, 200), (200, 200), (1500, 5000)])
+def test_gemm_nan(M, N, out):
     """A NaN scale of A reaches its row, one of B its 128 columns, a NaN code its row or column."""
     require_gpu()
-    a, b = _operands(M, 200, 512, 9)
+    a, b = _operands(M, N, 512, 9)
     a.scales[1, 2] = float("nan")
     b.scales[0, 3] = float("nan")
     b.codes[150, 7] = 0x7F

@@ -37,6 +37,7 @@ def test_fp8_quantize_and_dequantize(fmt):
     (dict(K=192), INV), (dict(K=(1 << 22) + 128), INV), (dict(sa=MIS), INV), (dict(sb=MIS), INV),
     (dict(ts=P), INV), (dict(ldc=63), INV), (dict(a=P4), INV), (dict(sb=None), INV),
     (dict(M=1 << 23, N=1 << 30, ldc=1 << 30), INV),  # more tiles than a grid holds
+    (dict(M=40, N=1 << 30, ldc=1 << 30), INV), (dict(M=65535 * 128, N=16512, ldc=16512), INV),
 ])
 def test_fp8_gemm(kw, status):
     a = dict(fa=A8, fb=B8, block=128, M=64, N=64, K=256, a=P, sa=P4, ts=None, b=P, sb=P4, ldc=64)
@@ -53,6 +54,7 @@ def test_fp8_gemm(kw, status):
     (dict(off=None), INV), (dict(off=MIS), INV), (dict(a=None), INV), (dict(sa=P4), INV), (dict(b=P4), INV),
     (dict(sb=None), INV), (dict(c=P4), INV), (dict(ldc=63), INV),
     (dict(M=1 << 30, N=1 << 30, ldc=1 << 30), INV),
+    (dict(groups=65535, M=1 << 20, N=16384, ldc=16384, fa=A8, fb=B8, block=128), INV),  # mostly partly filled tiles
 ])
 def test_grouped(kw, status):
     a = dict(fa=1, fb=1, block=32, rnd=0, groups=3, M=64, N=64, K=256, off=P4, a=P, sa=P, b=P, sb=P, od=0, c=P2, ldc=64)
@@ -173,7 +175,7 @@ def test_python_norm_quantize():
                       (dict(x=x.t()), "x must be"), (dict(residual=x[:3]), "residual must be"),
                       (dict(out=x.float()), "out must be"), (dict(weight=w[:128]), "weight must be"),
                       (dict(post_weight=w.float()), "post_weight must be"), (dict(gate=w[:128]), "gate must be"),
-                      (dict(gate=x.view(2, 3, 256)), "gate must be"), (dict(gate=x[:4]), "do not divide"),
+                      (dict(gate=x.view(2, 3, 256)), "gate must be"), (dict(gate=w[0]), "gate must be"), (dict(gate=x[:4]), "do not divide"),
                       (dict(gate=x[:0]), "do not divide")):
         with pytest.raises(ValueError, match=match):
             mx.norm_quantize(**{**dict(x=x, weight=w, fmt="mxfp4"), **kw})
