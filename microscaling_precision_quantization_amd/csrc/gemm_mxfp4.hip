@@ -313,7 +313,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_mxfp4_kernel(
   int tm, tn;
   if constexpr (GROUPED) {
     groups::Tile t;
-    if (!groups::tile_of<BM>(offsets, groups, M, tiles_n, blockIdx.x, t)) return;
+    if (!groups::tile_of<BM, true>(offsets, groups, M, tiles_n, blockIdx.x, t)) return;
     tm = 0;
     tn = t.tn;
     M = min(t.rows, BM);

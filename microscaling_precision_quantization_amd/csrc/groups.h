@@ -21,7 +21,7 @@ inline int64_t max_row_tiles(int64_t M, int64_t n, int64_t bm) {
 }
 
 // Workgroups of a 1-D grid for that many row tiles and tiles_n column tiles:
-// two multiples of 8 (whole and partly filled tiles), for tile_of below.
+// two multiples of 8 (both kinds of tiles), for tile_of below.
 inline int64_t grid_size(int64_t row_tiles, int64_t tiles_n) { return (row_tiles * tiles_n + 14) / 8 * 8; }
 
 struct Tile {
@@ -56,16 +56,21 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // Tile of workgroup `bid`; false: there is none. offsets null: one group of
-// all M rows. Whole tiles come first, partly filled ones, which take less
-// time, last, so that they even out the end of the launch. Workgroup ids go
-// round-robin over the 8 XCDs; XCD x gets an eighth of each kind in a row,
-// rastered in groups of 4 row tiles, so that its L2 holds the rows and
-// columns its tiles share.
-template <int BM>
+// all M rows. Workgroup ids go round-robin over the 8 XCDs. Tiles of more than
+// BM / 2 rows ("whole") come first, an expert's last tile of fewer, which takes
+// less time, at the end, so that these even out the end of the launch (FP8, 8192
+// rows over 16 experts of 4096 x 4096: 164 us, 172 where only tiles of BM rows come first).
+//   XCD x gets an eighth of each kind in a row, rastered in groups of 4 row
+// tiles, so that its L2 holds the rows and columns its tiles share.
+//   ROUNDS: the XCDs get 32 tiles (one a CU) each of one row of 256, and the next
+// 256, in groups of 8 row tiles: what the XCDs read at a time is then shared between
+// them too, and comes from HBM once. MXFP4, 16384 rows over 8 x 8192 x 4096: 345 us, 367
+// without; but FP8, whose steps take longer for the same bytes, is 2% slower so.
+template <int BM, bool ROUNDS = false>
 __device__ __forceinline__ bool tile_of(const int* offsets, int n, int M, int tiles_n, int bid, Tile& t) {
   const int lane = threadIdx.x & 63;
   // Each lane's group (of 64 at a time), and the scan of the whole tiles times
-  // 128 plus the partly filled ones, at most 64 in a wave.
+  // 128 plus the others, at most 64 in a wave.
   int lo = 0, hi = 0, scan = 0, whole = 0, part = 0;
   bool falls = false;
   auto look = [&](int c) {
@@ -75,12 +80,12 @@ __device__ __forceinline__ bool tile_of(const int* offsets, int n, int M, int ti
       hi = min(max(offsets[c + lane + 1], 0), M);
     }
     falls |= __ballot(hi < lo) != 0;
-    scan = wave_scan((hi - lo) / BM * 128 + ((hi - lo) % BM != 0));
+    scan = wave_scan((hi - lo + BM / 2 - 1) / BM * 128 + ((hi - lo) % BM != 0 && (hi - lo) % BM <= BM / 2));
     return __builtin_amdgcn_readlane(scan, 63);
   };
   if (!offsets) {
-    whole = M / BM;
-    part = M % BM != 0;
+    whole = (M + BM / 2 - 1) / BM;
+    part = M % BM != 0 && M % BM <= BM / 2;
   } else {
     for (int c = 0; c < n; c += 64) {
       const int all = look(c);
@@ -92,10 +97,17 @@ __device__ __forceinline__ bool tile_of(const int* offsets, int n, int M, int ti
   const int i = bid / 8, x = bid % 8;
   const int share = (whole * tiles_n + 7) / 8, share2 = (part * tiles_n + 7) / 8;
   const bool first = i < share;
-  const int id = first ? x * share + i : x * share2 + i - share;
-  const int rows = first ? whole : part;
-  if (i >= share + share2 || id >= rows * tiles_n) return false;
-  constexpr int GM = 4;
+  const int rows = first ? whole : part, j = first ? i : i - share;
+  if (i >= share + share2) return false;
+  int id;
+  if constexpr (ROUNDS) {
+    const int rounds = rows * tiles_n / 256, rest = rows * tiles_n - rounds * 256;
+    id = j < rounds * 32 ? (j / 32 * 8 + x) * 32 + j % 32 : rounds * 256 + x * ((rest + 7) / 8) + j - rounds * 32;
+  } else {
+    id = x * (first ? share : share2) + j;
+  }
+  if (id >= rows * tiles_n) return false;
+  constexpr int GM = ROUNDS ? 8 : 4;
   const int top = id / (GM * tiles_n) * GM, width = min(rows - top, GM);
   const int within = id % (GM * tiles_n);
   int tm = top + within % width;
