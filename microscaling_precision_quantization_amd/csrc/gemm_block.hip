@@ -16,10 +16,11 @@
 //
 // Operands and A's (MXFP4: both) scales go HBM -> LDS directly (buffer_load ...
 // lds) into a ring of NS stages, a K step each, NS - 1 of them in flight: with few tiles the
-// loads' latency is what a step takes. The buffer view of a tile ends with
-// the group's rows, so rows past the end load as zeros. LDS rows hold a K step
-// (128 or 64 bytes); the 16-byte chunk c of row r sits in slot c ^ swz(r), so that
-// the 16 lanes that read one column of chunks hit distinct banks.
+// loads' latency is what a step takes. A step is 128 bytes of each row, a whole line:
+// 128 K of FP8, 256 K (two MFMAs) of MXFP4. The buffer view of a tile ends with
+// the group's rows, so rows past the end load as zeros. The 16-byte chunk c of LDS
+// row r sits in slot c ^ swz(r), so that the 16 lanes that read one column of
+// chunks hit distinct banks.
 //
 // B goes first into the MFMA: lane r + 16 g then holds C[row r][columns 4 g ..
 // 4 g + 3] of a tile, one row (one s_A) and a run of columns to store.
@@ -42,11 +43,13 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
 constexpr uint32_t kOOB = 0x80000000u;        // an offset past every buffer's range
-constexpr int kSegSteps = 48;                 // K steps per accumulation chain (fp32 results)
+constexpr int kChain = 48;                    // MFMAs per accumulation chain (fp32 results)
+constexpr int kRow = 128, kCpr = kRow / 16;   // LDS bytes and chunks of a row's K step
+constexpr int kRpb = 64 / kCpr;               // rows per 1 KB load of a wave
 
 // Tile geometry: waves of 16 TMW x 16 TNW, WM x WN of them; NS stages. ALIGNED: a
-// row's MXFP4 scales start on dwords (K % 128 = 0), so that a step's four are
-// one load; otherwise they are four loads of a byte, which LDS holds as a dword.
+// row's MXFP4 scales start on dwords (K % 128 = 0), so that a step's eight are
+// two loads; otherwise they are eight loads of a byte, which LDS holds as a dword.
 template <int FMT, int TMW_, int TNW_, int WM_, int WN_, int NS_, bool ALIGNED_ = true>
 struct Geo {
   static constexpr int TMW = TMW_, TNW = TNW_, WM = WM_, WN = WN_, NS = NS_;
@@ -54,16 +57,13 @@ struct Geo {
   static constexpr int BM = 16 * TMW * WM, BN = 16 * TNW * WN;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr bool kFp8 = FMT == kFP8B128;
-  static constexpr int kRow = kFp8 ? 128 : 64;  // LDS bytes of a row's K step
-  static constexpr int kCpr = kRow / 16;        // chunks per row
-  static constexpr int kRpb = 64 / kCpr;        // rows per 1 KB load of a wave
   static constexpr int kOffB = BM * kRow;
   // Scales, a dword a row, loaded 64 rows at a time: FP8 s_A of A's rows; MXFP4
-  // the step's four of A's and then of B's rows, or (not ALIGNED) that four
-  // times, a byte of each.
+  // four of the step's of A's and then of B's rows, and the other four, or (not
+  // ALIGNED) that eight times, a byte of each.
   static constexpr int kOffS = kOffB + BN * kRow;
   static constexpr int kScaleA = (BM + 63) / 64, kScaleGroups = kFp8 ? kScaleA : kScaleA + (BN + 63) / 64;
-  static constexpr int kScaleLoads = kScaleGroups * (kAligned ? 1 : 4);
+  static constexpr int kScaleParts = kFp8 ? 1 : kAligned ? 2 : 8, kScaleLoads = kScaleGroups * kScaleParts;
   static constexpr int kCodeLoads = (BM + BN) / kRpb;
   // Loads of a wave and step: every wave the same number, so that a count of
   // outstanding loads means the same steps in all (the rest go nowhere: out of
@@ -71,13 +71,10 @@ struct Geo {
   static constexpr int kLoads = (kCodeLoads + kScaleLoads + kWaves - 1) / kWaves;
   static constexpr int kStage = kOffS + kScaleLoads * 256;
   static constexpr int kDummy = NS * kStage, kSmem = kDummy + 1024;
-  static_assert(kSmem <= 160 * 1024 && (NS - 1) * kLoads < 64, "tile");
+  static_assert(kSmem <= 160 * 1024 && (NS - 1) * kLoads < 64 && BM / kRpb % kWaves == 0 && BN / kRpb % kWaves == 0, "tile");
 };
 
-template <bool FP8>
-__device__ __forceinline__ int swz(int row) {
-  return FP8 ? (row >> 1) & 7 : (row >> 2) & 3;
-}
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
 // 8 E4M3 codes as bf16.
 __device__ __forceinline__ bf16x8 expand8(int lo, int hi) {
@@ -100,6 +97,7 @@ struct Args {
 template <int FMT, bool EXACT, int OUT, class G>
 __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
   constexpr bool FP8 = G::kFp8;
+  constexpr int kSeg = FP8 ? kChain : kChain / 2;  // steps of a chain
   __shared__ __attribute__((aligned(1024))) uint8_t smem[G::kSmem];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / G::WN, wn = wave % G::WN;
@@ -110,7 +108,7 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
   const int n0 = t.tn * G::BN;
   const int mrows = min(t.rows, G::BM), nrows = min(p.N - n0, G::BN);
   const uint32_t rowbytes = (uint32_t)(FP8 ? p.K : p.K / 2);
-  const int nk = (p.K + 127) / 128;
+  const int nk = (int)((rowbytes + kRow - 1) / kRow);
   const int kblocks = p.K / 32;                   // MXFP4: scales per row
   const int64_t brow = (int64_t)t.group * p.N + n0;  // row of B among all weights
 
@@ -127,37 +125,39 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
   const int nb = min(n0 + wn * 16 * G::TNW, p.N - 1) / 128;
   const float* sb_row = (const float*)p.SB + ((int64_t)t.group * ((p.N + 127) / 128) + nb) * nk;
 
-  // Loads of step s into its stage: codes, 1 KB (kRpb rows) each, then scales,
-  // 64 rows each. Steps past the last load nothing, but are counted.
+  // Loads of step s into its stage: A's and B's codes, 1 KB (kRpb rows) each, then
+  // scales, 64 rows each. Steps past the last load nothing, but are counted.
   auto issue = [&](int s, uint8_t* stage) __attribute__((always_inline)) {
-    constexpr int kA = G::BM / G::kRpb;
-    const bool in = s < nk;
+    constexpr int kA = G::BM / kRpb;
 #pragma unroll
-    for (int i = 0; i < G::kLoads; i++) {
+    for (int i = 0; i < G::kCodeLoads / G::kWaves; i++) {
+      const bool isA = i * G::kWaves < kA;  // (of all waves)
       const int b = wave + i * G::kWaves;
-      if ((i + 1) * G::kWaves <= G::kCodeLoads || b < G::kCodeLoads) {
-        const bool isA = b < kA;
-        const int row = (isA ? b : b - kA) * G::kRpb + lane / G::kCpr;
-        const uint32_t kb = (uint32_t)s * G::kRow + (uint32_t)((lane % G::kCpr) ^ swz<FP8>(row)) * 16u;
-        const uint32_t off = kb < rowbytes ? (uint32_t)row * rowbytes + kb : kOOB;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rA : rB, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
-        continue;
-      }
-      const int q = b - G::kCodeLoads;  // scale load
-      const bool real = in && q < G::kScaleLoads;
+      const int row = (isA ? b : b - kA) * kRpb + lane / kCpr;
+      const uint32_t kb = (uint32_t)s * kRow + (uint32_t)((lane % kCpr) ^ swz(row)) * 16u;
+      const uint32_t off = kb < rowbytes ? (uint32_t)row * rowbytes + kb : kOOB;
+      if (isA)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < G::kLoads - G::kCodeLoads / G::kWaves; i++) {
+      const int q = wave + i * G::kWaves;
+      const bool real = s < nk && q < G::kScaleLoads;
       uint8_t* dst = real ? stage + G::kOffS + q * 256 : smem + G::kDummy;
       if (FP8) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rSA, (lds_ptr_t)dst, 4, (uint32_t)(q * 64 + lane) * sstride,
                                                  real ? 4 * s : (int)kOOB, 0, 0);
       } else {
-        const int grp = q % G::kScaleGroups, j = q / G::kScaleGroups;  // j: the step's block (not ALIGNED)
+        const int grp = q % G::kScaleGroups, at = 8 * s + q / G::kScaleGroups * (G::kAligned ? 4 : 1);
         const bool isA = grp < G::kScaleA;
         const uint32_t off = (uint32_t)((isA ? grp : grp - G::kScaleA) * 64 + lane) * sstride;
-        const uint32_t so = real && 4 * s + j < kblocks ? (uint32_t)(4 * s + j) : kOOB;
+        const int so = real && at < kblocks ? at : (int)kOOB;
         if (G::kAligned)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rSA : rSB, (lds_ptr_t)dst, 4, off, (int)so, 0, 0);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rSA : rSB, (lds_ptr_t)dst, 4, off, so, 0, 0);
         else
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rSA : rSB, (lds_ptr_t)dst, 1, off, (int)so, 0, 0);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(isA ? rSA : rSB, (lds_ptr_t)dst, 1, off, so, 0, 0);
       }
     }
   };
@@ -189,8 +189,8 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
       // A lane's 32 bytes of the step: chunks g and g + 4 of its row (any
       // order of K is right, if A's and B's are the same).
       auto frag = [&](const uint8_t* rows, int row) {
-        const i32x4 lo = *(const i32x4*)(rows + row * 128 + ((g ^ swz<true>(row)) * 16));
-        const i32x4 hi = *(const i32x4*)(rows + row * 128 + (((g + 4) ^ swz<true>(row)) * 16));
+        const i32x4 lo = *(const i32x4*)(rows + row * 128 + ((g ^ swz(row)) * 16));
+        const i32x4 hi = *(const i32x4*)(rows + row * 128 + (((g + 4) ^ swz(row)) * 16));
         return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       };
       i32x8 bf[G::TNW];
@@ -236,34 +236,38 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
         }
       }
     } else {
-      // Lane (r, g) supplies K block g of its row and that block's scale.
-      auto frag = [&](const uint8_t* rows, int row) {
-        const i32x4 v = *(const i32x4*)(rows + row * 64 + ((g ^ swz<false>(row)) * 16));
-        return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-      };
-      auto scale = [&](int at) {  // at: row of A, or 64 kScaleA + row of B
-        return (int)cur[G::kOffS + (G::kAligned ? at * 4 + g : (g * (64 * G::kScaleGroups) + at) * 4)];
-      };
-      i32x8 bf[G::TNW];
-      int sbb[G::TNW];
+      // Of 128 K h, lane (r, g) supplies block g of its row and that block's scale.
 #pragma unroll
-      for (int j = 0; j < G::TNW; j++) {
-        const int row = wn * 16 * G::TNW + j * 16 + r;
-        bf[j] = frag(cur + G::kOffB, row);
-        sbb[j] = scale(64 * G::kScaleA + row);
-      }
+      for (int h = 0; h < 2; h++) {
+        auto frag = [&](const uint8_t* rows, int row) {
+          const i32x4 v = *(const i32x4*)(rows + row * 128 + (((4 * h + g) ^ swz(row)) * 16));
+          return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+        };
+        auto scale = [&](int at) {  // at: row of A, or 64 kScaleA + row of B
+          constexpr int kPart = 64 * G::kScaleGroups;
+          return (int)cur[G::kOffS + (G::kAligned ? (h * kPart + at) * 4 + g : ((4 * h + g) * kPart + at) * 4)];
+        };
+        i32x8 bf[G::TNW];
+        int sbb[G::TNW];
 #pragma unroll
-      for (int i = 0; i < G::TMW; i++) {
-        const int row = wm * 16 * G::TMW + i * 16 + r;
-        const i32x8 af = frag(cur, row);
-        const int sa = scale(row);
+        for (int j = 0; j < G::TNW; j++) {
+          const int row = wn * 16 * G::TNW + j * 16 + r;
+          bf[j] = frag(cur + G::kOffB, row);
+          sbb[j] = scale(64 * G::kScaleA + row);
+        }
 #pragma unroll
-        for (int j = 0; j < G::TNW; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, acc[i][j], 4, 4, 0, sbb[j], 0, sa);
+        for (int i = 0; i < G::TMW; i++) {
+          const int row = wm * 16 * G::TMW + i * 16 + r;
+          const i32x8 af = frag(cur, row);
+          const int sa = scale(row);
+#pragma unroll
+          for (int j = 0; j < G::TNW; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, acc[i][j], 4, 4, 0, sbb[j], 0, sa);
+        }
       }
     }
     if constexpr (OUT == kOutF32) {
-      if ((s + 1) % kSegSteps == 0 && s + 1 < nk) {
+      if ((s + 1) % kSeg == 0 && s + 1 < nk) {
 #pragma unroll
         for (int i = 0; i < G::TMW; i++)
 #pragma unroll
@@ -284,7 +288,7 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
     for (int j = 0; j < G::TNW; j++) {
       const int col = n0 + wn * 16 * G::TNW + j * 16 + 4 * g;
       f32x4 v = acc[i][j];
-      if (OUT == kOutF32) v = nk > kSegSteps ? v + tot[i][j] : v;
+      if (OUT == kOutF32) v = nk > kSeg ? v + tot[i][j] : v;
       const int64_t at = (int64_t)(t.row + lrow) * p.ldc + col;
       if (vec_ok && col + 4 <= p.N) {
         if (OUT == kOutF32)
@@ -324,16 +328,17 @@ hipError_t launch(const Args& a, hipStream_t s) {
                        G::kThreads, 0, s, p);
 }
 
-// The tile: a CU takes its operands at 35-45 bytes a ns whatever the tile, so
-// while tiles are fewer than CUs, smaller ones, spread over more CUs, are faster;
-// with enough tiles larger ones are, which read less for their outputs. Times
-// in us of 32 / 64 / 128 square tiles, M x N x K:
-//   fp8, bf16 result: 17 x 28672 x 4096 34 / 27 / 31, 32 x 14336 x 4096 12.4 / 15.0 / 28,
-//   64 x 14336 x 4096 22 / 15 / 29, 128 x 4096 x 4096 11.8 / 14.8 / 29, 128 x 28672 x
-//   4096 - / 54 / 37, 256 x 14336 x 4096 - / 35 / 31, 1500 x 8192 x 4096 - / 100 / 87,
-//   800 rows over 8 x 2048 x 4096 - / 22 / 31;
-//   mxfp4: 800 rows over 8 x 2048 x 4096 - / 28 / 22, 1920 over 64 x 2048 x 4096 - / 108 / 80,
-//   3000 over 4 x 600 x 992 - / 7.6 / 10.3.
+// The tile. While tiles are fewer than CUs, smaller ones, spread over more CUs, are
+// faster; with enough tiles larger ones are, which read less for their outputs.
+// Three stages are enough, more only keep workgroups from sharing a CU (64 x 64, 4 waves, fp8
+// 1500 x 2048 x 4096: 27.5 us with three, 30.8 with four, 43.8 with eight).
+// Times in us of 32 / 64 / 64 x 128 / 128 tiles, M x N x K:
+//   fp8, bf16 result: 32 x 14336 x 4096 12 / 15 / - / 28, 128 x 8192 x 4096 - / 13.8 / 17.8 / 25,
+//   777 x 2048 x 4096 - / 19.0 / 17.7 / -, 1500 x 1000 x 2432 - / 12.8 / 11.8 / -,
+//   128 x 28672 x 4096 - / 54 / 43 / 34, 800 rows over 8 x 2048 x 4096 - / 21 / 19.2 / 31;
+//   1000 over 64 x 2048 x 4096 - / - / 123 / 133, 4000 163 / 165;
+//   mxfp4: 1500 over 5 x 1000 x 2816 - / 12.6 / 9.7 / -, 800 over 8 x 2048 x 4096 - / 28 / 25.6 / 19.3,
+//   1920 over 64 x 2048 x 4096 - / 108 / 94 / 76.
 template <int FMT, bool EXACT, int OUT, bool ALIGNED>
 hipError_t by_tile(const Args& p, hipStream_t s) {
   if ((p.offsets || p.M > 48) && tiles(p, 128, 128) >= (FMT == kMXFP4 ? 150 : 200)) {
@@ -347,12 +352,41 @@ hipError_t by_tile(const Args& p, hipStream_t s) {
       if (7 * rounds(tiles(p, 256, 128)) < 4 * rounds(tiles(p, 128, 128)))
         return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 4, 2, 3, ALIGNED>>(p, s);
       return launch<FMT, EXACT, OUT, Geo<FMT, 4, 2, 2, 4, 3, ALIGNED>>(p, s);
+    } else if constexpr (FMT == kMXFP4) {
+      // Few rows an expert: weights from HBM, and two workgroups a CU are faster
+      // (600 rows over 64 x 2048 x 4096: 63 us, 72 with three stages; 4000: 102 and 98).
+      if (rows_each(p) <= 32) return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 2, ALIGNED>>(p, s);
+      return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 3, ALIGNED>>(p, s);
     } else {
-      return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 4, ALIGNED>>(p, s);
+      if (!p.offsets) return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 3, ALIGNED>>(p, s);
+      return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 4, 3, ALIGNED>>(p, s);
     }
   }
-  if (tiles(p, 64, 64) >= (p.M > 32 ? 200 : 300)) return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 2, 4, ALIGNED>>(p, s);
-  return launch<FMT, EXACT, OUT, Geo<FMT, 1, 1, 2, 2, 6, ALIGNED>>(p, s);
+  if (tiles(p, 64, 64) >= (p.M > 32 ? 200 : 300)) {
+    if constexpr (EXACT) {
+      // (777 x 2000 x 2432: 17.9 us; 64 x 128 with 8 waves 18.3, 64 x 64 with 8 20.9.)
+      return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 2, 3, ALIGNED>>(p, s);
+    } else {
+      // More than one tile of 64 x 64 a CU: 64 x 128. (Both of 8 waves: one
+      // round, 777 x 1000 x 2432 fp8, 9.0 us, with 4 waves 9.7.)
+      if (tiles(p, 64, 64) > 256) return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 4, 3, ALIGNED>>(p, s);
+      return launch<FMT, EXACT, OUT, Geo<FMT, 2, 1, 2, 4, 3, ALIGNED>>(p, s);
+    }
+  }
+  return launch<FMT, EXACT, OUT, Geo<FMT, 1, 1, 2, 2, 4, ALIGNED>>(p, s);
+}
+
+// Few rows of A: a stream of weights, which needs long rows of them. Times in us of that
+// kernel / the tiles:
+//   dense: 16 x 2048 x 2048 fp8 4.6 / 6.2, 16 x 4096 x 4096 7.4 / 10, 16 x 4096 x 1024
+//   3.9 / 4.4, but 16 x 14336 x 1024 7.7 / 5.4;
+//   by expert, rows over experts x N x K: fp8 704 over 64 x 2048 x 4096 107 / 116, 896 132 / 118;
+//   80 over 16 x 2048 x 2048 14.2 / 14.5, 128 15.7 / 14.2; mxfp4 320 over 64 x 2048 x 4096 55 / 60,
+//   512 64 / 61; fp8 32 over 64 x 2048 x 1024 13.5 / 10.9, mxfp4 14.7 / 8.3.
+bool few_rows(const Args& p, int fmt) {
+  const int64_t steps = (fmt == kMXFP4 ? p.K / 2 : p.K) / 128;  // lines of a row
+  if (!p.offsets) return p.M <= 16 && (steps >= 16 || p.N <= 8192);
+  return p.M <= (steps >= 32 ? 12 : steps >= 16 ? 6 : 0) * (int64_t)p.groups;
 }
 
 }  // namespace
@@ -372,10 +406,7 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
   const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
   const bool f32 = out_dtype == kOutF32;
-  // Few rows of A: a stream of weights. (16 rows against 4096 x 4096 fp8 7.4 us,
-  // 32 x 32 tiles 10; 512 rows over 64 x 2048 x 4096 mxfp4 65, tiles 79; 1024
-  // rows 106 and 92.)
-  if ((offsets ? M <= 8 * groups : M <= 16) && gemm_few_rows_fits(N, K, out_dtype))
+  if (few_rows(p, fmt) && gemm_few_rows_fits(N, K, out_dtype))
     return gemm_few_rows(fmt, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
   // Tiles of 256 x 256, for almost half of the CUs or more, where most are more than half full.
   // (Times of 256 / the best of the smaller tiles: fp8 1500 x 8192 x 4096 (192 tiles)

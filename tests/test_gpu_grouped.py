@@ -67,6 +67,11 @@ CASES = [  # sizes of the groups, N, K
     ([0, 2, 1] * 50, 33, 128),
     ([700], 260, 2048),
     # few rows per expert on average, more than 16 in one: further passes over its weight
+    ([0, 40, 1, 0, 0, 0, 17, 0, 3, 0, 0, 0], 200, 4096),
+    ([1] * 12 + [60] + [0] * 30, 2100, 2048),
+    ([0, 3, 0, 0, 30, 0, 1, 0, 0], 330, 8192),
+    ([2, 0, 20, 0], 100, 4480),
+    # the same with short rows of weights: tiles
     ([0, 40, 1, 0, 0, 0, 17, 0, 3, 0], 200, 1024),
     ([1] * 12 + [60] + [0] * 30, 2100, 512),
     # enough for tiles of 64, of 128 and of 256 square
@@ -89,7 +94,20 @@ def test_grouped(sizes, N, K, fmt, out):
 
 
 @pytest.mark.parametrize("out", [F32, BF16])
-@pytest.mark.parametrize("K", [32, 64, 96, 160, 224, 736, 1056, 2880])
+@pytest.mark.parametrize("sizes,N,K", [([20, 31, 0, 9] * 6, 1400, 384), ([20, 31, 0, 9] * 6, 1400, 416),
+                                       ([100, 200], 6500, 640), ([100, 200], 6500, 32), ([40] * 5, 3400, 640),
+                                       ([40] * 5, 3400, 672), ([350, 0, 90], 1790, 384), ([350, 0, 90], 1790, 288)])
+def test_mxfp4_tiles(sizes, N, K, out):
+    """MXFP4's steps of 256 K with an odd half at the end, on each tile: 128 square with
+    few and with many rows an expert, 64 x 128 and 64 square."""
+    require_gpu()
+    a, b = _operands("mxfp4", sum(sizes), len(sizes), N, K, N)
+    off, d = _offsets(sizes)
+    _check(mx.gemm_grouped(a, b, d, out), a, b, off, "mxfp4", out)
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("K", [32, 64, 96, 160, 224, 288, 384, 736, 1056, 2880, 4128, 4256, 4480])
 @pytest.mark.parametrize("sizes", [[2, 0, 3], [1, 18, 0, 0], [70, 150, 1], [300, 250, 600]])
 def test_mxfp4_odd_k(K, sizes, out):
     """K that is no multiple of a step. Then every second row's first scale is made
