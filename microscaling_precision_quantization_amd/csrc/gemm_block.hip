@@ -43,6 +43,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
 constexpr uint32_t kOOB = 0x80000000u;        // an offset past every buffer's range
+constexpr int kNonTemporal = 2;               // cache policy of a load: streamed
 constexpr int kChain = 48;                    // MFMAs per accumulation chain (fp32 results)
 constexpr int kRow = 128, kCpr = kRow / 16;   // LDS bytes and chunks of a row's K step
 constexpr int kRpb = 64 / kCpr;               // rows per 1 KB load of a wave
@@ -50,10 +51,12 @@ constexpr int kRpb = 64 / kCpr;               // rows per 1 KB load of a wave
 // Tile geometry: waves of 16 TMW x 16 TNW, WM x WN of them; NS stages. ALIGNED: a
 // row's MXFP4 scales start on dwords (K % 128 = 0), so that a step's eight are
 // two loads; otherwise they are eight loads of a byte, which LDS holds as a dword.
-template <int FMT, int TMW_, int TNW_, int WM_, int WN_, int NS_, bool ALIGNED_ = true>
+// STREAM_B: B's loads are non-temporal.
+template <int FMT, int TMW_, int TNW_, int WM_, int WN_, int NS_, bool ALIGNED_ = true, bool STREAM_B_ = false>
 struct Geo {
   static constexpr int TMW = TMW_, TNW = TNW_, WM = WM_, WN = WN_, NS = NS_;
   static constexpr bool kAligned = ALIGNED_;
+  static constexpr bool kStreamB = STREAM_B_;
   static constexpr int BM = 16 * TMW * WM, BN = 16 * TNW * WN;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr bool kFp8 = FMT == kFP8B128;
@@ -138,6 +141,8 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
       const uint32_t off = kb < rowbytes ? (uint32_t)row * rowbytes + kb : kOOB;
       if (isA)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
+      else if (G::kStreamB)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, kNonTemporal);
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(stage + b * 1024), 16, off, 0, 0, 0);
     }
@@ -359,6 +364,9 @@ hipError_t by_tile(const Args& p, hipStream_t s) {
       return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 3, ALIGNED>>(p, s);
     } else {
       if (!p.offsets) return launch<FMT, EXACT, OUT, Geo<FMT, 4, 4, 2, 2, 3, ALIGNED>>(p, s);
+      // Few rows an expert: a weight is read once, so non-temporally (208 rows over
+      // 16 x 4096 x 4096: 58 us, 90 without; 1000 over 64 x 2048 x 4096 109 and 118; 4000 166 and 157).
+      if (rows_each(p) <= 32) return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 4, 3, ALIGNED, true>>(p, s);
       return launch<FMT, EXACT, OUT, Geo<FMT, 2, 2, 2, 4, 3, ALIGNED>>(p, s);
     }
   }

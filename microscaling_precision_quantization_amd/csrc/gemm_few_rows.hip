@@ -8,14 +8,14 @@
 //  * A workgroup takes T tiles of 16 weight rows of one expert. K goes to its
 //    waves in chunks of W S steps of 128 bytes (128 K of FP8, 256 K of
 //    MXFP4), S consecutive steps each. A wave keeps A's fragments (and scales) of
-//    its S steps in VGPRs and runs tile by tile: its loads are 16 rows x 128 S
+//    its S steps in VGPRs and runs tile by tile: the waves' loads are 16 rows x 128 W S
 //    contiguous bytes, which keeps DRAM pages open, and A's cost is shared
 //    by T tiles. The waves' sums meet in LDS at the end, in a fixed order.
 //  * Weights go HBM -> LDS directly, whole 128-byte lines, 8 rows a load, into a
 //    ring of D steps of the wave's own: no barrier, D - 1 steps in flight, and no
-//    VGPRs for them. The loads are non-temporal (38 us instead of 43). (Loading fragments, 64 bytes of 16 rows a load, into VGPRs
-//    reached 4.5-5.2 TB/s at 16 x 28672 x 8192; this does 6.1.) The chunk swizzle of
-//    LDS rows is gemm_block.hip's.
+//    VGPRs for them. The loads are non-temporal (38 us instead of 43). (Loading
+//    fragments, 64 bytes of 16 rows a load, into VGPRs reached 4.5-5.2 TB/s at
+//    16 x 28672 x 8192; this does 6.2.) The chunk swizzle of LDS rows is gemm_block.hip's.
 //  * In a step lane (r, g) = (l % 16, l / 16) takes chunks g and g + 4 of row r of
 //    the tile; the same order of K in A.
 //  * Loads are range-checked buffer loads without a branch: rows past the
@@ -298,25 +298,33 @@ hipError_t launch(const Args& p, int64_t groups, hipStream_t s) {
 }
 
 // Experts that have rows are taken as min(groups, M). Times in us at 16 rows,
-// FP8, N x K (by expert: experts used x N x K).
+// FP8, N x K (by expert: rows over experts x N x K).
 template <bool FP8, bool EXACT, bool ALIGNED, int OUT>
 hipError_t dispatch(const Args& p, int64_t groups, hipStream_t s) {
   if constexpr (FP8) {
     const int64_t tiles = (p.N + 15) / 16 * (p.offsets && p.M < groups ? p.M : groups);
     const int nk = p.K / 128;
-    // Long rows, many of them: one workgroup of 8 waves a CU and 7 tiles
-    // share A (28672 x 8192: 38.2, T = 4 41.3, T = 2 53.5).
-    if (nk >= 48 && p.N >= 7 * 16 * 32 && tiles >= 7 * 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
-    // Dense, enough tiles for every CU (14336 x 4096: 14.3, T = 2 15.1, T = 1
-    // 20.1). By expert, fewer tiles spread better (8 x 2048 x 4096: T = 2
-    // 12.2, T = 4 16.3).
-    if (!p.offsets && nk > 16 && tiles >= 640) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 4, 9>(p, groups, s);
-    if (nk > 16 && tiles >= 512) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
+    if (p.offsets) {
+      // Few experts with rows: 4 waves on long runs (8 rows over 32 x 2048 x 4096: 12.0,
+      // below 14.7; 128 over 64: 60.2 and 59.2, 32 over 16 x 4096 x 7168: 79 and 65).
+      if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
+    } else {
+      // Long rows, many of them: one workgroup of 8 waves a CU and 7 tiles
+      // share A (28672 x 8192: 38.0, T = 4 41).
+      if (nk >= 48 && tiles >= 7 * 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
+      // The fewest tiles a workgroup that need one round of CUs (T = 1 / 2 / 3:
+      // 4096 x 4096 6.6 / 7.3 / 8.7, 6144 x 4096 9.7 / 7.6 / 9.2, 10240 x 8192 - / 24.9 / 16.8;
+      // 14336 x 4096: 13.6, with T = 2 13.9, T = 3 16.5).
+      if (tiles <= 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 2, 1, 3>(p, groups, s);
+      // (8192 x 28672: 4 waves on long runs 44.4, T = 2 46.5; one row 37.2 and 41.5.)
+      if (tiles <= 512 && nk >= 128) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
+      if (tiles > 512 && tiles <= 768) return launch<FP8, EXACT, ALIGNED, OUT, 8, 1, 3, 4>(p, groups, s);
+      if (tiles > 768 && nk > 16) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 4, 9>(p, groups, s);
+    }
   }
-  // Few tiles or short rows (4096 x 4096: 7.4, T = 2 7.9; 4096 x 14336: 15.6 and
-  // 21.7; 8192 x 1024: 5.2 and 6.0), and MXFP4, whose rows are half as long
-  // (32 x 2048 x 2048: 14.8, T = 2 20.9, S = 8 30.6).
-  return launch<FP8, EXACT, ALIGNED, OUT, 4, 4, 1, 5>(p, groups, s);
+  // Two tiles, a step of each in a wave's chunk: eight waves on one run of a row
+  // (mxfp4 128 over 64 x 2048 x 4096: 35.4, with 4 waves on runs of 4 steps 42.9, four tiles 37.7).
+  return launch<FP8, EXACT, ALIGNED, OUT, 8, 1, 2, 3>(p, groups, s);
 }
 
 template <bool ALIGNED>

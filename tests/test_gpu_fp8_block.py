@@ -167,7 +167,7 @@ def check(got, c, s, out):
 # of 32, 64, 128 and 256 square, each with ragged edges in M and N.
 SHAPES = [(1, 1, 128), (1, 4096, 1024), (2, 17, 256), (7, 130, 640), (16, 512, 4096),
           (3, 8200, 2304), (5, 10300, 2176), (9, 29000, 6400), (16, 300, 14336),
-          (9, 8300, 1024), (17, 129, 384), (33, 255, 1152), (700, 2100, 384), (64, 64, 128), (100, 1000, 2432), (129, 257, 512),
+          (9, 8300, 1024), (16, 6000, 2176), (11, 10100, 3200), (2, 16000, 2432), (3, 4200, 16512), (17, 129, 384), (33, 255, 1152), (700, 2100, 384), (64, 64, 128), (100, 1000, 2432), (129, 257, 512),
           (300, 513, 1024), (40, 13000, 256), (500, 1900, 640), (1000, 3300, 512), (130, 14300, 256),
           (1300, 5000, 384), (1290, 5100, 128), (2100, 2050, 640), (4000, 1500, 256)]
 

@@ -71,6 +71,8 @@ CASES = [  # sizes of the groups, N, K
     ([1] * 12 + [60] + [0] * 30, 2100, 2048),
     ([0, 3, 0, 0, 30, 0, 1, 0, 0], 330, 8192),
     ([2, 0, 20, 0], 100, 4480),
+    ([1, 0, 2, 0, 0, 17, 0, 1], 2100, 4224),
+    ([1, 3] * 10, 1800, 4224),
     # the same with short rows of weights: tiles
     ([0, 40, 1, 0, 0, 0, 17, 0, 3, 0], 200, 1024),
     ([1] * 12 + [60] + [0] * 30, 2100, 512),
