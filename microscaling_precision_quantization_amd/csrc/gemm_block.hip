@@ -416,13 +416,14 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
   const bool f32 = out_dtype == kOutF32;
   if (few_rows(p, fmt) && gemm_few_rows_fits(N, K, out_dtype))
     return gemm_few_rows(fmt, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
-  // Tiles of 256 x 256, for almost half of the CUs or more, where most are more than half full.
+  // Tiles of 256 x 256, for a third of the CUs or more, where most are more than half full.
   // (Times of 256 / the best of the smaller tiles: fp8 1500 x 8192 x 4096 (192 tiles)
-  // 53 / 87, 777 x 8192 x 4096 (128) 44 / 58, 256 x 28672 x 4096 (112) 60 / 63, 300 x
-  // 8192 x 4096 (64) 43 / 30, 128 x 28672 x 4096 (112, half full) 54 / 37; mxfp4 2400 rows
-  // over 16 x 2048 x 2048 (139) 20 / 22, 800 over 8 x 2048 x 4096 (57) 28 / 22; fp8 1600
-  // rows over 16 x 2048 x 2048 25 / 35.)
-  const bool large = rows_each(p) > (offsets ? 64 : 128) && tiles(p, 256, 256) >= 110;
+  // 50 / 83, 777 x 8192 x 4096 (128) 44 / 55, 256 x 28672 x 4096 (112) 61 / 59, 1500 x 4096 x
+  // 4096 (96) 44 / 55, 300 x 8192 x 4096 (64) 43 / 26, 128 x 28672 x 4096 (112, half full) 54 / 34;
+  // fp8 1600 rows over 16 x 2048 x 2048 (112) 25 / 27, 2000 over 8 x 2048 x 4096 (88) 45 / 42;
+  // mxfp4 2400 over 16 x 2048 x 2048 (136) 18 / 23, 2000 over 8 x 2048 x 4096 (88) 28 / 34,
+  // 800 over 8 (56) 28 / 19.)
+  const bool large = rows_each(p) > (offsets ? 64 : 128) && tiles(p, 256, 256) >= (fmt == kMXFP4 ? 80 : 90);
   if (fmt == kMXFP4) {
     if (large && gemm_mxfp4_fits(0, N, K))
       return gemm_mxfp4_grouped(M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
