@@ -379,7 +379,7 @@ mx_status mx_gemm_noalloc(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   rows; b_scales: MXFP4 [groups][N][K/32], FP8_B128X128
  *   [groups][ceil(N/128)][K/128] (each weight quantized by itself).
  * c: [M][ldc] fp32 or bf16. Limits: M, N <= 2^30, K <= 2^22, groups <= 65535,
- * M K and groups N K <= 2^40, and (M / 128 + min(groups, M)) * N / 128 tiles
+ * M K and groups N K <= 2^40, and (M / 64 + min(groups, M)) * N / 128 tiles
  * below 2^23. No workspace. Accuracy as mx_gemm's for the pair.
  */
 mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, int64_t groups,

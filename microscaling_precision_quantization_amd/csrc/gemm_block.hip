@@ -400,11 +400,11 @@ bool few_rows(const Args& p, int fmt) {
 }  // namespace
 
 // Whether the kernels' 32-bit offsets hold (256 rows of codes and of scales)
-// and the grid its 2^32 threads: 128 x 128 tiles of 512; smaller tiles are for
-// few, or for at most 48 rows, where 64 x 64 ones of 256 are twice as many.
+// and the grid its 2^32 threads: tiles of 128 x 128 or, by expert and for at most
+// 48 rows, 64 x 128 of 512 (64 x 64 of 256 for fp32 results; smaller ones are for few).
 bool gemm_block_fits(int64_t M, int64_t N, int64_t K, int64_t groups) {
   if (K > ((int64_t)1 << 22)) return false;
-  const int64_t tm = groups > 0 ? groups::max_row_tiles(M, groups, 128) : (M + 127) / 128;
+  const int64_t tm = groups > 0 ? groups::max_row_tiles(M, groups, 64) : (M + 127) / 128;
   return groups::grid_size(tm, (N + 127) / 128) < ((int64_t)1 << 23);
 }
 

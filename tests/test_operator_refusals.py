@@ -55,6 +55,7 @@ def test_fp8_gemm(kw, status):
     (dict(sb=None), INV), (dict(c=P4), INV), (dict(ldc=63), INV),
     (dict(M=1 << 30, N=1 << 30, ldc=1 << 30), INV),
     (dict(groups=65535, M=1 << 20, N=16384, ldc=16384, fa=A8, fb=B8, block=128), INV),  # mostly partly filled tiles
+    (dict(groups=65535, M=1 << 21, N=12800, ldc=12800, fa=A8, fb=B8, block=128), INV),  # of 64 x 128
 ])
 def test_grouped(kw, status):
     a = dict(fa=1, fb=1, block=32, rnd=0, groups=3, M=64, N=64, K=256, off=P4, a=P, sa=P, b=P, sb=P, od=0, c=P2, ldc=64)
