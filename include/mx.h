@@ -117,9 +117,9 @@ typedef enum {
  *     code. Non-finite T: s_t = NaN, every block scale 0x7F (E4M3 NaN),
  *     every code 0.
  *   FP8_B128, FP8_B128X128 (block 128): per 1 x 128 elements or 128 x 128 tile
- *     s = fl32(amax / 448) (1 if amax = 0), code = the E4M3 value nearest the
- *     exact quotient x / s, ties to the even code, the sign copied. A block
- *     holding Inf/NaN gets s = NaN and zero codes.
+ *     s = fl32(amax / 448) (1 if that is 0), code = the E4M3 value nearest the
+ *     exact quotient x / s, ties to the even code, saturating, the sign
+ *     copied. A block holding Inf/NaN gets s = NaN and zero codes.
  * x: bf16 [rows][cols]; codes, scales: outputs as in the layout above.
  * tensor_scale: NVFP4 only, one device fp32 written with s_t; NULL otherwise.
  * workspace: NVFP4 only, device scratch of at least

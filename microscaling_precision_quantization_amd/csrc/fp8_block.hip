@@ -4,8 +4,9 @@
 //   s    = fl32(amax / 448), 1 where amax = 0, NaN where an element is not finite
 //   code = the E4M3 value nearest the exact quotient x / s, ties to the even
 //          code, the sign copied; 0 under a NaN scale.
-// The quotient never reaches 464, where E4M3 would overflow: s is within
-// half an fp32 step of amax / 448, at worst 2^-8 of it among the subnormals.
+// The quotient of a bf16 x never reaches 464, where E4M3 would overflow: s is within
+// half an fp32 step of amax / 448, at worst 2^-8 of it among the subnormals. (The
+// fp32 values of norm_quantize.hip can be smaller than any bf16: fp8_encode.h.)
 //
 // Deciding the code without a division per element: x' rcp(s') is within 2^-21 of
 // the quotient (x' and s' are scaled by 2^64 when s < 2^-60, so that neither the

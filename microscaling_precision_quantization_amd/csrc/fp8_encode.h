@@ -23,7 +23,8 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 
 // A block's scale: the stored value, and what encode8 works with: the scale
 // times `lift` (2^64 for s < 2^-60, else 1), and its reciprocal a little
-// lowered and raised.
+// lowered and raised. An amax whose quotient rounds to 0 (up to 1.75 * 2^-142) is
+// stored under 1, as 0 is: its codes are zeros.
 struct Scale {
   float value, lifted, lift, down, up;
   bool finite;
@@ -33,7 +34,7 @@ __device__ __forceinline__ Scale scale_of(float amax) {
   Scale s;
   s.finite = __builtin_bit_cast(uint32_t, amax) < 0x7F800000u;
   float v = amax / 448.0f;
-  if (amax == 0.0f) v = 1.0f;
+  if (v == 0.0f) v = 1.0f;
   s.value = s.finite ? v : __builtin_nanf("");
   s.lift = v < 0x1p-60f ? 0x1p64f : 1.0f;
   s.lifted = v * s.lift;
@@ -71,8 +72,11 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], const Scale& s) {
 #pragma unroll
   for (int i = 0; i < 8; i++) y[i] = x[i];
   if (s.lift != 1.0f) {
+    // Among the fp32 subnormals a scale can be so coarse that quotients pass 464,
+    // where the conversion would give NaN: saturate.
+    const float most = 448.0f * s.lifted;
 #pragma unroll
-    for (int i = 0; i < 8; i++) y[i] *= s.lift;
+    for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(y[i] * s.lift, -most, most);
   }
   uint32_t lo[2], hi[2];
 #pragma unroll

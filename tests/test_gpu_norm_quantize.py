@@ -238,3 +238,54 @@ def test_expert_layer(tokens, kind):
         assert np.all(np.abs(_v(up) - c) <= 2.0**-18 * s * (1 + 2.0**-8) + 2.0**-8 * np.abs(c))
     w2v = ref.fp8_values(host(w2.codes), host(w2.scales), True) if kind == "fp8" else ref.mxfp4_values(host(w2.codes), host(w2.scales))
     check_fp8_gemm(down, *ref.product(val(qu), w2v), F32)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8", "fp8_b128"])
+@pytest.mark.parametrize("power", [-18, -4])
+@pytest.mark.parametrize("beside", [False, True])
+def test_blocks_of_subnormals(fmt, power, beside):
+    """Blocks of n from one fp32 subnormal step (2^-149) up, alone and beside a block of
+    normal size: an FP8 scale that would be zero is 1, under one too coarse (few steps of
+    2^-149) codes saturate, and nothing becomes NaN. mean(h^2) + eps is 1 or 4 without error,
+    so n, its codes and scales are exactly known."""
+    require_gpu()
+    r = np.random.RandomState(power + 50)
+    tops, cols = (1, 2, 3, 100, 127, 200, 225, 255), 2048
+    x = np.stack([r.randint(-k, k + 1, cols) * 2.0**-133 for k in tops])
+    x[:, 0::128], x[:, 1::128], x[:, 2::128] = np.array(tops)[:, None] * 2.0**-133, 0.0, -0.0
+    x[:, 3::32] = -x[:, 0:1]  # (every 32-element block has the row's largest)
+    w = np.repeat(2.0 ** (power + np.arange(16)), 128)
+    if beside:
+        x[:, 256:384], w[256:384] = r.choice([-4.0, 4.0], (len(tops), 128)), 1.0
+    x, w = _bf16_exact(x), _bf16_exact(w)
+    q, _ = mx.norm_quantize(x.cuda(), w.cuda(), fmt, eps=3.0 if beside else 1.0)
+    with np.errstate(under="ignore"):
+        h = np.float32(0) + x.float().numpy()  # (no residual: 0, so that -0 becomes 0)
+        n = (h * w.float().numpy()) * np.float32(0.5 if beside else 1.0)
+    size = 128 if fmt == "fp8_b128" else 32
+    nb = n.astype(np.float64).reshape(len(tops), -1, size)
+    amax = np.abs(nb).max(2)
+    if fmt == "fp8_b128":
+        scales = (amax.astype(np.float32) / np.float32(448)).astype(np.float32)
+        scales = np.where(scales == 0, np.float32(1), scales)
+        s = scales.astype(np.float64)
+        if power == -18:  # both kinds are there
+            assert (amax[(s == 1) & (amax > 0)] > 0).any() and ((amax / s > 464) & (s < 1)).any()
+    else:
+        with np.errstate(divide="ignore"):
+            scales = np.clip(np.ceil(np.log2(amax / (6 if fmt == "mxfp4" else 448))) + 127, 0, 254).astype(np.uint8)
+        s = 2.0 ** (scales.astype(np.float64) - 127)
+    table = ref.E2M1[:8] if fmt == "mxfp4" else ref.E4M3[:127]
+    code, neg = ref.nearest_code(nb / s[..., None], table)
+    want = (code + (8 if fmt == "mxfp4" else 128) * neg).astype(np.uint8).reshape(n.shape)
+    got = host(q.codes)
+    if fmt == "mxfp4":
+        got = np.stack([got & 15, got >> 4], -1).reshape(n.shape)
+    assert np.array_equal(host(q.scales), scales)
+    assert np.array_equal(got, want)
+
+
+def _bf16_exact(v):
+    t = torch.from_numpy(v.astype(np.float32)).to(BF16)
+    assert np.array_equal(_v(t), v)
+    return t
