@@ -1,7 +1,6 @@
 // Block-scaled GEMM C = A B^T for few rows of A (decode), dense or by expert:
 // MXFP4 x MXFP4, and FP8 x FP8 under fp32 scales per 1 x 128 of A and 128 x 128
-// of B. (The mathematics and the choice between the FP8 and the bf16 MFMA are
-// gemm_block.hip's.)
+// of B. (The mathematics is gemm_block.hip's.)
 //
 // Bound by HBM: every weight byte is read once and meets 16 rows of A, so
 // the kernel is a stream of weights from HBM through VGPRs to the matrix core.
@@ -20,6 +19,10 @@
 //    the tile; the same order of K in A.
 //  * Loads are range-checked buffer loads without a branch: rows past the
 //    group's or N, steps past K and 32-element blocks past K read as zeros.
+//  * FP8 codes meet in bf16 MFMAs, expanded exactly, for either result: the matrix core and
+//    the vector ALU wait for HBM, and the FP8 MFMA, which loses bits of a sum, would
+//    gain nothing (16 rows, FP8 MFMA / bf16: 28672 x 8192 37.8 / 37.8 us, 4096 x 4096
+//    6.8 / 6.9, 8192 x 28672 44.0 / 44.5; 128 rows over 64 x 2048 x 4096 73.4 / 73.9).
 //  * A group with more than 16 rows takes further passes over the weights.
 #include <type_traits>
 #include <utility>
@@ -75,7 +78,7 @@ __device__ __forceinline__ void unroll(F&& f) {
 
 // ALIGNED: a row's MXFP4 scales start on dwords (K % 128 = 0).
 // W: waves.
-template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int S, int T, int D>
+template <bool FP8, bool ALIGNED, int OUT, int W, int S, int T, int D>
 __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   constexpr int kWaves = W;
   constexpr int kSlot = 2048, kRing = kWaves * D * kSlot, kSums = kWaves * T * 4 * 64 * 4;
@@ -226,14 +229,10 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
           const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb[t]), s));
           const float f = sa[s] * w;
           f32x4 P = f32x4{0, 0, 0, 0};
-          if (EXACT) {
 #pragma unroll
-            for (int h = 0; h < 4; h++)
-              P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
-                                                          expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
-          } else {
-            P = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, a[s], P, 0, 0, 0, 127, 0, 127);
-          }
+          for (int h = 0; h < 4; h++)
+            P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
+                                                        expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
 #pragma unroll
           for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
         } else {
@@ -291,15 +290,15 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   }
 }
 
-template <bool FP8, bool EXACT, bool ALIGNED, int OUT, int W, int S, int T, int D>
+template <bool FP8, bool ALIGNED, int OUT, int W, int S, int T, int D>
 hipError_t launch(const Args& p, int64_t groups, hipStream_t s) {
   const dim3 grid((unsigned)((p.N + 16 * T - 1) / (16 * T)), (unsigned)groups);
-  return launch_kernel(&gemm_few_rows_kernel<FP8, EXACT, ALIGNED, OUT, W, S, T, D>, grid, 64 * W, 0, s, p);
+  return launch_kernel(&gemm_few_rows_kernel<FP8, ALIGNED, OUT, W, S, T, D>, grid, 64 * W, 0, s, p);
 }
 
 // Experts that have rows are taken as min(groups, M). Times in us at 16 rows,
 // FP8, N x K (by expert: rows over experts x N x K).
-template <bool FP8, bool EXACT, bool ALIGNED, int OUT>
+template <bool FP8, bool ALIGNED, int OUT>
 hipError_t dispatch(const Args& p, int64_t groups, hipStream_t s) {
   if constexpr (FP8) {
     const int64_t tiles = (p.N + 15) / 16 * (p.offsets && p.M < groups ? p.M : groups);
@@ -307,30 +306,30 @@ hipError_t dispatch(const Args& p, int64_t groups, hipStream_t s) {
     if (p.offsets) {
       // Few experts with rows: 4 waves on long runs (8 rows over 32 x 2048 x 4096: 12.0,
       // below 14.7; 128 over 64: 60.2 and 59.2, 32 over 16 x 4096 x 7168: 79 and 65).
-      if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
+      if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
     } else {
       // Long rows, many of them: one workgroup of 8 waves a CU and 7 tiles
       // share A (28672 x 8192: 38.0, T = 4 41).
-      if (nk >= 48 && tiles >= 7 * 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
+      if (nk >= 48 && tiles >= 7 * 256) return launch<FP8, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
       // The fewest tiles a workgroup that need one round of CUs (T = 1 / 2 / 3:
       // 4096 x 4096 6.6 / 7.3 / 8.7, 6144 x 4096 9.7 / 7.6 / 9.2, 10240 x 8192 - / 24.9 / 16.8;
       // 14336 x 4096: 13.6, with T = 2 13.9, T = 3 16.5).
-      if (tiles <= 256) return launch<FP8, EXACT, ALIGNED, OUT, 8, 2, 1, 3>(p, groups, s);
+      if (tiles <= 256) return launch<FP8, ALIGNED, OUT, 8, 2, 1, 3>(p, groups, s);
       // (8192 x 28672: 4 waves on long runs 44.4, T = 2 46.5; one row 37.2 and 41.5.)
-      if (tiles <= 512 && nk >= 128) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
-      if (tiles > 512 && tiles <= 768) return launch<FP8, EXACT, ALIGNED, OUT, 8, 1, 3, 4>(p, groups, s);
-      if (tiles > 768 && nk > 16) return launch<FP8, EXACT, ALIGNED, OUT, 4, 8, 4, 9>(p, groups, s);
+      if (tiles <= 512 && nk >= 128) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
+      if (tiles > 512 && tiles <= 768) return launch<FP8, ALIGNED, OUT, 8, 1, 3, 4>(p, groups, s);
+      if (tiles > 768 && nk > 16) return launch<FP8, ALIGNED, OUT, 4, 8, 4, 9>(p, groups, s);
     }
   }
   // Two tiles, a step of each in a wave's chunk: eight waves on one run of a row
   // (mxfp4 128 over 64 x 2048 x 4096: 35.4, with 4 waves on runs of 4 steps 42.9, four tiles 37.7).
-  return launch<FP8, EXACT, ALIGNED, OUT, 8, 1, 2, 3>(p, groups, s);
+  return launch<FP8, ALIGNED, OUT, 8, 1, 2, 3>(p, groups, s);
 }
 
 template <bool ALIGNED>
 hipError_t mxfp4(const Args& p, int64_t groups, bool f32, hipStream_t s) {
-  if (f32) return dispatch<false, false, ALIGNED, kOutF32>(p, groups, s);
-  return dispatch<false, false, ALIGNED, kOutBF16>(p, groups, s);
+  if (f32) return dispatch<false, ALIGNED, kOutF32>(p, groups, s);
+  return dispatch<false, ALIGNED, kOutBF16>(p, groups, s);
 }
 
 }  // namespace
@@ -350,7 +349,7 @@ hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a
   const int64_t g = offsets ? groups : 1;
   const bool f32 = out_dtype == kOutF32;
   if (fmt == kMXFP4) return K % 128 == 0 ? mxfp4<true>(p, g, f32, s) : mxfp4<false>(p, g, f32, s);
-  return f32 ? dispatch<true, true, true, kOutF32>(p, g, s) : dispatch<true, false, true, kOutBF16>(p, g, s);
+  return f32 ? dispatch<true, true, kOutF32>(p, g, s) : dispatch<true, true, kOutBF16>(p, g, s);
 }
 
 }  // namespace mx

@@ -250,3 +250,45 @@ def test_gemm_repeats_and_streams():
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o, first)
+
+
+def exact_tolerance(c, s):
+    """A bf16 rounding of a result within 2^-18 sum|ab|."""
+    return 2.0**-18 * s * (1 + 2.0**-8) + 2.0**-8 * np.abs(c)
+
+
+def _cancelling(rows, K, tall, seed):
+    """Codes 448 and, in b, -448 beside it, among values of 2 to 3.75: products of the first
+    cancel, and what is left lies below 2^-13 of them, the last bits of the FP8 MFMA's sum."""
+    r = np.random.RandomState(seed)
+    c = r.randint(0x40, 0x48, (rows, K)).astype(np.uint8) | (r.randint(0, 2, (rows, K)) << 7).astype(np.uint8)
+    c[:, 0::64], c[:, 1::64] = 0x7E, 0xFE if tall else 0x7E
+    s = np.exp2(r.uniform(-8, 8, (-(-rows // 128) if tall else rows, K // 128))).astype(np.float32)
+    return mx.QTensor(mx.FORMATS["fp8_b128x128" if tall else "fp8_b128"], rows, K, dev_u8(c), torch.from_numpy(s).cuda())
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 2048), (16, 200, 1024), (16, 9000, 2176), (9, 10300, 2304), (5, 29000, 6400),
+                                   (16, 300, 16512), (16, 6000, 2176)])
+def test_gemm_few_rows_exact_before_rounding(M, N, K):
+    """Up to 16 rows HBM is the bound and products are summed exactly: 2^-18 sum|ab| before
+    a bf16 rounding, also where most of a sum cancels."""
+    require_gpu()
+    a, b = _cancelling(M, K, False, M), _cancelling(N, K, True, N)
+    c, s = ref.product(_val(a), _val(b))
+    got = host(mx.gemm(a, b, BF16).float()).astype(np.float64)
+    bad = np.abs(got - c) > exact_tolerance(c, s)
+    assert not bad.any(), (bad.mean(), np.argwhere(bad)[:4], got[bad][:4], c[bad][:4])
+
+
+@pytest.mark.parametrize("sizes,N,K", [([3, 0, 17, 1], 300, 4096), ([1] * 8 + [0] * 24, 2048, 4224), ([2, 0, 5], 100, 2048)])
+def test_grouped_few_rows_exact_before_rounding(sizes, N, K):
+    require_gpu()
+    G, M = len(sizes), sum(sizes)
+    a = _cancelling(M, K, False, M)
+    w = [_cancelling(N, K, True, 7 + g) for g in range(G)]
+    b = mx.QTensor(w[0].fmt, G * N, K, torch.cat([x.codes for x in w]), torch.cat([x.scales for x in w]), groups=G)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    c, s = ref.grouped(_val(a), np.stack([_val(x) for x in w]), off)
+    got = host(mx.gemm_grouped(a, b, torch.from_numpy(off).cuda(), BF16).float()).astype(np.float64)
+    bad = np.abs(got - c) > exact_tolerance(c, s)
+    assert not bad.any(), (bad.mean(), np.argwhere(bad)[:4], got[bad][:4], c[bad][:4])
