@@ -292,3 +292,56 @@ def test_grouped_few_rows_exact_before_rounding(sizes, N, K):
     got = host(mx.gemm_grouped(a, b, torch.from_numpy(off).cuda(), BF16).float()).astype(np.float64)
     bad = np.abs(got - c) > exact_tolerance(c, s)
     assert not bad.any(), (bad.mean(), np.argwhere(bad)[:4], got[bad][:4], c[bad][:4])
+
+
+def _uneven(q, seed):
+    """Scales of q's 128-K blocks that differ 2^12-fold from one to the next."""
+    r = np.random.RandomState(seed)
+    f = np.exp2(r.randint(-6, 7, tuple(q.scales.shape))).astype(np.float32)
+    q.scales = q.scales * torch.from_numpy(f).cuda()
+    return q
+
+
+def check_bf16(got, a, b):
+    c, s = ref.product(a, b)
+    bad = np.abs(host(got.float()).astype(np.float64) - c) > ref.fp8_mfma_tolerance(a, b, c, s)
+    assert not bad.any(), (bad.mean(), np.argwhere(bad)[:4], c[bad][:4])
+
+
+@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s[0] > 16] + [
+    (9, 8300, 1024), (40, 1000, 4096), (300, 1000, 4096), (777, 2000, 2432), (150, 14300, 1664), (1300, 5000, 4096)])
+def test_gemm_bf16_of_normal_values(M, N, K):
+    """On each tile, long K among them: as near as sums of random signs are, which a lost or
+    repeated chunk of a row is not."""
+    require_gpu()
+    a, b = _operands(M, N, K, M + N + K)
+    check_bf16(mx.gemm(a, b, BF16), _val(a), _val(b))
+
+
+@pytest.mark.parametrize("M,N,K", [(1300, 5000, 1152), (1281, 5100, 1280), (1400, 4500, 1408), (1500, 5000, 1664),
+                                   (1536, 4096, 2048), (1300, 5000, 128), (1410, 5000, 2176)])
+def test_gemm_large_tiles_uneven_scales(M, N, K):
+    """256 x 256 tiles keep two groups of four steps' scales: from 9 steps on each is
+    refilled and read again. Scales of neighbouring steps differ, so that a step under another one's
+    shows (whole and partial groups, last row tiles of up to 64, 128 and 256 rows)."""
+    require_gpu()
+    a, b = _operands(M, N, K, M + K)
+    _uneven(a, 1), _uneven(b, 2)
+    check_bf16(mx.gemm(a, b, BF16), _val(a), _val(b))
+
+
+@pytest.mark.parametrize("K", [1152, 1280, 1408, 1664, 2048])
+def test_grouped_large_tiles_uneven_scales(K):
+    """The same by expert, weights two steps ahead."""
+    require_gpu()
+    sizes, N = [257, 64, 0, 65, 128, 129, 1000], 4200
+    G, M = len(sizes), sum(sizes)
+    a = _uneven(_operands(M, 1, K, K)[0], 1)
+    w = [_uneven(_operands(1, N, K, K + g)[1], 2 + g) for g in range(G)]
+    b = mx.QTensor(w[0].fmt, G * N, K, torch.cat([x.codes for x in w]), torch.cat([x.scales for x in w]), groups=G)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    got = mx.gemm_grouped(a, b, torch.from_numpy(off).cuda(), BF16)
+    values = _val(a)
+    for g in range(G):
+        rows = slice(off[g], off[g + 1])
+        check_bf16(got[rows], values[rows], _val(w[g]))
