@@ -296,6 +296,9 @@ hipError_t launch(const Args& p, int64_t groups, hipStream_t s) {
   return launch_kernel(&gemm_few_rows_kernel<FP8, ALIGNED, OUT, W, S, T, D>, grid, 64 * W, 0, s, p);
 }
 
+// Rounds of the 256 CUs that workgroups of T tiles make, one a CU at a time.
+int64_t rounds(int64_t tiles, int T) { return (tiles + 256 * T - 1) / (256 * T); }
+
 // Experts that have rows are taken as min(groups, M). Times in us at 16 rows,
 // FP8, N x K (by expert: rows over experts x N x K).
 template <bool FP8, bool ALIGNED, int OUT>
@@ -308,9 +311,13 @@ hipError_t dispatch(const Args& p, int64_t groups, hipStream_t s) {
       // below 14.7; 128 over 64: 60.2 and 59.2, 32 over 16 x 4096 x 7168: 79 and 65).
       if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
     } else {
-      // Long rows, many of them: one workgroup of 8 waves a CU and 7 tiles
-      // share A (28672 x 8192: 38.0, T = 4 41).
-      if (nk >= 48 && tiles >= 7 * 256) return launch<FP8, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
+      // Long rows, many of them: 7 tiles share A in a workgroup of 8 waves, one a CU, or 4 in one
+      // of 4 waves (below), whichever's rounds of CUs take fewer tiles (K = 8192, N = 14336 / 18432 /
+      // 28672 / 29568 / 32768 / 43008 / 57344 / 65536 / 86016 / 128256: 7 tiles 30 / 29 / 38 / 59 / 59 / 62 / 76 / 97 /
+      // 113 / 172, 4 tiles 24 / 38 / 40 / 41 / 45 / 59 / 78 / 86 / 119 / 167; K = 4096, N = 18432 / 28672: 21 / 26
+      // and 21 / 23).
+      if (nk >= 48 && tiles > 768 && 7 * rounds(tiles, 7) <= 4 * rounds(tiles, 4))
+        return launch<FP8, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
       // The fewest tiles a workgroup that need one round of CUs (T = 1 / 2 / 3:
       // 4096 x 4096 6.6 / 7.3 / 8.7, 6144 x 4096 9.7 / 7.6 / 9.2, 10240 x 8192 - / 24.9 / 16.8;
       // 14336 x 4096: 13.6, with T = 2 13.9, T = 3 16.5).

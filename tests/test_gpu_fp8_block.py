@@ -268,7 +268,7 @@ def _cancelling(rows, K, tall, seed):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 300, 2048), (16, 200, 1024), (16, 9000, 2176), (9, 10300, 2304), (5, 29000, 6400),
-                                   (16, 300, 16512), (16, 6000, 2176)])
+                                   (16, 300, 16512), (16, 6000, 2176), (7, 18500, 6272), (16, 28670, 6144)])
 def test_gemm_few_rows_exact_before_rounding(M, N, K):
     """Up to 16 rows HBM is the bound and products are summed exactly: 2^-18 sum|ab| before
     a bf16 rounding, also where most of a sum cancels."""
