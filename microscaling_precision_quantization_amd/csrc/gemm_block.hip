@@ -394,6 +394,9 @@ hipError_t by_tile(const Args& p, hipStream_t s) {
 //   by expert, rows over experts x N x K: fp8 704 over 64 x 2048 x 4096 107 / 116, 896 132 / 118;
 //   80 over 16 x 2048 x 2048 14.2 / 14.5, 128 15.7 / 14.2; mxfp4 320 over 64 x 2048 x 4096 55 / 60,
 //   512 64 / 61; fp8 32 over 64 x 2048 x 1024 13.5 / 10.9, mxfp4 14.7 / 8.3.
+// The host does not know the rows' distribution, and an even one is the slowest for both. With all
+// rows at one expert of 64 x 2048 x 4096 (each pass of 16 rows reads its weight): fp8 128 rows 12.8 / 17.6,
+// 384 30 / 22, 768 57 / 23 (even 96 / 127); mxfp4 128 9.7 / 16.7, 320 18.2 / 16.9 (even 47 / 63).
 bool few_rows(const Args& p, int fmt) {
   const int64_t steps = (fmt == kMXFP4 ? p.K / 2 : p.K) / 128;  // lines of a row
   if (!p.offsets) return p.M <= 16 && (steps >= 16 || p.N <= 8192);
@@ -417,7 +420,7 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
   const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
   const bool f32 = out_dtype == kOutF32;
-  if (few_rows(p, fmt) && gemm_few_rows_fits(N, K, out_dtype))
+  if (few_rows(p, fmt) && gemm_few_rows_fits(M, N, K, offsets ? groups : 0, out_dtype))
     return gemm_few_rows(fmt, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
   // Tiles of 256 x 256, for a third of the CUs or more, where most are more than half full.
   // (Times of 256 / the best of the smaller tiles: fp8 1500 x 8192 x 4096 (192 tiles)

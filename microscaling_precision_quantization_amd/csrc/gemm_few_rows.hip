@@ -23,7 +23,9 @@
 //    the vector ALU wait for HBM, and the FP8 MFMA, which loses bits of a sum, would
 //    gain nothing (16 rows, FP8 MFMA / bf16: 28672 x 8192 37.8 / 37.8 us, 4096 x 4096
 //    6.8 / 6.9, 8192 x 28672 44.0 / 44.5; 128 rows over 64 x 2048 x 4096 73.4 / 73.9).
-//  * A group with more than 16 rows takes further passes over the weights.
+//  * A group with more than 16 rows takes further passes over the weights, each in
+//    workgroups of its own, which find their group and rows from the offsets: all
+//    CUs share the passes of the one expert that a router may send everything to.
 #include <type_traits>
 #include <utility>
 
@@ -51,9 +53,9 @@ constexpr int kNonTemporal = 2;                // cache policy of a load: stream
 struct Args {
   const uint8_t *A, *SA, *B, *SB;
   void* C;
-  const int* offsets;  // null: dense
+  const int* offsets;  // null: dense (M at most 16)
   int64_t ldc;
-  int M, N, K;
+  int groups, M, N, K;
 };
 
 // 8 E4M3 codes as bf16.
@@ -86,12 +88,9 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   float(*part)[T][4][64] = (float(*)[T][4][64])smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * (16 * T), group = blockIdx.y;
-  int lo = 0, hi = p.M;
-  if (p.offsets) groups::rows_of(p.offsets, p.M, group, lo, hi);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
-  if (lo >= hi) return;
+  const int n0 = blockIdx.x * (16 * T);
+  int group = 0, m0 = 0, mrows = p.M;
+  if (p.offsets && !groups::pass_of(p.offsets, p.groups, p.M, blockIdx.y, group, m0, mrows)) return;
 
   const int nrows = min(p.N - n0, 16 * T);
   const uint32_t rowbytes = (uint32_t)(FP8 ? p.K : p.K / 2);
@@ -145,154 +144,153 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
     return u32x2{x << (8 * g), y << (8 * g)};
   };
 
-  for (int m0 = lo; m0 < hi; m0 += 16) {
-    if (m0 != lo) __syncthreads();  // (the last pass's sums, where the rings are, have been read)
-    const int mrows = min(hi - m0, 16);
-    const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.A + (int64_t)m0 * rowbytes), 0, (int)((uint32_t)mrows * rowbytes), kRsrcFlags);
-    const __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.SA + (int64_t)m0 * sstride), 0, (int)((uint32_t)mrows * sstride), kRsrcFlags);
-    f32x4 acc[T];
+  const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.A + (int64_t)m0 * rowbytes), 0, (int)((uint32_t)mrows * rowbytes), kRsrcFlags);
+  const __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.SA + (int64_t)m0 * sstride), 0, (int)((uint32_t)mrows * sstride), kRsrcFlags);
+  f32x4 acc[T];
 #pragma unroll
-    for (int j = 0; j < T; j++) acc[j] = f32x4{0, 0, 0, 0};
+  for (int j = 0; j < T; j++) acc[j] = f32x4{0, 0, 0, 0};
 
-    for (int c = 0; c < chunks; c++) {
-      const int s0 = (c * kWaves + wave) * S;
-      // The ring's first weights, then A of all S steps, then (FP8) the
-      // weights' scales: lane l's is step s0 + l's.
-      u32x2 wsc[D];  // MXFP4: the ring's scales
-      auto load = [&](int k) __attribute__((always_inline)) {
-        const int t = k / S, s = s0 + k % S;
-        const int so = step_at((uint32_t)(16 * t) * rowbytes, s);
+  for (int c = 0; c < chunks; c++) {
+    const int s0 = (c * kWaves + wave) * S;
+    // The ring's first weights, then A of all S steps, then (FP8) the
+    // weights' scales: lane l's is step s0 + l's.
+    u32x2 wsc[D];  // MXFP4: the ring's scales
+    auto load = [&](int k) __attribute__((always_inline)) {
+      const int t = k / S, s = s0 + k % S;
+      const int so = step_at((uint32_t)(16 * t) * rowbytes, s);
 #pragma unroll
-        for (int h = 0; h < 2; h++)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(ring + (k % D) * kSlot + h * 1024), 16,
-                                                   FP8 || s < nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
-        if (!FP8) wsc[k % D] = load_scales(rSB, (uint32_t)(16 * t) * sstride, s);
-      };
+      for (int h = 0; h < 2; h++)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(ring + (k % D) * kSlot + h * 1024), 16,
+                                                 FP8 || s < nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
+      if (!FP8) wsc[k % D] = load_scales(rSB, (uint32_t)(16 * t) * sstride, s);
+    };
 #pragma unroll
-      for (int k = 0; k < D - 1; k++)
-        if (k < T * S) load(k);
-      i32x8 a[S];
-      float sa[S];
-      u32x2 sc[S];
+    for (int k = 0; k < D - 1; k++)
+      if (k < T * S) load(k);
+    i32x8 a[S];
+    float sa[S];
+    u32x2 sc[S];
 #pragma unroll
-      for (int s = 0; s < S; s++) {
-        const int so = step_at(0, s0 + s);
-        const bool full = FP8 || s0 + s < nk - 1;
-        const i32x4 x = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[0] : va_last[0], so, 0));
-        const i32x4 y = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[1] : va_last[1], so, 0));
-        a[s] = i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        if (FP8)
-          sa[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-              rSA, soff, (int)(s0 + s < nk ? (uint32_t)(s0 + s) * 4u : kScalarOOB), 0));
-        else
-          sc[s] = load_scales(rSA, 0, s0 + s);
-      }
-      float sb[T];
-      if (FP8) {
-#pragma unroll
-        for (int t = 0; t < T; t++) {
-          const uint32_t nb = (uint32_t)((n0 + 16 * t) / 128 - nb0);  // (a tile past N: out of range)
-          sb[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-              rSB, s0 + lane < nk ? (uint32_t)lane * 4u : kOOB, (int)(nb * sstride + (uint32_t)s0 * 4u), 0));
-        }
-      }
-      // Step k + 1's fragments are read before step k's MFMAs. Loads end in
-      // order: step k + 1's have arrived when only the later steps' are out
-      // (the first time, A's too, which came last).
-      constexpr int kLoads = FP8 ? 2 : ALIGNED ? 3 : 4;  // of a step
-      auto arrived = [&](auto n) __attribute__((always_inline)) {
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"i"(decltype(n)::value) : "memory");
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      auto read = [&](int k) __attribute__((always_inline)) {
-        const i32x4 x = *(const i32x4*)(ring + (k % D) * kSlot + frag0), y = *(const i32x4*)(ring + (k % D) * kSlot + frag1);
-        return i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      };
-      arrived(std::integral_constant<int, 0>{});
-      i32x8 next = read(0);
-      unroll<T * S>([&](auto kk) __attribute__((always_inline)) {
-        constexpr int k = decltype(kk)::value, t = k / S, s = k % S;
-        const i32x8 bv = next;
-        if (k + D - 1 < T * S) load(k + D - 1);
-        if constexpr (k + 1 < T * S) {
-          // Steps loaded behind k + 1 (the first D - 1 have all arrived).
-          constexpr int last = k + D - 1 < T * S ? k + D - 1 : T * S - 1;
-          constexpr int behind = last - (k + 1);
-          if constexpr (k + 1 >= D - 1) arrived(std::integral_constant<int, behind * kLoads>{});
-          next = read(k + 1);
-        }
-        const u32x2 wscale = wsc[k % D];
-        if constexpr (FP8) {
-          const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb[t]), s));
-          const float f = sa[s] * w;
-          f32x4 P = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int h = 0; h < 4; h++)
-            P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
-                                                        expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const i32x8 bh = {bv[4 * h], bv[4 * h + 1], bv[4 * h + 2], bv[4 * h + 3], 0, 0, 0, 0};
-            const int wb = (int)((wscale[h] >> (8 * g)) & 0xFFu);
-            const i32x8 av = {a[s][4 * h], a[s][4 * h + 1], a[s][4 * h + 2], a[s][4 * h + 3], 0, 0, 0, 0};
-            const int wa = (int)((sc[s][h] >> (8 * g)) & 0xFFu);
-            acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bh, av, acc[t], 4, 4, 0, wb, 0, wa);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
+    for (int s = 0; s < S; s++) {
+      const int so = step_at(0, s0 + s);
+      const bool full = FP8 || s0 + s < nk - 1;
+      const i32x4 x = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[0] : va_last[0], so, 0));
+      const i32x4 y = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, full ? va[1] : va_last[1], so, 0));
+      a[s] = i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      if (FP8)
+        sa[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+            rSA, soff, (int)(s0 + s < nk ? (uint32_t)(s0 + s) * 4u : kScalarOOB), 0));
+      else
+        sc[s] = load_scales(rSA, 0, s0 + s);
     }
-
-    // The waves' sums, added in their order. acc[j][e] of lane (r, g) is row r,
-    // column 16 j + 4 g + e.
-    __syncthreads();  // (every ring has been read)
+    float sb[T];
+    if (FP8) {
 #pragma unroll
-    for (int j = 0; j < T; j++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) part[wave][j][e][lane] = acc[j][e];
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < (T + kWaves - 1) / kWaves; u++) {
-      const int j = u * kWaves + wave;
-      if (j >= T) break;
-      f32x4 v;
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        v[e] = part[0][j][e][lane];
-#pragma unroll
-        for (int w = 1; w < kWaves; w++) v[e] += part[w][j][e][lane];
+      for (int t = 0; t < T; t++) {
+        const uint32_t nb = (uint32_t)((n0 + 16 * t) / 128 - nb0);  // (a tile past N: out of range)
+        sb[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+            rSB, s0 + lane < nk ? (uint32_t)lane * 4u : kOOB, (int)(nb * sstride + (uint32_t)s0 * 4u), 0));
       }
-      const int col = n0 + 16 * j + 4 * g;
-      if (r >= mrows) continue;
-      const int64_t at = (int64_t)(m0 + r) * p.ldc + col;
-      if (p.ldc % 4 == 0 && col + 4 <= p.N) {
-        if (OUT == kOutF32)
-          *(f32x4*)((float*)p.C + at) = v;
-        else
-          *(u32x2*)((uint16_t*)p.C + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+    // Step k + 1's fragments are read before step k's MFMAs. Loads end in
+    // order: step k + 1's have arrived when only the later steps' are out
+    // (the first time, A's too, which came last).
+    constexpr int kLoads = FP8 ? 2 : ALIGNED ? 3 : 4;  // of a step
+    auto arrived = [&](auto n) __attribute__((always_inline)) {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"i"(decltype(n)::value) : "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto read = [&](int k) __attribute__((always_inline)) {
+      const i32x4 x = *(const i32x4*)(ring + (k % D) * kSlot + frag0), y = *(const i32x4*)(ring + (k % D) * kSlot + frag1);
+      return i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    };
+    arrived(std::integral_constant<int, 0>{});
+    i32x8 next = read(0);
+    unroll<T * S>([&](auto kk) __attribute__((always_inline)) {
+      constexpr int k = decltype(kk)::value, t = k / S, s = k % S;
+      const i32x8 bv = next;
+      if (k + D - 1 < T * S) load(k + D - 1);
+      if constexpr (k + 1 < T * S) {
+        // Steps loaded behind k + 1 (the first D - 1 have all arrived).
+        constexpr int last = k + D - 1 < T * S ? k + D - 1 : T * S - 1;
+        constexpr int behind = last - (k + 1);
+        if constexpr (k + 1 >= D - 1) arrived(std::integral_constant<int, behind * kLoads>{});
+        next = read(k + 1);
+      }
+      const u32x2 wscale = wsc[k % D];
+      if constexpr (FP8) {
+        const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb[t]), s));
+        const float f = sa[s] * w;
+        f32x4 P = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 4; h++)
+          P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
+                                                      expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (col + e < p.N) {
-            if (OUT == kOutF32)
-              ((float*)p.C)[at + e] = v[e];
-            else
-              ((uint16_t*)p.C)[at + e] = bf16_bits(v[e]);
-          }
+        for (int h = 0; h < 2; h++) {
+          const i32x8 bh = {bv[4 * h], bv[4 * h + 1], bv[4 * h + 2], bv[4 * h + 3], 0, 0, 0, 0};
+          const int wb = (int)((wscale[h] >> (8 * g)) & 0xFFu);
+          const i32x8 av = {a[s][4 * h], a[s][4 * h + 1], a[s][4 * h + 2], a[s][4 * h + 3], 0, 0, 0, 0};
+          const int wa = (int)((sc[s][h] >> (8 * g)) & 0xFFu);
+          acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bh, av, acc[t], 4, 4, 0, wb, 0, wa);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+
+  // The waves' sums, added in their order. acc[j][e] of lane (r, g) is row r,
+  // column 16 j + 4 g + e.
+  __syncthreads();  // (every ring has been read)
+#pragma unroll
+  for (int j = 0; j < T; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) part[wave][j][e][lane] = acc[j][e];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < (T + kWaves - 1) / kWaves; u++) {
+    const int j = u * kWaves + wave;
+    if (j >= T) break;
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      v[e] = part[0][j][e][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; w++) v[e] += part[w][j][e][lane];
+    }
+    const int col = n0 + 16 * j + 4 * g;
+    if (r >= mrows) continue;
+    const int64_t at = (int64_t)(m0 + r) * p.ldc + col;
+    if (p.ldc % 4 == 0 && col + 4 <= p.N) {
+      if (OUT == kOutF32)
+        *(f32x4*)((float*)p.C + at) = v;
+      else
+        *(u32x2*)((uint16_t*)p.C + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (col + e < p.N) {
+          if (OUT == kOutF32)
+            ((float*)p.C)[at + e] = v[e];
+          else
+            ((uint16_t*)p.C)[at + e] = bf16_bits(v[e]);
+        }
     }
   }
 }
 
+// Passes of 16 rows that any offsets can need (dense: one).
+int64_t passes(int64_t M, int64_t groups) { return groups > 0 ? groups::max_row_tiles(M, groups, 16) : 1; }
+
 template <bool FP8, bool ALIGNED, int OUT, int W, int S, int T, int D>
-hipError_t launch(const Args& p, int64_t groups, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N + 16 * T - 1) / (16 * T)), (unsigned)groups);
+hipError_t launch(const Args& p, hipStream_t s) {
+  const dim3 grid((unsigned)((p.N + 16 * T - 1) / (16 * T)), (unsigned)passes(p.M, p.offsets ? p.groups : 0));
   return launch_kernel(&gemm_few_rows_kernel<FP8, ALIGNED, OUT, W, S, T, D>, grid, 64 * W, 0, s, p);
 }
 
@@ -302,14 +300,14 @@ int64_t rounds(int64_t tiles, int T) { return (tiles + 256 * T - 1) / (256 * T);
 // Experts that have rows are taken as min(groups, M). Times in us at 16 rows,
 // FP8, N x K (by expert: rows over experts x N x K).
 template <bool FP8, bool ALIGNED, int OUT>
-hipError_t dispatch(const Args& p, int64_t groups, hipStream_t s) {
+hipError_t dispatch(const Args& p, hipStream_t s) {
   if constexpr (FP8) {
-    const int64_t tiles = (p.N + 15) / 16 * (p.offsets && p.M < groups ? p.M : groups);
+    const int64_t tiles = (p.N + 15) / 16 * (!p.offsets ? 1 : p.M < p.groups ? p.M : p.groups);
     const int nk = p.K / 128;
     if (p.offsets) {
       // Few experts with rows: 4 waves on long runs (8 rows over 32 x 2048 x 4096: 12.0,
       // below 14.7; 128 over 64: 60.2 and 59.2, 32 over 16 x 4096 x 7168: 79 and 65).
-      if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
+      if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, s);
     } else {
       // Long rows, many of them: 7 tiles share A in a workgroup of 8 waves, one a CU, or 4 in one
       // of 4 waves (below), whichever's rounds of CUs take fewer tiles (K = 8192, N = 14336 / 18432 /
@@ -317,34 +315,35 @@ hipError_t dispatch(const Args& p, int64_t groups, hipStream_t s) {
       // 113 / 172, 4 tiles 24 / 38 / 40 / 41 / 45 / 59 / 78 / 86 / 119 / 167; K = 4096, N = 18432 / 28672: 21 / 26
       // and 21 / 23).
       if (nk >= 48 && tiles > 768 && 7 * rounds(tiles, 7) <= 4 * rounds(tiles, 4))
-        return launch<FP8, ALIGNED, OUT, 8, 8, 7, 8>(p, groups, s);
+        return launch<FP8, ALIGNED, OUT, 8, 8, 7, 8>(p, s);
       // The fewest tiles a workgroup that need one round of CUs (T = 1 / 2 / 3:
       // 4096 x 4096 6.6 / 7.3 / 8.7, 6144 x 4096 9.7 / 7.6 / 9.2, 10240 x 8192 - / 24.9 / 16.8;
       // 14336 x 4096: 13.6, with T = 2 13.9, T = 3 16.5).
-      if (tiles <= 256) return launch<FP8, ALIGNED, OUT, 8, 2, 1, 3>(p, groups, s);
+      if (tiles <= 256) return launch<FP8, ALIGNED, OUT, 8, 2, 1, 3>(p, s);
       // (8192 x 28672: 4 waves on long runs 44.4, T = 2 46.5; one row 37.2 and 41.5.)
-      if (tiles <= 512 && nk >= 128) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, groups, s);
-      if (tiles > 512 && tiles <= 768) return launch<FP8, ALIGNED, OUT, 8, 1, 3, 4>(p, groups, s);
-      if (tiles > 768 && nk > 16) return launch<FP8, ALIGNED, OUT, 4, 8, 4, 9>(p, groups, s);
+      if (tiles <= 512 && nk >= 128) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, s);
+      if (tiles > 512 && tiles <= 768) return launch<FP8, ALIGNED, OUT, 8, 1, 3, 4>(p, s);
+      if (tiles > 768 && nk > 16) return launch<FP8, ALIGNED, OUT, 4, 8, 4, 9>(p, s);
     }
   }
   // Two tiles, a step of each in a wave's chunk: eight waves on one run of a row
   // (mxfp4 128 over 64 x 2048 x 4096: 35.4, with 4 waves on runs of 4 steps 42.9, four tiles 37.7).
-  return launch<FP8, ALIGNED, OUT, 8, 1, 2, 3>(p, groups, s);
+  return launch<FP8, ALIGNED, OUT, 8, 1, 2, 3>(p, s);
 }
 
 template <bool ALIGNED>
-hipError_t mxfp4(const Args& p, int64_t groups, bool f32, hipStream_t s) {
-  if (f32) return dispatch<false, ALIGNED, kOutF32>(p, groups, s);
-  return dispatch<false, ALIGNED, kOutBF16>(p, groups, s);
+hipError_t mxfp4(const Args& p, bool f32, hipStream_t s) {
+  if (f32) return dispatch<false, ALIGNED, kOutF32>(p, s);
+  return dispatch<false, ALIGNED, kOutBF16>(p, s);
 }
 
 }  // namespace
 
 // fp32 results: accumulation chains of at most 48 matrix instructions or scale
 // blocks, of 128 K, in a wave.
-bool gemm_few_rows_fits(int64_t N, int64_t K, int out_dtype) {
-  if (N > ((int64_t)1 << 27)) return false;  // (16 columns a workgroup: the grid)
+bool gemm_few_rows_fits(int64_t M, int64_t N, int64_t K, int64_t groups, int out_dtype) {
+  // (The grid: 16 columns a workgroup across, passes down.)
+  if (N > ((int64_t)1 << 27) || passes(M, groups) > 65535) return false;
   return out_dtype != kOutF32 || K <= (int64_t)48 * 128 * 4;
 }
 
@@ -352,11 +351,10 @@ hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a
                          const void* b, const void* sb, const int32_t* offsets, int64_t groups,
                          int out_dtype, void* c, int64_t ldc, hipStream_t s) {
   const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
-               ldc, (int)M, (int)N, (int)K};
-  const int64_t g = offsets ? groups : 1;
+               ldc, (int)groups, (int)M, (int)N, (int)K};
   const bool f32 = out_dtype == kOutF32;
-  if (fmt == kMXFP4) return K % 128 == 0 ? mxfp4<true>(p, g, f32, s) : mxfp4<false>(p, g, f32, s);
-  return f32 ? dispatch<true, true, kOutF32>(p, g, s) : dispatch<true, true, kOutBF16>(p, g, s);
+  if (fmt == kMXFP4) return K % 128 == 0 ? mxfp4<true>(p, f32, s) : mxfp4<false>(p, f32, s);
+  return f32 ? dispatch<true, true, kOutF32>(p, s) : dispatch<true, true, kOutBF16>(p, s);
 }
 
 }  // namespace mx

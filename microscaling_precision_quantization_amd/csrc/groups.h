@@ -30,12 +30,6 @@ struct Tile {
   int tn;            // column tile
 };
 
-// Rows of group g: [lo, hi).
-__device__ __forceinline__ void rows_of(const int* offsets, int M, int g, int& lo, int& hi) {
-  lo = min(max(offsets[g], 0), M);
-  hi = max(min(offsets[g + 1], M), lo);
-}
-
 // v of another lane by DPP, 0 where there is none (or ROWS leaves the row out).
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ int dpp0(int v) {
@@ -53,6 +47,31 @@ __device__ __forceinline__ int wave_scan(int v) {
   v += dpp0<0x142, 0xA>(v);
   v += dpp0<0x143, 0xC>(v);
   return v;
+}
+
+// Pass `i` of up to 16 rows, counting each group's passes in turn: its group and first
+// row, and its rows; false: there is none.
+__device__ __forceinline__ bool pass_of(const int* offsets, int n, int M, int i, int& group, int& row, int& rows) {
+  const int lane = threadIdx.x & 63;
+  for (int c = 0; c < n; c += 64) {
+    int lo = 0, hi = 0;
+    if (c + lane < n) {
+      lo = min(max(offsets[c + lane], 0), M);
+      hi = max(min(offsets[c + lane + 1], M), lo);
+    }
+    const int upto = wave_scan((hi - lo + 15) / 16);
+    const int sum = __builtin_amdgcn_readlane(upto, 63);
+    if (i < sum) {
+      const int l = __builtin_ctzll(__ballot(upto > i));
+      const int before = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0;
+      group = __builtin_amdgcn_readfirstlane(c + l);
+      row = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_readlane(lo, l) + (i - before) * 16);
+      rows = __builtin_amdgcn_readfirstlane(min(__builtin_amdgcn_readlane(hi, l) - row, 16));
+      return true;
+    }
+    i -= sum;
+  }
+  return false;
 }
 
 // Tile of workgroup `bid`; false: there is none. offsets null: one group of

@@ -264,3 +264,41 @@ def test_captured_with_new_offsets(fmt, M, N):
         torch.cuda.synchronize()
         _check(out, a, b, off, fmt, BF16)
         assert torch.equal(out, mx.gemm_grouped(a, b, new, BF16))
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+def test_few_rows_skewed(fmt, out):
+    """Few rows an expert on average (long rows of weights), most of them in one: its passes
+    of 16 rows, found by scanning the groups 64 at a time."""
+    require_gpu()
+    for G, at, rows in ((64, 0, 384), (64, 63, 383), (65, 64, 200), (130, 70, 500), (200, 199, 17), (3, 1, 18)):
+        sizes = [0] * G
+        sizes[at] = rows - 2 if G > 3 else rows
+        sizes[G // 2] += 1
+        sizes[G - 1] += 1
+        a, b = _operands(fmt, sum(sizes), G, 40, 4096, G + at)
+        off, d = _offsets(sizes)
+        _check(mx.gemm_grouped(a, b, d, out), a, b, off, fmt, out)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+def test_few_rows_offsets(fmt):
+    """Few rows, long rows of weights: rows of no group are left, row numbers clamped to
+    [0, M], and offsets out of order write nothing outside C."""
+    require_gpu()
+    M, G, N, K = 60, 70, 100, 4096
+    a, b = _operands(fmt, M, G, N, K, 1)
+    sizes = np.zeros(G, np.int64)
+    sizes[[0, 3, 63, 64, 69]] = [2, 20, 1, 17, 3]
+    off, d = _offsets(sizes, 5)
+    buf = torch.full((M + 1, N + 4), 7.0, dtype=BF16, device="cuda")
+    _check(mx.gemm_grouped(a, b, d, BF16, out=buf[:M, :N]), a, b, off, fmt, BF16)
+    assert bool((buf[:5] == 7).all()) and bool((buf[off[-1]:] == 7).all()) and bool((buf[:, N:] == 7).all())
+    wide = np.where(np.arange(G + 1) < 4, -9, np.where(np.arange(G + 1) < 66, 31, M + 99)).astype(np.int32)
+    _check(mx.gemm_grouped(a, b, torch.from_numpy(wide).cuda(), BF16), a, b, np.clip(wide, 0, M), fmt, BF16)
+    r = np.random.RandomState(0)
+    for bad in (np.arange(G + 1) % 2 * M, r.randint(-50, 150, G + 1), M - np.arange(G + 1)):
+        buf.fill_(7)
+        mx.gemm_grouped(a, b, torch.from_numpy(bad.astype(np.int32)).cuda(), BF16, out=buf[:M, :N])
+        assert bool((buf[M] == 7).all()) and bool((buf[:, N:] == 7).all())
