@@ -452,16 +452,17 @@ def gemm(a, b, out_dtype=None, out=None, workspace=None):
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         wsb = workspace.numel() * workspace.element_size()  # the C call checks it is enough
+    ldc = c.stride(0) if M > 1 else N  # (the row stride of a single row says nothing)
     la = a.layout if isinstance(a, QTensor) else MX_LAYOUT_ROWS
     a_parts = (a.codes, a.scales, a.tensor_scale) if isinstance(a, QTensor) else (a,)
     stream = _stream(torch, dev, *a_parts, b.codes, b.scales, b.tensor_scale, c, workspace)
     if la != MX_LAYOUT_ROWS or b.layout != MX_LAYOUT_ROWS:
         _check(_on(dev, lib().mx_gemm_ex, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta,
-                   _ptr(b.codes), _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0),
+                   _ptr(b.codes), _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), ldc,
                    _ptr(workspace), wsb, stream, la, b.layout), "mx_gemm_ex")
         return c
     _check(_on(dev, lib().mx_gemm, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta, _ptr(b.codes),
-               _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), c.stride(0), _ptr(workspace), wsb,
+               _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), ldc, _ptr(workspace), wsb,
                stream), "mx_gemm")
     return c
 

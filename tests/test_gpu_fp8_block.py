@@ -345,3 +345,19 @@ def test_grouped_large_tiles_uneven_scales(K):
     for g in range(G):
         rows = slice(off[g], off[g + 1])
         check_bf16(got[rows], values[rows], _val(w[g]))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "mxfp4", "mxfp8", "w4a16"])
+def test_gemm_one_row_into_any_stride(kind):
+    """The row stride of a single row says nothing."""
+    require_gpu()
+    N, K = 100, 256
+    x, w = _mixed(1, K, 1).cuda(), _mixed(N, K, 2).cuda()
+    if kind == "fp8":
+        a, b = mx.quantize(x, "fp8_b128"), mx.quantize(w, "fp8_b128x128")
+    else:
+        a, b = x if kind == "w4a16" else mx.quantize(x, kind), mx.quantize(w, "mxfp4" if kind == "w4a16" else kind)
+    out = torch.full((N, 1), 7.0, dtype=BF16, device="cuda").t()
+    assert out.stride() == (1, 1)
+    assert mx.gemm(a, b, BF16, out=out) is out
+    assert torch.equal(out, mx.gemm(a, b, BF16))
