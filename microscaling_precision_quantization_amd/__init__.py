@@ -36,6 +36,7 @@ BLOCK = {MX_FMT_MXFP4: 32, MX_FMT_MXFP8: 32, MX_FMT_NVFP4: 16, MX_FMT_BF16: 32,
          MX_FMT_MXFP4_MBS16: 16, MX_FMT_FP8_B128: 128, MX_FMT_FP8_B128X128: 128}
 MBS_FORMATS = (MX_FMT_MXFP4_MBS, MX_FMT_MXFP4_MBS16)
 FP8_BLOCK_FORMATS = (MX_FMT_FP8_B128, MX_FMT_FP8_B128X128)  # fp32 scales
+PAIRS = {MX_FMT_BF16: MX_FMT_MXFP4, MX_FMT_FP8_B128: MX_FMT_FP8_B128X128}  # a GEMM's b, where not a's format
 
 
 def code_cols(fmt, cols):
@@ -310,7 +311,8 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
     the layout given; otherwise layout "kpanel" (MXFP4, MXFP8, E5M2, E3M2,
     NVFP4) selects mx_quantize_layout. A [groups][rows][cols] tensor ("mxfp4"
     or "fp8_b128x128", row layout) is a stack of weights for gemm_grouped, each
-    quantized by itself."""
+    quantized by itself. No rows (but for NVFP4, whose scale is the tensor's) give
+    an empty QTensor, which the calls below take too."""
     import torch
     f = _fmt_id(fmt)
     lay = LAYOUTS[layout]
@@ -341,6 +343,8 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
     codes = torch.empty(rows, code_cols(f, cols), dtype=torch.uint8, device=dev)
     scales = torch.empty(*scale_shape(f, rows, cols), device=dev,
                          dtype=torch.float32 if f in FP8_BLOCK_FORMATS else torch.uint8)
+    if rows == 0 and f != MX_FMT_NVFP4:
+        return _empty(f, cols, codes, scales, lay, "mx_quantize", x)
     ts = ws = None
     wsb = 0
     if f == MX_FMT_NVFP4:
@@ -355,6 +359,16 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
                    _ptr(scales), _ptr(ts), _ptr(ws), wsb, _stream(torch, dev, x), lay),
                "mx_quantize_layout")
     return QTensor(f, rows, cols, codes, scales, ts, lay)
+
+
+def _empty(f, cols, codes, scales, layout, what, *inputs):
+    """The QTensor of no rows (a rank that a router sent no tokens): nothing is launched."""
+    import torch
+    _stream(torch, codes.device, *inputs)
+    granule = 128 if f in MBS_FORMATS else BLOCK[f]
+    if f == MX_FMT_BF16 or cols == 0 or cols % granule != 0:
+        raise MXError(MX_ERR_INVALID_ARG, what)
+    return QTensor(f, 0, cols, codes, scales, None, layout)
 
 
 def _quantize_tile_stack(x, scale_rule, rotation):
@@ -392,6 +406,9 @@ def dequantize(q, out_dtype=None):
         return torch.cat([dequantize(QTensor(q.fmt, n, q.cols, codes[i], scales[i]), out_dtype)
                           for i in range(q.groups)])
     y = torch.empty(q.rows, q.cols, dtype=out_dtype, device=q.codes.device)
+    if q.rows == 0:
+        _stream(torch, q.codes.device, q.codes, q.scales, q.tensor_scale)
+        return y
     _check(_on(q.codes.device, mx_dequantize, q.fmt, q.block, MX_ROUND_RNE, q.rows, q.cols,
                _ptr(q.codes), _ptr(q.scales), _ptr(q.tensor_scale), od, _ptr(y),
                _stream(torch, q.codes.device, q.codes, q.scales, q.tensor_scale)), "mx_dequantize")
@@ -456,6 +473,9 @@ def gemm(a, b, out_dtype=None, out=None, workspace=None):
     la = a.layout if isinstance(a, QTensor) else MX_LAYOUT_ROWS
     a_parts = (a.codes, a.scales, a.tensor_scale) if isinstance(a, QTensor) else (a,)
     stream = _stream(torch, dev, *a_parts, b.codes, b.scales, b.tensor_scale, c, workspace)
+    if M == 0:
+        _check(MX_OK if b.fmt == PAIRS.get(fa, fa) else MX_ERR_UNSUPPORTED, "mx_gemm")
+        return c
     if la != MX_LAYOUT_ROWS or b.layout != MX_LAYOUT_ROWS:
         _check(_on(dev, lib().mx_gemm_ex, fa, b.fmt, b.block, MX_ROUND_RNE, M, N, K, pa, psa, pta,
                    _ptr(b.codes), _ptr(b.scales), _ptr(b.tensor_scale), od, _ptr(c), ldc,
@@ -495,6 +515,10 @@ def gemm_grouped(a, b, offsets, out_dtype=None, out=None):
     elif out.dtype != out_dtype or out.dim() != 2 or tuple(out.shape) != (M, N) or out.stride(1) != 1:
         raise ValueError(f"out must be a [{M}][{N}] {out_dtype} tensor with unit column stride")
     stream = _stream(torch, dev, a.codes, a.scales, b.codes, b.scales, offsets, out)
+    if M == 0:
+        pair = a.fmt in (MX_FMT_MXFP4, MX_FMT_FP8_B128) and b.fmt == PAIRS.get(a.fmt, a.fmt)
+        _check(MX_OK if pair else MX_ERR_UNSUPPORTED, "mx_gemm_grouped")
+        return out
     _check(_on(dev, lib().mx_gemm_grouped, a.fmt, b.fmt, b.block, MX_ROUND_RNE, G, M, N, K, _ptr(offsets),
                _ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales),
                MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, _ptr(out),
@@ -543,6 +567,8 @@ def norm_quantize(x, weight, fmt, residual=None, gate=None, post_weight=None, al
                          dtype=torch.float32 if f == MX_FMT_FP8_B128 else torch.uint8)
     lay = LAYOUTS[layout]
     stream = _stream(torch, dev, x, residual, gate, post_weight, weight, out)
+    if rows == 0:
+        return _empty(f, cols, codes, scales, lay, "mx_norm_quantize"), out
     # (The row stride of a single row says nothing.)
     ldx = x.stride(0) if rows > 1 else cols
     ldr = residual.stride(0) if residual is not None and rows > 1 else cols
