@@ -40,15 +40,6 @@ __device__ __forceinline__ uint32_t chunk_absmax(u32x4 v) {
   return r.x > r.y ? r.x : r.y;
 }
 
-__device__ __forceinline__ void unpack8(u32x4 v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; k++) {
-    x[2 * k] = __builtin_bit_cast(float, w[k] << 16);
-    x[2 * k + 1] = __builtin_bit_cast(float, w[k] & 0xFFFF0000u);
-  }
-}
-
 // 1 x 128 blocks: the input is a flat array of 16-byte chunks (cols is a
 // multiple of 128), 16 consecutive lanes (a DPP row) own a block.
 __global__ __launch_bounds__(kThreads) void quant_fp8_rows_kernel(const u32x4* __restrict__ x,

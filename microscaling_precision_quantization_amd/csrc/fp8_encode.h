@@ -1,5 +1,6 @@
 // E4M3 codes under an fp32 scale: the scale from a block's amax, and codes
-// that are nearest to the exact quotient x / s (see fp8_block.hip).
+// that are nearest to the exact quotient x / s (see fp8_block.hip); and codes back
+// to values.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -9,6 +10,8 @@ namespace mx {
 namespace fp8 {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Max of v over each DPP row of 16 lanes, in every lane of the row.
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
@@ -53,6 +56,16 @@ __device__ __forceinline__ void decode4(uint32_t q, float* o) {
   const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)q, false);
   const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)q, true);
   o[0] = a.x; o[1] = a.y; o[2] = b.x; o[3] = b.y;
+}
+
+// 8 E4M3 codes as bf16.
+__device__ __forceinline__ bf16x8 expand8(int lo, int hi) {
+  u32x4 o;
+  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, false));
+  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, true));
+  o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, false));
+  o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, true));
+  return __builtin_bit_cast(bf16x8, o);
 }
 
 // The code between two neighbouring candidates lo < hi (magnitudes' codes, or

@@ -1,6 +1,6 @@
-// Block-scaled GEMM C = A B^T on 16 x 16 x 128 matrix instructions, dense or
-// by expert (groups.h), for MXFP4 x MXFP4 and for FP8 x FP8 under fp32 scales
-// per 1 x 128 of A and 128 x 128 of B.
+// Block-scaled GEMM C = A B^T on 16 x 16 x 128 matrix instructions: FP8 x FP8 under
+// fp32 scales per 1 x 128 of A and 128 x 128 of B, dense or by expert (groups.h),
+// and MXFP4 x MXFP4 by expert (dense: gemm_mx.hip, gemm_mxfp4.hip).
 //
 // FP8: a K step of 128 is one scale block, so the step's MFMA starts from
 // zero, and the vector ALU adds its partial sum times s_A(row) s_B(tile):
@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "bf16.h"
+#include "fp8_encode.h"
 #include "groups.h"
 #include "mx_internal.h"
 
@@ -41,7 +42,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+using fp8::bf16x8;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
@@ -82,20 +83,10 @@ struct Geo {
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
-// 8 E4M3 codes as bf16.
-__device__ __forceinline__ bf16x8 expand8(int lo, int hi) {
-  u32x4 o;
-  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, false));
-  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, true));
-  o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, false));
-  o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, true));
-  return __builtin_bit_cast(bf16x8, o);
-}
-
 struct Args {
   const uint8_t *A, *SA, *B, *SB;
   void* C;
-  const int* offsets;  // null: dense
+  const int* offsets;  // null: dense (FP8)
   int64_t ldc;
   int groups, M, N, K, tiles_n;
 };
@@ -209,7 +200,7 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
 #pragma unroll
         for (int j = 0; j < G::TNW; j++)
 #pragma unroll
-          for (int q = 0; q < 4; q++) be[j][q] = expand8(bf[j][2 * q], bf[j][2 * q + 1]);
+          for (int q = 0; q < 4; q++) be[j][q] = fp8::expand8(bf[j][2 * q], bf[j][2 * q + 1]);
 #pragma unroll
         for (int i = 0; i < G::TMW; i++) {
           const int row = wm * 16 * G::TMW + i * 16 + r;
@@ -217,7 +208,7 @@ __global__ __launch_bounds__(G::kThreads) void gemm_block_kernel(Args p) {
           const i32x8 af = frag(cur, row);
           bf16x8 ae[4];
 #pragma unroll
-          for (int q = 0; q < 4; q++) ae[q] = expand8(af[2 * q], af[2 * q + 1]);
+          for (int q = 0; q < 4; q++) ae[q] = fp8::expand8(af[2 * q], af[2 * q + 1]);
 #pragma unroll
           for (int j = 0; j < G::TNW; j++) {
             f32x4 P = f32x4{0, 0, 0, 0};
@@ -398,8 +389,8 @@ hipError_t by_tile(const Args& p, hipStream_t s) {
 // rows at one expert of 64 x 2048 x 4096 (each pass of 16 rows reads its weight): fp8 128 rows 12.8 / 17.6,
 // 384 30 / 22, 768 57 / 23 (even 96 / 127); mxfp4 128 9.7 / 16.7, 320 18.2 / 16.9 (even 47 / 63).
 bool few_rows(const Args& p, int fmt) {
+  if (!p.offsets) return p.M <= 16 && (p.K >= 16 * 128 || p.N <= 8192);
   const int64_t steps = (fmt == kMXFP4 ? p.K / 2 : p.K) / 128;  // lines of a row
-  if (!p.offsets) return p.M <= 16 && (steps >= 16 || p.N <= 8192);
   return p.M <= (steps >= 32 ? 12 : steps >= 16 ? 6 : 0) * (int64_t)p.groups;
 }
 

@@ -1,6 +1,6 @@
-// Block-scaled GEMM C = A B^T for few rows of A (decode), dense or by expert:
-// MXFP4 x MXFP4, and FP8 x FP8 under fp32 scales per 1 x 128 of A and 128 x 128
-// of B. (The mathematics is gemm_block.hip's.)
+// Block-scaled GEMM C = A B^T for few rows of A (decode): FP8 x FP8 under fp32 scales
+// per 1 x 128 of A and 128 x 128 of B, dense or by expert, and MXFP4 x MXFP4 by
+// expert. (The mathematics is gemm_block.hip's.)
 //
 // Bound by HBM: every weight byte is read once and meets 16 rows of A, so
 // the kernel is a stream of weights from HBM through VGPRs to the matrix core.
@@ -30,6 +30,7 @@
 #include <utility>
 
 #include "bf16.h"
+#include "fp8_encode.h"
 #include "groups.h"
 #include "mx_internal.h"
 
@@ -41,7 +42,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
 // Lane and scalar offsets past every buffer's range (256 rows of at most 2^22
@@ -53,20 +53,10 @@ constexpr int kNonTemporal = 2;                // cache policy of a load: stream
 struct Args {
   const uint8_t *A, *SA, *B, *SB;
   void* C;
-  const int* offsets;  // null: dense (M at most 16)
+  const int* offsets;  // null: dense (FP8, M at most 16)
   int64_t ldc;
   int groups, M, N, K;
 };
-
-// 8 E4M3 codes as bf16.
-__device__ __forceinline__ bf16x8 expand8(int lo, int hi) {
-  u32x4 o;
-  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, false));
-  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.0f, true));
-  o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, false));
-  o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.0f, true));
-  return __builtin_bit_cast(bf16x8, o);
-}
 
 template <typename F, int... K>
 __device__ __forceinline__ void unroll_at(F&& f, std::integer_sequence<int, K...>) {
@@ -90,7 +80,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   const int r = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * (16 * T);
   int group = 0, m0 = 0, mrows = p.M;
-  if (p.offsets && !groups::pass_of(p.offsets, p.groups, p.M, blockIdx.y, group, m0, mrows)) return;
+  if ((!FP8 || p.offsets) && !groups::pass_of(p.offsets, p.groups, p.M, blockIdx.y, group, m0, mrows)) return;
 
   const int nrows = min(p.N - n0, 16 * T);
   const uint32_t rowbytes = (uint32_t)(FP8 ? p.K : p.K / 2);
@@ -227,8 +217,8 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
         f32x4 P = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < 4; h++)
-          P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand8(bv[2 * h], bv[2 * h + 1]),
-                                                      expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
+          P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8::expand8(bv[2 * h], bv[2 * h + 1]),
+                                                      fp8::expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
       } else {

@@ -120,7 +120,7 @@ hipError_t quant_fp8(int fmt, int64_t rows, int64_t cols, const void* x, void* c
 hipError_t dequant_fp8(int fmt, int64_t rows, int64_t cols, const void* codes, const void* scales,
                        int out_dtype, void* y, hipStream_t s);
 
-// ---- gemm_block.hip: C = A B^T, dense (offsets null) or by expert (rows
+// ---- gemm_block.hip: C = A B^T, dense (offsets null; FP8) or by expert (rows
 // offsets[g] .. offsets[g+1]-1 against weight g of `groups`, offsets on the
 // device). fmt: kMXFP4 (both operands) or kFP8B128 (B is kFP8B128X128).
 bool gemm_block_fits(int64_t M, int64_t N, int64_t K, int64_t groups);
