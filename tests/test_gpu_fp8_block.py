@@ -361,3 +361,21 @@ def test_gemm_one_row_into_any_stride(kind):
     assert out.stride() == (1, 1)
     assert mx.gemm(a, b, BF16, out=out) is out
     assert torch.equal(out, mx.gemm(a, b, BF16))
+
+
+@pytest.mark.parametrize("N", [1, 100, 128, 384])
+def test_stack_is_each_weight_by_itself(N):
+    """Codes, scales and dequantized values of a stack; weights of different magnitudes."""
+    require_gpu()
+    G, K = 5, 256
+    x = torch.stack([_mixed(N, K, g) * 4.0**g for g in range(G)])
+    q = mx.quantize(x.cuda(), "fp8_b128x128")
+    assert q.groups == G and tuple(q.codes.shape) == (G * N, K) and tuple(q.scales.shape) == (G, -(-N // 128), K // 128)
+    for out in (F32, BF16):
+        y = mx.dequantize(q, out)
+        assert tuple(y.shape) == (G * N, K)
+        for g in range(G):
+            codes, scales = ref.quantize_fp8(_values(x[g]), True)
+            rows = slice(g * N, (g + 1) * N)
+            assert np.array_equal(host(q.codes[rows]), codes) and np.array_equal(host(q.scales[g]), scales)
+            assert torch.equal(y[rows].cpu(), torch.from_numpy(ref.fp8_values(codes, scales, True)).to(F32).to(out))
