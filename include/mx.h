@@ -283,15 +283,16 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
  * A bf16 output rounds an fp32 value once more (within 2^-8 * |C_ij|); on the
  * 256 x 256-tile kernels that value is one chain over all of K (K / 64 steps
  * for MXFP4, K / 16 for the 16-bit paths, K / 128 for MBS), so before that
- * rounding it errs by at most (steps + c) * 2^-24 * S_ij. The FP8 pair (the
- * products s_A s_B within fp32's range): an
- * fp32 result has chains of 48 blocks of 128 K, each block adding at most 6
- * roundings of its own (c = 6), and so has a bf16 result of few rows (at most
- * 16, by expert at most 12 each on average, where K >= 4096) before its
- * rounding; other bf16 results take P from the FP8 MFMA,
- * which drops low bits of a 128-term sum (measured: of 8 products that it adds
- * together, each loses less than 2^-13 of the largest): at most 2^-10 * S_ij
- * before the rounding, about 2^-16 on quantized normal values. Conditions: no
+ * rounding it errs by at most (steps + c) * 2^-24 * S_ij.
+ * The FP8 pair (the products s_A s_B within fp32's range): an fp32 result has
+ * chains of 48 blocks of 128 K, c = 6 roundings of a block's own, and is within
+ * 2^-18 * S_ij for K <= 67584. A bf16 result of few rows (at most 16, by expert
+ * at most 12 each on average, where K >= 4096) errs by at most
+ * (K / 512 + 21) * 2^-24 * S_ij before its rounding (2^-18 for K <= 22016). Other
+ * bf16 results take P from the FP8 MFMA, which drops low bits of a 128-term sum
+ * (measured: of 8 products that it adds together, each loses less than 2^-13 of
+ * the largest), and err by at most (2^-10 + (K / 128 + 6) * 2^-24) * S_ij before
+ * the rounding; on quantized normal values by about 2^-16. Conditions: no
  * product or partial sum leaves fp32's range; below 2^-126 each fp32 step may
  * lose up to 2^-150 (K * 2^-149 in all); and for MXFP8 / E5M2 / MXFP6
  * operands whose E8M0 byte is at most 2, e * 2^(E-127) must lie on the bf16
@@ -382,7 +383,8 @@ mx_status mx_gemm_noalloc(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   [groups][ceil(N/128)][K/128] (each weight quantized by itself).
  * c: [M][ldc] fp32 or bf16. Limits: M, N <= 2^30, K <= 2^22, groups <= 65535,
  * M K and groups N K <= 2^40, and (M / 64 + min(groups, M)) * N / 128 tiles
- * below 2^23. No workspace. Accuracy as mx_gemm's for the pair.
+ * below 2^23. No workspace. Accuracy as mx_gemm's for the pair; a bf16 MXFP4
+ * result is one chain of K / 64 or K / 128 steps.
  */
 mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, int64_t groups,
                           int64_t M, int64_t N, int64_t K, const int32_t* offsets, const void* a,
