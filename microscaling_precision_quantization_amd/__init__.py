@@ -311,8 +311,8 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
     the layout given; otherwise layout "kpanel" (MXFP4, MXFP8, E5M2, E3M2,
     NVFP4) selects mx_quantize_layout. A [groups][rows][cols] tensor ("mxfp4"
     or "fp8_b128x128", row layout) is a stack of weights for gemm_grouped, each
-    quantized by itself. No rows (but for NVFP4, whose scale is the tensor's) give
-    an empty QTensor, which the calls below take too."""
+    quantized by itself. No rows give an empty QTensor, which dequantize, gemm and
+    gemm_grouped take (not for NVFP4, whose scale is the tensor's, nor by mx_quantize_ex)."""
     import torch
     f = _fmt_id(fmt)
     lay = LAYOUTS[layout]
