@@ -72,10 +72,15 @@ typedef enum {
   MX_FMT_FP8_B128 = 8,    /* E4M3 + one fp32 scale per 1 x 128 elements
                              (activations): block 128, scales fp32
                              [rows][cols/128], aligned to 4 bytes */
-  MX_FMT_FP8_B128X128 = 9 /* E4M3 + one fp32 scale per 128 x 128 tile (weights):
+  MX_FMT_FP8_B128X128 = 9, /* E4M3 + one fp32 scale per 128 x 128 tile (weights):
                              block 128, scales fp32 [ceil(rows/128)][cols/128],
                              aligned to 4 bytes; the last tile of a column may
                              have fewer rows */
+  MX_FMT_INT8 = 10        /* 8-bit integers (two's complement) + one fp32 scale
+                             per row (a token of the activations, an output
+                             channel of a weight): block 0 (the row), cols a
+                             multiple of 16, scales fp32 [rows], aligned to 4
+                             bytes */
 } mx_format;
 
 typedef enum { MX_ROUND_RNE = 0 } mx_round; /* nearest, ties to even */
@@ -120,6 +125,9 @@ typedef enum {
  *     s = fl32(amax / 448) (1 if that is 0), code = the E4M3 value nearest the
  *     exact quotient x / s, ties to the even code, saturating, the sign
  *     copied. A block holding Inf/NaN gets s = NaN and zero codes.
+ *   INT8 (block 0): per row s = fl32(amax / 127) (1 if that is 0), code = the
+ *     integer nearest the exact quotient x / s, ties to even, so in [-127, 127].
+ *     A row holding Inf/NaN gets s = NaN and zero codes.
  * x: bf16 [rows][cols]; codes, scales: outputs as in the layout above.
  * tensor_scale: NVFP4 only, one device fp32 written with s_t; NULL otherwise.
  * workspace: NVFP4 only, device scratch of at least
@@ -218,7 +226,7 @@ mx_status mx_quantize_layout(mx_format fmt, int block, mx_round rnd, int64_t row
  * Dequantization (x_real = S * x_elem on the produtoramaxvision page): MX
  * y = val(code) * 2^(E-127); MXFP4_MBS y = val(code) * 2^(E-127) * (1 + m/256);
  * NVFP4 y = fl32(fl32(val(code) * s_b) * s_t); FP8_B128 and FP8_B128X128
- * y = fl32(val(code) * s).
+ * y = fl32(val(code) * s), INT8 y = fl32(code * s).
  * The fp32 value is the output for MX_OUT_F32; MX_OUT_BF16 rounds it to bf16,
  * nearest-even (overflow gives Inf; E = 255 or an E4M3 NaN scale gives NaN).
  * tensor_scale: NVFP4 only, device pointer to one fp32; NULL otherwise.
@@ -258,6 +266,10 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
  *                       the vector ALU. P comes from bf16 MFMAs on the exactly
  *                       expanded codes; for a bf16 result from the FP8 MFMA,
  *                       but where few rows of A make HBM the bound
+ *   (INT8, INT8, 0)     K a multiple of 16, at most 2^17 - 16, M and N as for
+ *                       FP8: the sum of the codes' products exact in int32
+ *                       (codes of -128, which mx_quantize does not write, too),
+ *                       times s_A s_B
  *   (BF16,  MXFP4, 32)  W4A16: bf16 activations times MXFP4 weights expanded
  *                       exactly to bf16 (weight-only quantization)
  * a: codes (or bf16 for MX_FMT_BF16) [M][...]; a_scales [M][K/block] (NULL for
@@ -267,7 +279,7 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
  * c: [M][ldc] fp32 or bf16 (rnd rounds the bf16 epilogue).
  * workspace: device scratch of at least mx_gemm_workspace_bytes(...) bytes
  * (may be NULL when that is 0).
- * K must be a multiple of 32 for every pair, and at most 65536 for W4A16;
+ * K must be a multiple of 32 for every pair but INT8's, and at most 65536 for W4A16;
  * other shapes return MX_ERR_INVALID_ARG.
  * Accuracy. With S_ij = sum_k |a_ik b_jk| over the dequantized operands, an
  * fp32 output errs from the exact sum by at most (L + c + n - 1) * 2^-24 *
@@ -292,7 +304,10 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
  * bf16 results take P from the FP8 MFMA, which drops low bits of a 128-term sum
  * (measured: of 8 products that it adds together, each loses less than 2^-13 of
  * the largest), and err by at most (2^-10 + (K / 128 + 6) * 2^-24) * S_ij before
- * the rounding; on quantized normal values by about 2^-16. Conditions: no
+ * the rounding; on quantized normal values by about 2^-16. INT8: the exact sum is
+ * converted, multiplied by s_A s_B and that product rounded: an fp32 result errs by
+ * at most 3 * 2^-24 * |C_ij|, whatever the scales (and by 2^-150 where it is below
+ * 2^-126). Conditions: no
  * product or partial sum leaves fp32's range; below 2^-126 each fp32 step may
  * lose up to 2^-150 (K * 2^-149 in all); and for MXFP8 / E5M2 / MXFP6
  * operands whose E8M0 byte is at most 2, e * 2^(E-127) must lie on the bf16
@@ -371,7 +386,8 @@ mx_status mx_gemm_noalloc(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
 /*
  * GEMM by expert: rows offsets[g] .. offsets[g + 1] - 1 of A (sorted by expert)
  * meet weight g, C = A * B_g^T, for g = 0 .. groups - 1. Pairs: (MXFP4, MXFP4,
- * 32) and (FP8_B128, FP8_B128X128, 128); K a multiple of the block.
+ * 32), (FP8_B128, FP8_B128X128, 128) and (INT8, INT8, 0); K a multiple of the block,
+ * INT8's as in mx_gemm.
  * offsets: groups + 1 int32 on the device, aligned to 4 bytes, 0 <= offsets[0]
  *   <= offsets[1] <= ... <= offsets[groups] <= M. They are read by the kernels
  *   only, so a router on the same stream may have just written them, and a
@@ -380,7 +396,7 @@ mx_status mx_gemm_noalloc(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   of that order give undefined rows of C, but no access outside the buffers.
  * a, a_scales: M rows, as in mx_gemm. b: the codes of all weights, [groups][N]
  *   rows; b_scales: MXFP4 [groups][N][K/32], FP8_B128X128
- *   [groups][ceil(N/128)][K/128] (each weight quantized by itself).
+ *   [groups][ceil(N/128)][K/128] (each weight quantized by itself), INT8 [groups][N].
  * c: [M][ldc] fp32 or bf16. Limits: M, N <= 2^30, K <= 2^22, groups <= 65535,
  * M K and groups N K <= 2^40, and (M / 64 + min(groups, M)) * N / 128 tiles
  * below 2^23. No workspace. Accuracy as mx_gemm's for the pair; a bf16 MXFP4

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, "libmx.so")
 
 MX_FMT_BF16, MX_FMT_MXFP4, MX_FMT_MXFP8, MX_FMT_NVFP4 = 0, 1, 2, 3
 MX_FMT_MXFP8_E5M2, MX_FMT_MXFP6_E3M2, MX_FMT_MXFP4_MBS, MX_FMT_MXFP4_MBS16 = 4, 5, 6, 7
-MX_FMT_FP8_B128, MX_FMT_FP8_B128X128 = 8, 9
+MX_FMT_FP8_B128, MX_FMT_FP8_B128X128, MX_FMT_INT8 = 8, 9, 10
 MX_ROUND_RNE = 0
 MX_SCALE_CEIL, MX_SCALE_OAS = 0, 1
 MX_ROTATE_NONE, MX_ROTATE_WHT32 = 0, 1
@@ -30,28 +30,42 @@ MX_LAYOUT_ROWS, MX_LAYOUT_KPANEL = 0, 1
 FORMATS = {"mxfp4": MX_FMT_MXFP4, "mxfp8": MX_FMT_MXFP8, "nvfp4": MX_FMT_NVFP4, "bf16": MX_FMT_BF16,
            "mxfp8_e5m2": MX_FMT_MXFP8_E5M2, "mxfp6_e3m2": MX_FMT_MXFP6_E3M2,
            "mxfp4_mbs": MX_FMT_MXFP4_MBS, "mxfp4_mbs16": MX_FMT_MXFP4_MBS16,
-           "fp8_b128": MX_FMT_FP8_B128, "fp8_b128x128": MX_FMT_FP8_B128X128}
+           "fp8_b128": MX_FMT_FP8_B128, "fp8_b128x128": MX_FMT_FP8_B128X128, "int8": MX_FMT_INT8}
 BLOCK = {MX_FMT_MXFP4: 32, MX_FMT_MXFP8: 32, MX_FMT_NVFP4: 16, MX_FMT_BF16: 32,
          MX_FMT_MXFP8_E5M2: 32, MX_FMT_MXFP6_E3M2: 32, MX_FMT_MXFP4_MBS: 32,
-         MX_FMT_MXFP4_MBS16: 16, MX_FMT_FP8_B128: 128, MX_FMT_FP8_B128X128: 128}
+         MX_FMT_MXFP4_MBS16: 16, MX_FMT_FP8_B128: 128, MX_FMT_FP8_B128X128: 128,
+         MX_FMT_INT8: 0}  # (0: the whole row)
 MBS_FORMATS = (MX_FMT_MXFP4_MBS, MX_FMT_MXFP4_MBS16)
-FP8_BLOCK_FORMATS = (MX_FMT_FP8_B128, MX_FMT_FP8_B128X128)  # fp32 scales
+FP8_BLOCK_FORMATS = (MX_FMT_FP8_B128, MX_FMT_FP8_B128X128)
+F32_SCALE_FORMATS = FP8_BLOCK_FORMATS + (MX_FMT_INT8,)
+STACK_FORMATS = (MX_FMT_MXFP4, MX_FMT_FP8_B128X128, MX_FMT_INT8)  # weights of gemm_grouped
 PAIRS = {MX_FMT_BF16: MX_FMT_MXFP4, MX_FMT_FP8_B128: MX_FMT_FP8_B128X128}  # a GEMM's b, where not a's format
 
 
 def code_cols(fmt, cols):
     """Bytes of codes per row of `cols` elements."""
-    if fmt in (MX_FMT_MXFP8, MX_FMT_MXFP8_E5M2) or fmt in FP8_BLOCK_FORMATS:
+    if fmt in (MX_FMT_MXFP8, MX_FMT_MXFP8_E5M2) or fmt in F32_SCALE_FORMATS:
         return cols
     if fmt == MX_FMT_MXFP6_E3M2:
         return cols * 3 // 4
     return cols // 2
 
+
+def granule(fmt):
+    """Columns are a multiple of this: the block, the 128 elements of a macro
+    block, or the 16 bytes of a load of INT8's rows."""
+    if fmt == MX_FMT_INT8:
+        return 16
+    return 128 if fmt in MBS_FORMATS else BLOCK[fmt]
+
+
 def scale_shape(fmt, rows, cols):
     """Shape of the scales tensor: [rows][cols/block]; for MXFP4-MBS (block 32)
     and MXFP4-MBS16 (block 16) one flat buffer, the E8M0 plane
     [rows][cols/block] followed by the macro mantissa plane [rows][cols/128];
-    for FP8_B128X128 [ceil(rows/128)][cols/128]."""
+    for FP8_B128X128 [ceil(rows/128)][cols/128]; for INT8 [rows]."""
+    if fmt == MX_FMT_INT8:
+        return (rows,)
     if fmt == MX_FMT_FP8_B128X128:
         return (-(-rows // 128), cols // 128)
     if fmt in MBS_FORMATS:
@@ -217,7 +231,8 @@ def status_string(status):
 class QTensor:
     """A block-quantized [rows][cols] tensor: codes, scales and (NVFP4) the
     fp32 tensor scale, all device tensors; layout MX_LAYOUT_KPANEL after pack().
-    Scales are uint8, or float32 for the FP8 block formats. groups: a stack of
+    Scales are uint8, or float32 for the FP8 block formats and INT8 (whose codes'
+    bytes are two's complement). groups: a stack of
     that many [rows / groups][cols] weights, each quantized by itself (the b of
     gemm_grouped)."""
     fmt: int
@@ -239,12 +254,14 @@ def _check_qtensor(q, what):
     buffers of another size, type or layout in memory."""
     import torch
     fmt, codes, scales = q.fmt, q.codes, q.scales
-    if fmt not in BLOCK or fmt == MX_FMT_BF16 or q.cols % BLOCK[fmt] != 0:
+    if fmt not in BLOCK or fmt == MX_FMT_BF16 or q.cols % (granule(fmt) if fmt == MX_FMT_INT8 else BLOCK[fmt]) != 0:
         raise ValueError(f"{what}: not a quantized tensor of a supported format")
     if q.groups < 1 or q.rows % q.groups != 0:
         raise ValueError(f"{what}: {q.rows} rows are not a stack of {q.groups} weights")
     need_c = q.rows * code_cols(fmt, q.cols)
-    if fmt == MX_FMT_FP8_B128X128 or fmt in MBS_FORMATS:
+    if fmt == MX_FMT_INT8:
+        need_s = q.rows
+    elif fmt == MX_FMT_FP8_B128X128 or fmt in MBS_FORMATS:
         need_s = q.groups
         for d in scale_shape(fmt, q.rows // q.groups, q.cols):
             need_s *= d
@@ -252,7 +269,7 @@ def _check_qtensor(q, what):
         need_s = q.rows * (q.cols // BLOCK[fmt])
     if codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.numel() != need_c:
         raise ValueError(f"{what}: codes must be a contiguous uint8 tensor of {need_c} bytes")
-    st, name = (torch.float32, "float32") if fmt in FP8_BLOCK_FORMATS else (torch.uint8, "uint8")
+    st, name = (torch.float32, "float32") if fmt in F32_SCALE_FORMATS else (torch.uint8, "uint8")
     if scales.dtype != st or not scales.is_contiguous() or scales.numel() != need_s:
         raise ValueError(f"{what}: scales must be a contiguous {name} tensor of {need_s} elements")
     if fmt == MX_FMT_NVFP4:
@@ -309,21 +326,21 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
     """Quantize a contiguous bf16 [rows][cols] device tensor. scale_rule "oas"
     (MXFP4) and rotation "wht32" (MXFP4, MXFP8) select mx_quantize_ex, with
     the layout given; otherwise layout "kpanel" (MXFP4, MXFP8, E5M2, E3M2,
-    NVFP4) selects mx_quantize_layout. A [groups][rows][cols] tensor ("mxfp4"
-    or "fp8_b128x128", row layout) is a stack of weights for gemm_grouped, each
+    NVFP4) selects mx_quantize_layout. A [groups][rows][cols] tensor ("mxfp4",
+    "fp8_b128x128" or "int8", row layout) is a stack of weights for gemm_grouped, each
     quantized by itself. No rows give an empty QTensor, which dequantize, gemm and
     gemm_grouped take (not for NVFP4, whose scale is the tensor's, nor by mx_quantize_ex)."""
     import torch
     f = _fmt_id(fmt)
     lay = LAYOUTS[layout]
     if x.dim() == 3:
-        if f not in (MX_FMT_MXFP4, MX_FMT_FP8_B128X128) or lay != MX_LAYOUT_ROWS:
-            raise ValueError("a stack of weights is quantized to mxfp4 or fp8_b128x128 in the row layout")
+        if f not in STACK_FORMATS or lay != MX_LAYOUT_ROWS:
+            raise ValueError("a stack of weights is quantized to mxfp4, fp8_b128x128 or int8 in the row layout")
         if f == MX_FMT_FP8_B128X128:
             return _quantize_tile_stack(x, scale_rule, rotation)
         if not x.is_contiguous():
             raise ValueError("quantize expects a contiguous bfloat16 tensor")
-        q = quantize(x.view(-1, x.shape[2]), fmt, scale_rule, rotation)
+        q = quantize(x.view(x.shape[0] * x.shape[1], x.shape[2]), fmt, scale_rule, rotation)
         q.groups = x.shape[0]
         return q
     if scale_rule != "ceil" or rotation not in (None, "none"):
@@ -342,7 +359,7 @@ def quantize(x, fmt, scale_rule="ceil", rotation=None, layout="rows"):
     dev = x.device
     codes = torch.empty(rows, code_cols(f, cols), dtype=torch.uint8, device=dev)
     scales = torch.empty(*scale_shape(f, rows, cols), device=dev,
-                         dtype=torch.float32 if f in FP8_BLOCK_FORMATS else torch.uint8)
+                         dtype=torch.float32 if f in F32_SCALE_FORMATS else torch.uint8)
     if rows == 0 and f != MX_FMT_NVFP4:
         return _empty(f, cols, codes, scales, lay, "mx_quantize", x)
     ts = ws = None
@@ -365,9 +382,10 @@ def _empty(f, cols, codes, scales, layout, what, *inputs):
     """The QTensor of no rows (a rank that a router sent no tokens): nothing is launched."""
     import torch
     _stream(torch, codes.device, *inputs)
-    granule = 128 if f in MBS_FORMATS else BLOCK[f]
-    if f == MX_FMT_BF16 or cols == 0 or cols % granule != 0:
+    if f == MX_FMT_BF16 or cols == 0 or cols % granule(f) != 0:
         raise MXError(MX_ERR_INVALID_ARG, what)
+    if f == MX_FMT_INT8 and layout != MX_LAYOUT_ROWS:
+        raise MXError(MX_ERR_UNSUPPORTED, what)
     return QTensor(f, 0, cols, codes, scales, None, layout)
 
 
@@ -492,9 +510,9 @@ def gemm(a, b, out_dtype=None, out=None, workspace=None):
 
 
 def gemm_grouped(a, b, offsets, out_dtype=None, out=None):
-    """C = A * B_g^T by expert. a: QTensor [M][K] (mxfp4 or fp8_b128), rows
-    sorted by expert; b: a stack of `groups` [N][K] weights (mxfp4 or
-    fp8_b128x128; quantize of a 3-D tensor); offsets: int32 device tensor of
+    """C = A * B_g^T by expert. a: QTensor [M][K] (mxfp4, fp8_b128 or int8), rows
+    sorted by expert; b: a stack of `groups` [N][K] weights (mxfp4,
+    fp8_b128x128 or int8; quantize of a 3-D tensor); offsets: int32 device tensor of
     groups + 1 nondecreasing row numbers, expert g's rows being offsets[g] ..
     offsets[g + 1] - 1. The offsets are read on the device only. Rows of no
     expert are left as `out` had them (undefined without `out`)."""
@@ -520,7 +538,7 @@ def gemm_grouped(a, b, offsets, out_dtype=None, out=None):
         raise ValueError(f"out must be a [{M}][{N}] {out_dtype} tensor with unit column stride")
     stream = _stream(torch, dev, a.codes, a.scales, b.codes, b.scales, offsets, out)
     if M == 0:
-        pair = a.fmt in (MX_FMT_MXFP4, MX_FMT_FP8_B128) and b.fmt == PAIRS.get(a.fmt, a.fmt)
+        pair = a.fmt in (MX_FMT_MXFP4, MX_FMT_FP8_B128, MX_FMT_INT8) and b.fmt == PAIRS.get(a.fmt, a.fmt)
         _check(MX_OK if pair else MX_ERR_UNSUPPORTED, "mx_gemm_grouped")
         return out
     _check(_on(dev, lib().mx_gemm_grouped, a.fmt, b.fmt, b.block, MX_ROUND_RNE, G, M, N, K, _ptr(offsets),

@@ -20,19 +20,20 @@ bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool is_quant_fmt(int f) {
   return f == MX_FMT_MXFP4 || f == MX_FMT_MXFP8 || f == MX_FMT_NVFP4 || f == MX_FMT_MXFP8_E5M2 ||
          f == MX_FMT_MXFP6_E3M2 || f == MX_FMT_MXFP4_MBS || f == MX_FMT_MXFP4_MBS16 ||
-         f == MX_FMT_FP8_B128 || f == MX_FMT_FP8_B128X128;
+         f == MX_FMT_FP8_B128 || f == MX_FMT_FP8_B128X128 || f == MX_FMT_INT8;
 }
 bool is_mbs(int f) { return f == MX_FMT_MXFP4_MBS || f == MX_FMT_MXFP4_MBS16; }
 bool is_fp8b(int f) { return f == MX_FMT_FP8_B128 || f == MX_FMT_FP8_B128X128; }
 int block_of(int f) {
+  if (f == MX_FMT_INT8) return 0;  // the whole row
   if (is_fp8b(f)) return 128;
   return (f == MX_FMT_NVFP4 || f == MX_FMT_MXFP4_MBS16) ? 16 : 32;
 }
 // fp32 scales need the alignment of a float, the others' bytes are read wide.
-bool scales_aligned(int f, const void* p) { return is_fp8b(f) ? aligned4(p) : aligned16(p); }
+bool scales_aligned(int f, const void* p) { return is_fp8b(f) || f == MX_FMT_INT8 ? aligned4(p) : aligned16(p); }
 // cols (and K) must be a multiple of this: the block, or the 128-element macro
-// block of MXFP4-MBS and MXFP4-MBS16.
-int granule_of(int f) { return is_mbs(f) ? 128 : block_of(f); }  // (the FP8 formats' block is 128)
+// block of MXFP4-MBS and MXFP4-MBS16, or the 16 bytes of a load of INT8's rows.
+int granule_of(int f) { return is_mbs(f) ? 128 : f == MX_FMT_INT8 ? 16 : block_of(f); }  // (the FP8 formats' block is 128)
 
 // Elements per tensor stay below 2^40 and every GEMM extent below 2^30 so that
 // the kernels' index arithmetic (int64 offsets, int extents) cannot overflow.
@@ -53,7 +54,7 @@ int panel_width(int fmt) { return fmt == MX_FMT_MXFP4 ? 256 : 64; }
 
 // Code bytes of a row of cols elements.
 int64_t code_bytes(int fmt, int64_t cols) {
-  if (fmt == MX_FMT_MXFP8 || fmt == MX_FMT_MXFP8_E5M2 || is_fp8b(fmt)) return cols;
+  if (fmt == MX_FMT_MXFP8 || fmt == MX_FMT_MXFP8_E5M2 || is_fp8b(fmt) || fmt == MX_FMT_INT8) return cols;
   if (fmt == MX_FMT_MXFP6_E3M2) return cols * 3 / 4;
   return cols / 2;
 }
@@ -110,6 +111,7 @@ mx_status mx_quantize_layout(mx_format fmt, int block, mx_round rnd, int64_t row
   }
   if (tensor_scale) return MX_ERR_INVALID_ARG;
   if (is_mbs(fmt)) return hip_status(mx::quant_mbs(rows, cols, x, codes, scales, s, block));
+  if (fmt == MX_FMT_INT8) return hip_status(mx::quant_int8(rows, cols, x, codes, scales, s));
   if (is_fp8b(fmt)) return hip_status(mx::quant_fp8(fmt, rows, cols, x, codes, scales, s));
   return hip_status(mx::quant_mx(fmt, rows, cols, x, codes, scales, s, false, false, panel));
 }
@@ -152,6 +154,8 @@ mx_status mx_dequantize(mx_format fmt, int block, mx_round rnd, int64_t rows, in
   } else if (tensor_scale) {
     return MX_ERR_INVALID_ARG;
   }
+  if (fmt == MX_FMT_INT8)
+    return hip_status(mx::dequant_int8(rows, cols, codes, scales, out_dtype, y, (hipStream_t)stream));
   if (is_fp8b(fmt))
     return hip_status(mx::dequant_fp8(fmt, rows, cols, codes, scales, out_dtype, y, (hipStream_t)stream));
   return hip_status(mx::dequant(fmt, rows, cols, codes, scales, tensor_scale, out_dtype, y,
@@ -184,7 +188,8 @@ mx_status gemm_impl(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, i
   const bool mbs = (fmt_a == MX_FMT_MXFP4_MBS && fmt_b == MX_FMT_MXFP4_MBS && block == 32) ||
                    (fmt_a == MX_FMT_MXFP4_MBS16 && fmt_b == MX_FMT_MXFP4_MBS16 && block == 16);
   const bool fp8b = fmt_a == MX_FMT_FP8_B128 && fmt_b == MX_FMT_FP8_B128X128 && block == 128;
-  if (!(w4a4 || w8a8 || nv || w4a16 || alt || mbs || fp8b)) return MX_ERR_UNSUPPORTED;
+  const bool int8 = fmt_a == MX_FMT_INT8 && fmt_b == MX_FMT_INT8 && block == 0;
+  if (!(w4a4 || w8a8 || nv || w4a16 || alt || mbs || fp8b || int8)) return MX_ERR_UNSUPPORTED;
   // K-panel operands: the MXFP4 pair (either operand or both), or both
   // operands of the pairs on the 16-bit MFMAs.
   if ((panel_a || panel_b) && !w4a4 && !((w8a8 || nv || alt) && panel_a && panel_b))
@@ -194,10 +199,10 @@ mx_status gemm_impl(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, i
   if (M <= 0 || N <= 0 || K <= 0 || M > kMaxExtent || N > kMaxExtent || K > kMaxExtent)
     return MX_ERR_INVALID_ARG;
   // K is a whole number of 32-element groups for every path (NVFP4 included:
-  // its 16-blocks are staged in pairs).
-  if (K % 32 != 0 || ((mbs || fp8b) && K % 128 != 0)) return MX_ERR_INVALID_ARG;
+  // its 16-blocks are staged in pairs) but INT8's, of 16-byte loads.
+  if (K % (int8 ? 16 : 32) != 0 || (int8 && K > mx::kInt8MaxK) || ((mbs || fp8b) && K % 128 != 0)) return MX_ERR_INVALID_ARG;
   if (ldc < N) return MX_ERR_INVALID_ARG;
-  if (fp8b && !mx::gemm_block_fits(M, N, K, 0)) return MX_ERR_INVALID_ARG;
+  if ((fp8b || int8) && !mx::gemm_block_fits(M, N, K, 0)) return MX_ERR_INVALID_ARG;
   // Row tiles run along gridDim.y (at most 65535): 128 rows per tile for the
   // W4A4/W8A8 kernels, 16 for W4A16.
   if (M > (w4a16 ? 16 : 128) * (int64_t)65535) return MX_ERR_INVALID_ARG;
@@ -240,6 +245,8 @@ mx_status gemm_impl(mx_format fmt_a, mx_format fmt_b, int block, mx_round rnd, i
     return hip_status(mx::gemm_mx(M, N, K, a, a_scales, b, b_scales, out_dtype, c, ldc, s));
   if (fp8b)
     return hip_status(mx::gemm_block(fmt_a, M, N, K, a, a_scales, b, b_scales, nullptr, 0, out_dtype, c, ldc, s));
+  if (int8)
+    return hip_status(mx::gemm_int8(M, N, K, a, a_scales, b, b_scales, nullptr, 0, out_dtype, c, ldc, s));
   if (mbs)
     return hip_status(mx::gemm_mbs(M, N, K, a, a_scales, b, b_scales, out_dtype, c, ldc, s, block));
   if (w8a8 || nv)
@@ -305,19 +312,23 @@ mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
                           mx_dtype out_dtype, void* c, int64_t ldc, void* stream) {
   const bool w4a4 = fmt_a == MX_FMT_MXFP4 && fmt_b == MX_FMT_MXFP4 && block == 32;
   const bool fp8b = fmt_a == MX_FMT_FP8_B128 && fmt_b == MX_FMT_FP8_B128X128 && block == 128;
-  if (!(w4a4 || fp8b)) return MX_ERR_UNSUPPORTED;
+  const bool int8 = fmt_a == MX_FMT_INT8 && fmt_b == MX_FMT_INT8 && block == 0;
+  if (!(w4a4 || fp8b || int8)) return MX_ERR_UNSUPPORTED;
   if (rnd != MX_ROUND_RNE) return MX_ERR_UNSUPPORTED;
   if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return MX_ERR_UNSUPPORTED;
   if (M <= 0 || N <= 0 || K <= 0 || M > kMaxExtent || N > kMaxExtent || K > kMaxExtent)
     return MX_ERR_INVALID_ARG;
   if (groups <= 0 || groups > kMaxGroups || M > kMaxElems / K || groups * N > kMaxElems / K)
     return MX_ERR_INVALID_ARG;
-  if (K % block != 0 || ldc < N) return MX_ERR_INVALID_ARG;
+  if (K % granule_of(fmt_a) != 0 || (int8 && K > mx::kInt8MaxK) || ldc < N) return MX_ERR_INVALID_ARG;
   if (!mx::gemm_block_fits(M, N, K, groups)) return MX_ERR_INVALID_ARG;
   if (!offsets || !aligned4(offsets)) return MX_ERR_INVALID_ARG;
   if (!a || !a_scales || !b || !b_scales || !c) return MX_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(b) || !aligned16(c)) return MX_ERR_INVALID_ARG;
   if (!scales_aligned(fmt_a, a_scales) || !scales_aligned(fmt_b, b_scales)) return MX_ERR_INVALID_ARG;
+  if (int8)
+    return hip_status(mx::gemm_int8(M, N, K, a, a_scales, b, b_scales, offsets, groups, out_dtype, c, ldc,
+                                    (hipStream_t)stream));
   return hip_status(mx::gemm_block(fmt_a, M, N, K, a, a_scales, b, b_scales, offsets, groups, out_dtype,
                                    c, ldc, (hipStream_t)stream));
 }

@@ -40,7 +40,7 @@ inline hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, siz
 
 // Format ids, kept equal to the public mx_format values.
 enum : int { kBF16 = 0, kMXFP4 = 1, kMXFP8 = 2, kNVFP4 = 3, kMXFP8E5M2 = 4, kMXFP6 = 5, kMXFP4MBS = 6,
-             kMXFP4MBS16 = 7, kFP8B128 = 8, kFP8B128X128 = 9 };
+             kMXFP4MBS16 = 7, kFP8B128 = 8, kFP8B128X128 = 9, kINT8 = 10 };
 enum : int { kOutF32 = 0, kOutBF16 = 1 };
 
 // ---- quantize.hip
@@ -119,6 +119,19 @@ hipError_t quant_fp8(int fmt, int64_t rows, int64_t cols, const void* x, void* c
                      hipStream_t s);
 hipError_t dequant_fp8(int fmt, int64_t rows, int64_t cols, const void* codes, const void* scales,
                        int out_dtype, void* y, hipStream_t s);
+
+// ---- int8_row.hip: 8-bit integers under an fp32 scale per row
+hipError_t quant_int8(int64_t rows, int64_t cols, const void* x, void* codes, void* scales, hipStream_t s);
+hipError_t dequant_int8(int64_t rows, int64_t cols, const void* codes, const void* scales, int out_dtype, void* y,
+                        hipStream_t s);
+
+// ---- gemm_int8.hip: C = A B^T over those, dense (offsets null) or by expert (gemm_block's
+// arguments; its limits on M, N and groups). K: a multiple of 16, at most kInt8MaxK, so
+// that K products of two codes, -128 among them, stay within int32.
+constexpr int64_t kInt8MaxK = ((int64_t)1 << 17) - 16;
+hipError_t gemm_int8(int64_t M, int64_t N, int64_t K, const void* a, const void* sa, const void* b,
+                     const void* sb, const int32_t* offsets, int64_t groups, int out_dtype, void* c,
+                     int64_t ldc, hipStream_t s);
 
 // ---- gemm_block.hip: C = A B^T, dense (offsets null; FP8) or by expert (rows
 // offsets[g] .. offsets[g+1]-1 against weight g of `groups`, offsets on the
