@@ -408,6 +408,37 @@ mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
                           mx_dtype out_dtype, void* c, int64_t ldc, void* stream);
 
 /*
+ * A mixture-of-experts layer for a few tokens, on bf16 activations and quantized
+ * weights, the experts chosen by a router:
+ *   y_t = sum over j < top of weights[t][j] * down_e h,  e = ids[t][j],
+ *   h = silu(gate_e x_t) * (up_e x_t),  silu(v) = v / (1 + exp(-v)).
+ * fmt, block: MXFP4 (32), FP8_B128X128 (128) or INT8 (0), of both weights; hidden and inter
+ *   multiples of the block (INT8: 16), at most 2^20.
+ * tokens <= 64, top <= 32, experts <= 1024 (more tokens: mx_gemm_grouped).
+ * x: bf16 [tokens][ldx], ldx a multiple of 8, at most 2^20. ids: int32 [tokens][top], weights:
+ *   fp32 [tokens][top], on the device, read by the kernels only; an id outside 0 .. experts - 1
+ *   adds nothing (an expert of another rank), and a token may name an expert twice.
+ * up: the codes of [experts][2 inter][hidden], gate_e's rows before up_e's; down: of
+ *   [experts][hidden][inter]; their scales as mx_gemm_grouped's b_scales.
+ * y: [tokens][ldy] fp32 or bf16, ldy a multiple of 4; every row is written (zeros for a token
+ *   without experts).
+ * workspace: device scratch of at least mx_moe_workspace_bytes(...) bytes, 16-byte aligned,
+ *   needing no initialization; calls that may overlap need one each.
+ * Sums are fp32 over exactly expanded codes, in a fixed order; h is rounded to bf16
+ * once. With the products of a row of codes and its scale in fp32's range, and in units
+ * of u = 2^-24: gate_e x and up_e x err by at most (hidden / 16 + 12) u times the sum of their
+ * terms' magnitudes, h then by 2^-8 of itself, and down_e h by (inter / 16 + 12) u times its own.
+ */
+size_t mx_moe_workspace_bytes(int64_t tokens, int64_t top, int64_t experts, int64_t hidden,
+                              int64_t inter);
+
+mx_status mx_moe(mx_format fmt, int block, mx_round rnd, int64_t tokens, int64_t top,
+                 int64_t experts, int64_t hidden, int64_t inter, const void* x, int64_t ldx,
+                 const int32_t* ids, const float* weights, const void* up, const void* up_scales,
+                 const void* down, const void* down_scales, mx_dtype out_dtype, void* y, int64_t ldy,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The norms between two blocks, fused with the residual and the quantizer:
  *   y = x, or post_weight * x * rsqrt(mean(x^2) + eps) (post_weight not NULL)
  *   h = residual + alpha * gate * y

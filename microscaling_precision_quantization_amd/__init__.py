@@ -4,7 +4,7 @@ block-scaled GEMM on AMD Instinct MI355X (gfx950).
 Two layers:
   * mx_quantize, mx_dequantize, mx_gemm, ... : the C ABI (include/mx.h) under
     the same names, taking integers and raw device pointers;
-  * quantize, dequantize, gemm, gemm_grouped, norm_quantize : torch conveniences that allocate outputs on
+  * quantize, dequantize, gemm, gemm_grouped, moe, norm_quantize : torch conveniences that allocate outputs on
     the input's device and pass data_ptr() plus the current HIP stream.
 
 Every step of the computation runs in libmx's HIP kernels. If libmx.so is not
@@ -84,7 +84,8 @@ def mbs_planes(scales, rows, cols, block=32):
 EXPORTS = ("mx_quantize", "mx_quantize_workspace_bytes", "mx_quantize_ex", "mx_quantize_layout",
            "mx_dequantize",
            "mx_gemm", "mx_gemm_workspace_bytes", "mx_last_hip_error", "mx_status_string",
-           "mx_pack", "mx_gemm_ex", "mx_gemm_noalloc", "mx_gemm_grouped", "mx_norm_quantize")
+           "mx_pack", "mx_gemm_ex", "mx_gemm_noalloc", "mx_gemm_grouped", "mx_norm_quantize",
+           "mx_moe", "mx_moe_workspace_bytes")
 
 _lib = None
 
@@ -135,6 +136,10 @@ def lib():
         L.mx_norm_quantize.restype = i32
         L.mx_norm_quantize.argtypes = [i32, i32, i32, i64, i64, P, i64, P, i64, P, i64, P,
                                        ctypes.c_float, P, ctypes.c_float, P, i64, P, P, P, i32]
+        L.mx_moe.restype = i32
+        L.mx_moe.argtypes = [i32, i32, i32, i64, i64, i64, i64, i64, P, i64, P, P, P, P, P, P, i32, P, i64, P, sz, P]
+        L.mx_moe_workspace_bytes.restype = sz
+        L.mx_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
         L.mx_pack.restype = i32
         L.mx_pack.argtypes = [i32, i32, i64, i64, P, P, P, P, P]
         L.mx_gemm_workspace_bytes.restype = sz
@@ -204,6 +209,16 @@ def mx_norm_quantize(fmt, block, rnd, rows, cols, x, ldx, residual, ldr, gate, g
     return lib().mx_norm_quantize(fmt, block, rnd, rows, cols, x, ldx, residual, ldr, gate, gate_rows,
                                   post_weight, alpha, weight, eps, h, ldh, codes, scales, stream,
                                   layout)
+
+
+def mx_moe(fmt, block, rnd, tokens, top, experts, hidden, inter, x, ldx, ids, weights, up, up_scales, down,
+           down_scales, out_dtype, y, ldy, workspace, workspace_bytes, stream):
+    return lib().mx_moe(fmt, block, rnd, tokens, top, experts, hidden, inter, x, ldx, ids, weights, up, up_scales, down,
+                        down_scales, out_dtype, y, ldy, workspace, workspace_bytes, stream)
+
+
+def mx_moe_workspace_bytes(tokens, top, experts, hidden, inter):
+    return lib().mx_moe_workspace_bytes(tokens, top, experts, hidden, inter)
 
 
 def mx_pack(fmt, block, rows, cols, codes, scales, packed_codes, packed_scales, stream):
@@ -545,6 +560,57 @@ def gemm_grouped(a, b, offsets, out_dtype=None, out=None):
                _ptr(a.codes), _ptr(a.scales), _ptr(b.codes), _ptr(b.scales),
                MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, _ptr(out),
                out.stride(0) if M > 1 else N, stream), "mx_gemm_grouped")
+    return out
+
+
+def moe(x, ids, weights, up, down, out_dtype=None, out=None, workspace=None):
+    """A mixture-of-experts layer for a few tokens (at most 64; more: quantize and
+    gemm_grouped), y_t = sum of weights[t][j] * down_e h with h = silu(gate_e x_t) *
+    (up_e x_t) and e = ids[t][j]. x: bf16 [tokens][hidden] with unit column stride and
+    rows that start on 16 bytes; ids: int32, weights: float32, both contiguous
+    [tokens][top] device tensors, read on the device only; an id of no expert (-1: one
+    of another rank) adds nothing. up: a stack of [2 * inter][hidden] weights, each gate
+    above up; down: a stack of [hidden][inter] ones (mxfp4, fp8_b128x128 or int8;
+    quantize of a 3-D tensor), the same format for both. The activations stay bf16:
+    with few tokens the weights' bytes are what a layer costs."""
+    import torch
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    _check_qtensor(up, "moe weight up")
+    _check_qtensor(down, "moe weight down")
+    if up.layout != MX_LAYOUT_ROWS or down.layout != MX_LAYOUT_ROWS:
+        raise ValueError("moe takes weights in the row layout")
+    if up.fmt not in STACK_FORMATS or down.fmt != up.fmt:
+        raise ValueError("moe weights are both mxfp4, both fp8_b128x128 or both int8")
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be a 2-D bfloat16 tensor with unit column stride")
+    T, H = x.shape
+    E, I = up.groups, down.cols
+    if down.groups != E or up.cols != H or down.rows != E * H or up.rows != E * 2 * I:
+        raise ValueError(f"for {E} experts and x of {H} columns, up must be a stack of [2 * inter][{H}] and down of [{H}][inter] weights")
+    for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
+        if t.dtype != dt or t.dim() != 2 or t.shape[0] != T or t.shape != ids.shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dt} tensor of [{T}][top]")
+    top, dev = ids.shape[1], x.device
+    if T > 64:
+        raise ValueError(f"moe takes at most 64 tokens, not {T}: quantize and gemm_grouped take more")
+    if out is None:
+        out = torch.empty(T, H, dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or out.dim() != 2 or tuple(out.shape) != (T, H) or out.stride(1) != 1:
+        raise ValueError(f"out must be a [{T}][{H}] {out_dtype} tensor with unit column stride")
+    stream = _stream(torch, dev, x, ids, weights, up.codes, up.scales, down.codes, down.scales, out, workspace)
+    if T == 0:
+        return out
+    if workspace is None:
+        workspace = torch.empty(mx_moe_workspace_bytes(T, top, E, H, I), dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    # (The row stride of a single row says nothing.)
+    _check(_on(dev, lib().mx_moe, up.fmt, up.block, MX_ROUND_RNE, T, top, E, H, I, _ptr(x), x.stride(0) if T > 1 else H, _ptr(ids),
+               _ptr(weights), _ptr(up.codes), _ptr(up.scales), _ptr(down.codes), _ptr(down.scales),
+               MX_OUT_F32 if out_dtype == torch.float32 else MX_OUT_BF16, _ptr(out), out.stride(0) if T > 1 else H,
+               _ptr(workspace), workspace.numel() * workspace.element_size(), stream), "mx_moe")
     return out
 
 

@@ -40,6 +40,7 @@ int granule_of(int f) { return is_mbs(f) ? 128 : f == MX_FMT_INT8 ? 16 : block_o
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxExtent = (int64_t)1 << 30;
 constexpr int64_t kW4A16MaxK = 65536;
+constexpr int64_t kMoeMaxWidth = (int64_t)1 << 20;  // hidden, inter and x's row stride of mx_moe
 constexpr int64_t kMaxGroups = 65535;  // experts of a grouped GEMM (a grid dimension)
 
 mx_status hip_status(hipError_t e) {
@@ -331,6 +332,35 @@ mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
                                     (hipStream_t)stream));
   return hip_status(mx::gemm_block(fmt_a, M, N, K, a, a_scales, b, b_scales, offsets, groups, out_dtype,
                                    c, ldc, (hipStream_t)stream));
+}
+
+size_t mx_moe_workspace_bytes(int64_t tokens, int64_t top, int64_t experts, int64_t hidden, int64_t inter) {
+  if (tokens <= 0 || top <= 0 || experts <= 0 || hidden <= 0 || inter <= 0) return 0;
+  if (tokens > mx::kMoeMaxTokens || top > mx::kMoeMaxTop || experts > mx::kMoeMaxExperts) return 0;
+  if (hidden > kMoeMaxWidth || inter > kMoeMaxWidth) return 0;
+  return mx::moe_workspace(tokens, top, experts, hidden, inter);
+}
+
+mx_status mx_moe(mx_format fmt, int block, mx_round rnd, int64_t tokens, int64_t top, int64_t experts,
+                 int64_t hidden, int64_t inter, const void* x, int64_t ldx, const int32_t* ids,
+                 const float* weights, const void* up, const void* up_scales, const void* down,
+                 const void* down_scales, mx_dtype out_dtype, void* y, int64_t ldy, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  if ((fmt != MX_FMT_MXFP4 && fmt != MX_FMT_FP8_B128X128 && fmt != MX_FMT_INT8) || block != block_of(fmt)) return MX_ERR_UNSUPPORTED;
+  if (rnd != MX_ROUND_RNE) return MX_ERR_UNSUPPORTED;
+  if (out_dtype != MX_OUT_F32 && out_dtype != MX_OUT_BF16) return MX_ERR_UNSUPPORTED;
+  // (0: a size or a limit)
+  const size_t need = mx_moe_workspace_bytes(tokens, top, experts, hidden, inter);
+  if (need == 0 || hidden % granule_of(fmt) != 0 || inter % granule_of(fmt) != 0) return MX_ERR_INVALID_ARG;
+  if (experts * 2 * inter > kMaxElems / hidden) return MX_ERR_INVALID_ARG;
+  // Rows of x are read 16 bytes at a time at 32-bit offsets, those of y written 4 elements at a time.
+  if (ldx < hidden || ldx % 8 != 0 || ldx > kMoeMaxWidth || ldy < hidden || ldy % 4 != 0 || ldy > kMaxExtent) return MX_ERR_INVALID_ARG;
+  if (!x || !ids || !weights || !up || !up_scales || !down || !down_scales || !y || !workspace) return MX_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned4(ids) || !aligned4(weights) || !aligned16(up) || !aligned16(down) || !aligned16(y)) return MX_ERR_INVALID_ARG;
+  if (!scales_aligned(fmt, up_scales) || !scales_aligned(fmt, down_scales)) return MX_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || workspace_bytes < need) return MX_ERR_INVALID_ARG;
+  return hip_status(mx::moe(fmt, tokens, top, experts, hidden, inter, x, ldx, ids, weights, up, up_scales, down, down_scales,
+                            out_dtype, y, ldy, workspace, (hipStream_t)stream));
 }
 
 mx_status mx_norm_quantize(mx_format fmt, int block, mx_round rnd, int64_t rows, int64_t cols,

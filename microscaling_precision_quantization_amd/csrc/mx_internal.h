@@ -153,6 +153,14 @@ hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a
                          const void* b, const void* sb, const int32_t* offsets, int64_t groups,
                          int out_dtype, void* c, int64_t ldc, hipStream_t s);
 
+// ---- moe.hip: a mixture-of-experts layer for at most kMoeMaxTokens tokens, top experts each,
+// of at most kMoeMaxExperts; fmt (of both weights): kMXFP4, kFP8B128X128 or kINT8.
+constexpr int64_t kMoeMaxTokens = 64, kMoeMaxTop = 32, kMoeMaxExperts = 1024;
+size_t moe_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t hidden, int64_t inter);
+hipError_t moe(int fmt, int64_t tokens, int64_t top, int64_t experts, int64_t hidden, int64_t inter, const void* x, int64_t ldx,
+               const int32_t* ids, const float* weights, const void* up, const void* up_scales, const void* down,
+               const void* down_scales, int out_dtype, void* y, int64_t ldy, void* workspace, hipStream_t s);
+
 // ---- norm_quantize.hip (kMXFP4, kMXFP8 or kFP8B128; cols at most kNormMaxCols;
 // panel: elements per K panel of the codes and scales, 0 for the row layout)
 constexpr int64_t kNormMaxCols = 32768;

@@ -1,0 +1,322 @@
+"""The mixture-of-experts layer for a few tokens against its definition in 64
+bits: layers whose every step is exact bit for bit, others within the roundings of
+their steps."""
+import pytest
+import torch
+
+import microscaling_precision_quantization_amd as mx
+import moe_reference as ref
+from gpu_helpers import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+FMTS = {"mxfp4": mx.MX_FMT_MXFP4, "fp8_b128x128": mx.MX_FMT_FP8_B128X128, "int8": mx.MX_FMT_INT8}
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _whole(fmt, values):
+    """A stack of whole numbers -2 .. 2 [E][rows][cols] in `fmt`, exactly (scales of 1)."""
+    E, rows, cols = values.shape
+    v = values.long()
+    if fmt == "int8":
+        return mx.QTensor(FMTS[fmt], E * rows, cols, (v & 255).to(torch.uint8).view(-1, cols), torch.ones(E * rows, device="cuda"), groups=E)
+    if fmt == "fp8_b128x128":
+        codes = values.float().to(torch.float8_e4m3fn).view(torch.uint8).view(-1, cols)
+        return mx.QTensor(FMTS[fmt], E * rows, cols, codes, torch.ones(E, -(-rows // 128), cols // 128, device="cuda"), groups=E)
+    code = torch.tensor([0, 2, 4], device="cuda")[v.abs()] | (v < 0) * 8
+    code = code.view(E * rows, cols // 2, 2)
+    codes = (code[..., 0] | code[..., 1] << 4).to(torch.uint8)
+    return mx.QTensor(FMTS[fmt], E * rows, cols, codes, torch.full((E * rows, cols // 32), 127, dtype=torch.uint8, device="cuda"), groups=E)
+
+
+def _exact_layer(fmt, T, E, H, I, seed):
+    """x and weights whose gate is 64 (so that silu(gate) = gate in fp32: 1 + exp(-64) is 1),
+    whose up projections are whole numbers of at most 18 and down's of at most 2: every step is
+    exact. Three columns of x besides the first are not zero."""
+    g = _gen(seed)
+    up = torch.randint(-2, 3, (E, 2 * I, H), device="cuda", generator=g)
+    up[:, :I] = 0
+    up[:, :I, 0] = 1
+    up[:, I:, 0] = 0
+    down = torch.randint(-2, 3, (E, H, I), device="cuda", generator=g)
+    x = torch.zeros(T, H, device="cuda")
+    for _ in range(3):
+        x[torch.arange(T), torch.randint(1, H, (T,), device="cuda", generator=g)] = torch.randint(1, 4, (T,), device="cuda", generator=g).float()
+    x[:, 0] = 64
+    return x.bfloat16(), _whole(fmt, up), _whole(fmt, down), up.double(), down.double()
+
+
+def _exact(x, ids, weights, up, down):
+    x, I = x.double(), down.shape[2]
+    y = torch.zeros(x.shape, dtype=torch.float64, device="cuda")
+    for t in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if 0 <= e < up.shape[0]:
+                both = up[e] @ x[t]
+                y[t] += weights[t, j].double() * (down[e] @ (both[:I] * both[I:]))
+    return y
+
+
+def _ids(T, E, top, seed, kind="distinct"):
+    g = _gen(seed)
+    if kind == "distinct":
+        ids = torch.rand(T, E, device="cuda", generator=g).argsort(1)[:, :top]
+    elif kind == "any":  # the same expert twice, and none
+        ids = torch.randint(-2, E + 2, (T, top), device="cuda", generator=g)
+    elif kind == "one":  # all tokens to the last expert
+        ids = torch.full((T, top), E - 1, device="cuda")
+        ids[:, 1:] = -1
+    elif kind == "none":
+        ids = torch.full((T, top), -1, device="cuda")
+        ids[::2] = E
+    ids = ids.to(torch.int32).contiguous()
+    weights = torch.exp2(torch.randint(-3, 2, (T, top), device="cuda", generator=g).float())
+    return ids, weights
+
+
+SIZES = {"mxfp4": [(64, 32), (256, 128), (288, 352), (1056, 416), (2880, 1440)],
+         "fp8_b128x128": [(128, 128), (256, 384), (1408, 256), (2048, 1408)],
+         "int8": [(16, 16), (128, 256), (144, 400), (1040, 336), (2064, 1424)]}
+
+
+@pytest.mark.parametrize("T,E,top,kind", [(1, 1, 1, "distinct"), (1, 32, 8, "distinct"), (4, 64, 6, "distinct"), (17, 5, 2, "distinct"),
+                                          (33, 9, 4, "any"), (64, 3, 3, "distinct"), (64, 70, 8, "any"), (64, 6, 2, "one"), (40, 4, 3, "none"),
+                                          (3, 200, 32, "any")])
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_exact_layers(fmt, T, E, top, kind):
+    require_gpu()
+    for H, I in SIZES[fmt]:
+        if E * H * I > 1 << 27:
+            continue
+        x, up, down, vu, vd = _exact_layer(fmt, T, E, H, I, T + E + H)
+        ids, weights = _ids(T, E, top, T * H + I, kind)
+        y = _exact(x, ids, weights, vu, vd)
+        # |up x| <= 18, so every sum is of multiples of 64 / 8 (the least weight) and of magnitudes below 2^24 of these.
+        assert 64 * 18 * 2 * I * top * 2 < 2**24 * 8
+        got = mx.moe(x, ids, weights, up, down, F32)
+        assert torch.equal(got.double(), y), (H, I)
+        assert torch.equal(mx.moe(x, ids, weights, up, down), y.float().bfloat16())
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("T,E,top", [(1, 8, 2), (5, 12, 4), (31, 6, 3)])
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_random_layers(fmt, T, E, top, out):
+    require_gpu()
+    for H, I in SIZES[fmt][1:]:
+        g = _gen(H + I)
+        x = torch.randn(T, H, device="cuda", generator=g)
+        x[:, torch.rand(H, device="cuda", generator=g) < 0.01] *= 40
+        x = x.bfloat16()
+        up = mx.quantize((torch.randn(E, 2 * I, H, device="cuda", generator=g) * H**-0.5).bfloat16(), fmt)
+        down = mx.quantize((torch.randn(E, H, I, device="cuda", generator=g) * 0.02).bfloat16(), fmt)
+        ids, _ = _ids(T, E, top, H)
+        weights = torch.softmax(torch.randn(T, top, device="cuda", generator=g), 1)
+        y, tol = ref.layer(x, ids, weights, ref.stack_values(up, mx), ref.stack_values(down, mx))
+        ref.check(mx.moe(x, ids, weights, up, down, out), y, tol, out)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_scales(fmt):
+    """Scales that differ from block to block, row to row and expert to expert by powers of two up to 2^40."""
+    require_gpu()
+    T, E, top, H, I = 6, 5, 2, 512, 384
+    x, up, down, _, _ = _exact_layer(fmt, T, E, H, I, 3)
+    x = (x.float() * 2.0**-12).bfloat16()
+    g = _gen(9)
+    for q in (up, down):
+        if fmt == "mxfp4":
+            q.scales.copy_(127 + torch.randint(-20, 20, q.scales.shape, device="cuda", generator=g))
+        else:
+            q.scales.copy_(torch.exp2(torch.randint(-20, 20, q.scales.shape, device="cuda", generator=g).float()))
+    ids, weights = _ids(T, E, top, 1)
+    y, tol = ref.layer(x, ids, weights, ref.stack_values(up, mx), ref.stack_values(down, mx), random=False)
+    for out in (F32, BF16):
+        ref.check(mx.moe(x, ids, weights, up, down, out), y, tol, out)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_nan_stays_with_its_tokens(fmt):
+    """NaN and Inf in a token reach no other; an expert with a NaN scale reaches its own tokens
+    only; infinities next to columns that weights of zero meet give NaN, as 0 * Inf does."""
+    require_gpu()
+    T, E, top, H, I = 20, 4, 2, 288 if fmt == "mxfp4" else 256, 128
+    x, up, down, vu, vd = _exact_layer(fmt, T, E, H, I, 5)
+    ids, weights = _ids(T, E, top, 2)
+    clean = mx.moe(x, ids, weights, up, down, F32)
+    x[3, 7], x[11, H - 1] = float("nan"), float("inf")
+    got = mx.moe(x, ids, weights, up, down, F32)
+    keep = [t for t in range(T) if t not in (3, 11)]
+    assert torch.isnan(got[3]).all() and torch.isnan(got[11]).all() and torch.equal(got[keep], clean[keep])
+    x[3, 7], x[11, H - 1] = 0, 0
+    for q in (up, down):
+        s = q.scales.view(E, -1)
+        old = s[2].clone()
+        s[2] = 255 if fmt == "mxfp4" else float("nan")
+        got = mx.moe(x, ids, weights, up, down, F32)
+        s[2] = old
+        hit = (ids == 2).any(1)
+        again = mx.moe(x, ids, weights, up, down, F32)
+        assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], again[~hit])
+
+
+def test_extreme_gates():
+    """Gates so large either way that exp overflows or vanishes."""
+    require_gpu()
+    H = I = 128
+    up = torch.zeros(1, 2 * I, H, device="cuda")
+    up[0, torch.arange(I), torch.arange(I)] = 1   # gate i = x_i
+    up[0, I:, 0] = 1                              # up i = x_0
+    down = torch.zeros(1, H, I, device="cuda")
+    down[0, torch.arange(H), torch.arange(I)] = 1
+    x = torch.zeros(2, H, device="cuda")
+    x[:, 0] = 2
+    x[0, 1:8] = torch.tensor([-1e4, 1e4, -88.5, -104.0, 88.5, -0.0, 1e37])
+    x[1, 1:4] = torch.tensor([-3e38, -700.0, 0.25])
+    x = x.bfloat16()
+    got = mx.moe(x, torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.ones(2, 1, device="cuda"), _whole("int8", up), _whole("int8", down), F32)
+    v = x.double()
+    want = v * torch.sigmoid(v) * v[:, :1]
+    # (an exponential of 88 has an argument rounded to 2^-18: h is within 2^-15 of itself, then bf16; tiny values to 0)
+    assert ((got.double() - want).abs() <= want.abs() * (2.0**-8 + 2.0**-15) + 1e-37).all()
+
+
+def test_strides_and_out():
+    require_gpu()
+    T, E, top, H, I = 7, 4, 2, 256, 128
+    x, up, down, vu, vd = _exact_layer("mxfp4", T, E, H, I, 8)
+    ids, weights = _ids(T, E, top, 4)
+    y = _exact(x, ids, weights, vu, vd)
+    wide = torch.full((T, H + 24), float("nan"), dtype=BF16, device="cuda")
+    wide[:, 8:8 + H] = x
+    for out in (F32, BF16):
+        dst = torch.full((T + 2, H + 16), 5.0, dtype=out, device="cuda")
+        got = mx.moe(wide[:, 8:8 + H], ids, weights, up, down, out, out=dst[1:1 + T, 4 if out == F32 else 8:][:, :H])
+        assert torch.equal(got.double(), y.to(out).double())
+        at = 4 if out == F32 else 8
+        dst[1:1 + T, at:at + H] = 5
+        assert (dst == 5).all()
+    one = mx.moe(x[:1], ids[:1], weights[:1], up, down, F32, out=torch.zeros(1, H, device="cuda").as_strided((1, H), (3, 1)))
+    assert torch.equal(one.double(), y[:1])
+    with pytest.raises(mx.MXError):  # rows that do not start on 16 bytes
+        mx.moe(torch.zeros(T, H + 4, dtype=BF16, device="cuda")[:, :H], ids, weights, up, down)
+    with pytest.raises(mx.MXError):
+        mx.moe(x, ids, weights, up, down, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(mx.MXError):
+        mx.moe(x, ids[:, :0].contiguous(), weights[:, :0].contiguous(), up, down)
+    assert tuple(mx.moe(x[:0], ids[:0], weights[:0], up, down).shape) == (0, H)
+
+
+def test_workspace():
+    """Any contents of the workspace, and nothing written past it."""
+    require_gpu()
+    T, E, top, H, I = 30, 7, 4, 512, 256
+    x, up, down, vu, vd = _exact_layer("int8", T, E, H, I, 8)
+    n = mx.mx_moe_workspace_bytes(T, top, E, H, I)
+    ws = torch.empty(n + 4096, dtype=torch.uint8, device="cuda")
+    for seed, fill in ((1, 255), (2, 0), (3, 127)):
+        ids, weights = _ids(T, E, top, seed, "any")
+        ws.fill_(fill)
+        got = mx.moe(x, ids, weights, up, down, F32, workspace=ws[:n])
+        assert torch.equal(got.double(), _exact(x, ids, weights, vu, vd))
+        assert (ws[n:] == fill).all()
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_captured(fmt):
+    """Captured once, replayed with other tokens and ids between eager work: the eager result, bit for bit."""
+    require_gpu()
+    T, E, top, H, I = 24, 6, 3, 512, 384
+    x, up, down, _, _ = _exact_layer(fmt, T, E, H, I, 8)
+    ids, weights = _ids(T, E, top, 1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mx.moe(x, ids, weights, up, down)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = mx.moe(x, ids, weights, up, down, F32)
+    for i, kind in enumerate(("distinct", "any", "one", "none", "any")):
+        a, b = _ids(T, E, top, 10 + i, kind)
+        ids.copy_(a)
+        weights.copy_(b * 0.3)
+        x.copy_(torch.randn(T, H, device="cuda", generator=_gen(i)))
+        graph.replay()
+        got = y.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, mx.moe(x, ids, weights, up, down, F32)), i
+        again = mx.moe(x, ids, weights, up, down, F32)
+        assert torch.equal(got, again)
+
+
+def test_two_streams():
+    """Two calls at once, each with its own workspace."""
+    require_gpu()
+    T, E, top, H, I = 16, 6, 3, 1024, 512
+    x, up, down, _, _ = _exact_layer("mxfp4", T, E, H, I, 8)
+    args = [(_ids(T, E, top, s)) for s in range(8)]
+    want = [mx.moe(x, i, w, up, down, F32) for i, w in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for n, (i, w) in enumerate(args):
+        with torch.cuda.stream(streams[n % 2]):
+            got.append(mx.moe(x, i, w, up, down, F32))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_equals_the_products_by_expert():
+    """The same layer by gemm_grouped: rows sorted by expert, the activations in the codes of int8
+    (whole numbers below 128, so exactly), the result the same."""
+    require_gpu()
+    T, E, top, H, I = 48, 5, 2, 256, 160
+    x, up, down, vu, vd = _exact_layer("int8", T, E, H, I, 21)
+    x[:, 0], x[:, 1] = 64, 127   # (a scale of 1 for every row)
+    ids, weights = _ids(T, E, top, 3)
+    order = ids.flatten().long().argsort(stable=True)
+    rows = order // top
+    counts = torch.bincount(ids.flatten().long(), minlength=E)
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+    both = mx.gemm_grouped(mx.quantize(x[rows].contiguous(), "int8"), up, offsets, F32)
+    h = both[:, :I] * both[:, I:]  # (silu(64) = 64)
+    q = mx.quantize((h / 64).bfloat16(), "int8")
+    assert (both[:, :I] == 64).all()
+    part = mx.gemm_grouped(q, down, offsets, F32) * 64 * weights.flatten()[order, None]
+    y = torch.zeros(T, H, device="cuda").index_add_(0, rows, part)
+    got = mx.moe(x, ids, weights, up, down, F32)
+    # h here is rounded to int8's steps, half of amax / 127 each: within that times the weights' magnitudes.
+    step = (h.abs().amax(1, keepdim=True) / 254).double()
+    tol = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    dmag = down.codes.view(torch.int8).double().view(E, H, I).abs().sum(2)
+    tol.index_add_(0, rows, step * dmag[ids.flatten().long()[order]] * weights.flatten()[order, None].double())
+    # (bf16 of h, both ways: 2^-8 of its terms, which are at most 254 of those half steps)
+    assert ((got - y).double().abs() <= tol * 1.02 + 2 * 2.0**-8 * tol * 254).all()
+
+
+def test_experts_past_32_bits():
+    require_gpu()
+    E, H, I = 40, 8192, 4096  # 2.7 GB of up, 1.3 of down
+    g = _gen(0)
+    up = mx.QTensor(mx.MX_FMT_INT8, E * 2 * I, H, torch.randint(0, 256, (E * 2 * I, H), dtype=torch.uint8, device="cuda", generator=g),
+                    torch.full((E * 2 * I,), 1e-4, device="cuda"), groups=E)
+    down = mx.QTensor(mx.MX_FMT_INT8, E * H, I, torch.randint(0, 256, (E * H, I), dtype=torch.uint8, device="cuda", generator=g),
+                      torch.full((E * H,), 1e-4, device="cuda"), groups=E)
+    x = torch.randn(2, H, device="cuda", generator=g).bfloat16()
+    ids = torch.tensor([[39, 0], [20, 39]], dtype=torch.int32, device="cuda")
+    weights = torch.tensor([[0.5, 0.25], [0.75, 0.5]], device="cuda")
+    got = mx.moe(x, ids, weights, up, down, F32)
+    def one(e):
+        a = mx.QTensor(mx.MX_FMT_INT8, 2 * I, H, up.codes[e * 2 * I:(e + 1) * 2 * I], up.scales[:2 * I])
+        b = mx.QTensor(mx.MX_FMT_INT8, H, I, down.codes[e * H:(e + 1) * H], down.scales[:H])
+        return ref.stack_values(a, mx), ref.stack_values(b, mx)
+    us, ds = zip(*(one(e) for e in (0, 20, 39)))
+    small = torch.tensor([[2, 0], [1, 2]], dtype=torch.int32, device="cuda")
+    y, tol = ref.layer(x, small, weights, torch.cat(us), torch.cat(ds))
+    ref.check(got, y, tol, F32)
