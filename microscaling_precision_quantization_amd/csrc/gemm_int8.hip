@@ -164,6 +164,8 @@ __global__ __launch_bounds__(G::kThreads) void gemm_int8_kernel(Args p) {
 // Experts that have rows, and rows each, as far as the host can know.
 int64_t used(const Args& p) { return !p.offsets ? 1 : p.groups < p.M ? p.groups : p.M; }
 
+int64_t rows_each(const Args& p) { return p.M / used(p); }
+
 // Tiles to expect: an expert's last row tile half full.
 int64_t tiles(const Args& p, int bm, int bn) {
   const int64_t tm = p.offsets ? (p.M + used(p) * (bm / 2)) / bm : (p.M + bm - 1) / bm;
@@ -196,6 +198,9 @@ hipError_t gemm_int8(int64_t M, int64_t N, int64_t K, const void* a, const void*
                      const int32_t* offsets, int64_t groups, int out_dtype, void* c, int64_t ldc, hipStream_t s) {
   const Args p{(const uint8_t*)a, (const uint8_t*)b, (const float*)sa, (const float*)sb, c, offsets,
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
+  // Tiles of 256 x 256, for a third of the CUs or more, where most are more than half full.
+  if (rows_each(p) > (offsets ? 64 : 128) && tiles(p, 256, 256) >= 90)
+    return gemm_int8_large(M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
   return out_dtype == kOutF32 ? by_tile<kOutF32>(p, s) : by_tile<kOutBF16>(p, s);
 }
 

@@ -133,6 +133,11 @@ hipError_t gemm_int8(int64_t M, int64_t N, int64_t K, const void* a, const void*
                      const void* sb, const int32_t* offsets, int64_t groups, int out_dtype, void* c,
                      int64_t ldc, hipStream_t s);
 
+// ---- gemm_int8_large.hip (256 x 256 tiles; gemm_int8's arguments)
+hipError_t gemm_int8_large(int64_t M, int64_t N, int64_t K, const void* a, const void* sa, const void* b,
+                           const void* sb, const int32_t* offsets, int64_t groups, int out_dtype, void* c,
+                           int64_t ldc, hipStream_t s);
+
 // ---- gemm_block.hip: C = A B^T, dense (offsets null; FP8) or by expert (rows
 // offsets[g] .. offsets[g+1]-1 against weight g of `groups`, offsets on the
 // device). fmt: kMXFP4 (both operands) or kFP8B128 (B is kFP8B128X128).
