@@ -411,7 +411,7 @@ hipError_t gemm_block(int fmt, int64_t M, int64_t N, int64_t K, const void* a, c
   const Args p{(const uint8_t*)a, (const uint8_t*)sa, (const uint8_t*)b, (const uint8_t*)sb, c, offsets,
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
   const bool f32 = out_dtype == kOutF32;
-  if (few_rows(p, fmt) && gemm_few_rows_fits(M, N, K, offsets ? groups : 0, out_dtype))
+  if (few_rows(p, fmt) && gemm_few_rows_fits(fmt, M, N, K, offsets ? groups : 0, out_dtype))
     return gemm_few_rows(fmt, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
   // Tiles of 256 x 256, for a third of the CUs or more, where most are more than half full.
   // (Times of 256 / the best of the smaller tiles: fp8 1500 x 8192 x 4096 (192 tiles)

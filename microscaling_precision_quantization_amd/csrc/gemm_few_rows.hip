@@ -1,6 +1,7 @@
 // Block-scaled GEMM C = A B^T for few rows of A (decode): FP8 x FP8 under fp32 scales
-// per 1 x 128 of A and 128 x 128 of B, dense or by expert, and MXFP4 x MXFP4 by
-// expert. (The mathematics is gemm_block.hip's.)
+// per 1 x 128 of A and 128 x 128 of B, dense or by expert, MXFP4 x MXFP4 by
+// expert, and INT8 x INT8 under a scale per row, dense or by expert. (The mathematics is
+// gemm_block.hip's and gemm_int8.hip's.)
 //
 // Bound by HBM: every weight byte is read once and meets 16 rows of A, so
 // the kernel is a stream of weights from HBM through VGPRs to the matrix core.
@@ -32,6 +33,7 @@
 #include "bf16.h"
 #include "fp8_encode.h"
 #include "groups.h"
+#include "int8.h"
 #include "mx_internal.h"
 
 namespace mx {
@@ -53,7 +55,7 @@ constexpr int kNonTemporal = 2;                // cache policy of a load: stream
 struct Args {
   const uint8_t *A, *SA, *B, *SB;
   void* C;
-  const int* offsets;  // null: dense (FP8, M at most 16)
+  const int* offsets;  // null: dense (FP8 and INT8, M at most 16)
   int64_t ldc;
   int groups, M, N, K;
 };
@@ -70,22 +72,25 @@ __device__ __forceinline__ void unroll(F&& f) {
 
 // ALIGNED: a row's MXFP4 scales start on dwords (K % 128 = 0).
 // W: waves.
-template <bool FP8, bool ALIGNED, int OUT, int W, int S, int T, int D>
+template <int FMT, bool ALIGNED, int OUT, int W, int S, int T, int D>
 __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
+  constexpr bool FP4 = FMT == kMXFP4, FP8 = FMT == kFP8B128, INT8 = FMT == kINT8;
+  using Sum = typename std::conditional<INT8, int, float>::type;
+  using Sum4 = typename std::conditional<INT8, i32x4, f32x4>::type;
   constexpr int kWaves = W;
   constexpr int kSlot = 2048, kRing = kWaves * D * kSlot, kSums = kWaves * T * 4 * 64 * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kRing > kSums ? kRing : kSums];
-  float(*part)[T][4][64] = (float(*)[T][4][64])smem;
+  Sum(*part)[T][4][64] = (Sum(*)[T][4][64])smem;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * (16 * T);
   int group = 0, m0 = 0, mrows = p.M;
-  if ((!FP8 || p.offsets) && !groups::pass_of(p.offsets, p.groups, p.M, blockIdx.y, group, m0, mrows)) return;
+  if ((FP4 || p.offsets) && !groups::pass_of(p.offsets, p.groups, p.M, blockIdx.y, group, m0, mrows)) return;
 
   const int nrows = min(p.N - n0, 16 * T);
-  const uint32_t rowbytes = (uint32_t)(FP8 ? p.K : p.K / 2);
+  const uint32_t rowbytes = (uint32_t)(FP4 ? p.K / 2 : p.K);
   const int nk = (int)((rowbytes + 127) / 128);
-  const uint32_t sstride = FP8 ? (uint32_t)(nk * 4) : (uint32_t)(p.K / 32);  // scale bytes per row
+  const uint32_t sstride = FP8 ? (uint32_t)(nk * 4) : FP4 ? (uint32_t)(p.K / 32) : 0;  // scale bytes per row
   const int64_t brow = (int64_t)group * p.N + n0;
   const __amdgpu_buffer_rsrc_t rB = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(p.B + brow * rowbytes), 0, (int)((uint32_t)nrows * rowbytes), kRsrcFlags);
@@ -95,11 +100,12 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
       FP8 ? __builtin_amdgcn_make_buffer_rsrc((void*)(p.SB + ((int64_t)group * nbs + nb0) * sstride), 0,
                                               (int)((uint32_t)(nbs - nb0) * sstride), kRsrcFlags)
           : __builtin_amdgcn_make_buffer_rsrc((void*)(p.SB + brow * sstride), 0, (int)((uint32_t)nrows * sstride), kRsrcFlags);
+  // (INT8's scales are the result's, read at the end.)
   // Lane offsets within a tile, for A's fragments (row r, chunks g and g + 4)
   // and for the weights' loads (row l / 8 + 8 h, the chunk that belongs into slot
   // l % 8): the step and the tile go into the scalar offset, which the range
-  // check counts too. In the last step of an MXFP4 row that is no multiple
-  // of 256 K long, chunks past its end are left out.
+  // check counts too. In the last step of an MXFP4 or INT8 row that is no multiple
+  // of 128 bytes long, chunks past its end are left out.
   const uint32_t left = rowbytes - 128u * (uint32_t)(nk - 1);
   uint32_t va[2], va_last[2], vb[2], vb_last[2];
 #pragma unroll
@@ -138,9 +144,9 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
       (void*)(p.A + (int64_t)m0 * rowbytes), 0, (int)((uint32_t)mrows * rowbytes), kRsrcFlags);
   const __amdgpu_buffer_rsrc_t rSA = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(p.SA + (int64_t)m0 * sstride), 0, (int)((uint32_t)mrows * sstride), kRsrcFlags);
-  f32x4 acc[T];
+  Sum4 acc[T];
 #pragma unroll
-  for (int j = 0; j < T; j++) acc[j] = f32x4{0, 0, 0, 0};
+  for (int j = 0; j < T; j++) acc[j] = Sum4{0, 0, 0, 0};
 
   for (int c = 0; c < chunks; c++) {
     const int s0 = (c * kWaves + wave) * S;
@@ -154,7 +160,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
       for (int h = 0; h < 2; h++)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr_t)(ring + (k % D) * kSlot + h * 1024), 16,
                                                  FP8 || s < nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
-      if (!FP8) wsc[k % D] = load_scales(rSB, (uint32_t)(16 * t) * sstride, s);
+      if (FP4) wsc[k % D] = load_scales(rSB, (uint32_t)(16 * t) * sstride, s);
     };
 #pragma unroll
     for (int k = 0; k < D - 1; k++)
@@ -172,7 +178,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
       if (FP8)
         sa[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
             rSA, soff, (int)(s0 + s < nk ? (uint32_t)(s0 + s) * 4u : kScalarOOB), 0));
-      else
+      else if (FP4)
         sc[s] = load_scales(rSA, 0, s0 + s);
     }
     float sb[T];
@@ -187,7 +193,7 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
     // Step k + 1's fragments are read before step k's MFMAs. Loads end in
     // order: step k + 1's have arrived when only the later steps' are out
     // (the first time, A's too, which came last).
-    constexpr int kLoads = FP8 ? 2 : ALIGNED ? 3 : 4;  // of a step
+    constexpr int kLoads = !FP4 ? 2 : ALIGNED ? 3 : 4;  // of a step
     auto arrived = [&](auto n) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("s_waitcnt vmcnt(%0)" ::"i"(decltype(n)::value) : "memory");
@@ -221,6 +227,11 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
                                                       fp8::expand8(a[s][2 * h], a[s][2 * h + 1]), P, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
+      } else if constexpr (INT8) {
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{bv[4 * h], bv[4 * h + 1], bv[4 * h + 2], bv[4 * h + 3]},
+                                                         i32x4{a[s][4 * h], a[s][4 * h + 1], a[s][4 * h + 2], a[s][4 * h + 3]}, acc[t], 0, 0, 0);
       } else {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
@@ -247,15 +258,24 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
   for (int u = 0; u < (T + kWaves - 1) / kWaves; u++) {
     const int j = u * kWaves + wave;
     if (j >= T) break;
-    f32x4 v;
+    Sum4 sum;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
-      v[e] = part[0][j][e][lane];
+      sum[e] = part[0][j][e][lane];
 #pragma unroll
-      for (int w = 1; w < kWaves; w++) v[e] += part[w][j][e][lane];
+      for (int w = 1; w < kWaves; w++) sum[e] += part[w][j][e][lane];
     }
     const int col = n0 + 16 * j + 4 * g;
     if (r >= mrows) continue;
+    f32x4 v;
+    if constexpr (INT8) {
+      const int8::Scale sa = int8::split(((const float*)p.SA)[m0 + r]);
+      const float* sb = (const float*)p.SB + (int64_t)group * p.N + col;
+#pragma unroll
+      for (int e = 0; e < 4; e++) v[e] = int8::apply(sum[e], sa, int8::split(col + e < p.N ? sb[e] : 0.0f));
+    } else {
+      v = sum;
+    }
     const int64_t at = (int64_t)(m0 + r) * p.ldc + col;
     if (p.ldc % 4 == 0 && col + 4 <= p.N) {
       if (OUT == kOutF32)
@@ -278,26 +298,26 @@ __global__ __launch_bounds__(64 * W) void gemm_few_rows_kernel(Args p) {
 // Passes of 16 rows that any offsets can need (dense: one).
 int64_t passes(int64_t M, int64_t groups) { return groups > 0 ? groups::max_row_tiles(M, groups, 16) : 1; }
 
-template <bool FP8, bool ALIGNED, int OUT, int W, int S, int T, int D>
+template <int FMT, bool ALIGNED, int OUT, int W, int S, int T, int D>
 hipError_t launch(const Args& p, hipStream_t s) {
   const dim3 grid((unsigned)((p.N + 16 * T - 1) / (16 * T)), (unsigned)passes(p.M, p.offsets ? p.groups : 0));
-  return launch_kernel(&gemm_few_rows_kernel<FP8, ALIGNED, OUT, W, S, T, D>, grid, 64 * W, 0, s, p);
+  return launch_kernel(&gemm_few_rows_kernel<FMT, ALIGNED, OUT, W, S, T, D>, grid, 64 * W, 0, s, p);
 }
 
 // Rounds of the 256 CUs that workgroups of T tiles make, one a CU at a time.
 int64_t rounds(int64_t tiles, int T) { return (tiles + 256 * T - 1) / (256 * T); }
 
 // Experts that have rows are taken as min(groups, M). Times in us at 16 rows,
-// FP8, N x K (by expert: rows over experts x N x K).
-template <bool FP8, bool ALIGNED, int OUT>
+// FP8, N x K (by expert: rows over experts x N x K); INT8's rows are as long.
+template <int FMT, bool ALIGNED, int OUT>
 hipError_t dispatch(const Args& p, hipStream_t s) {
-  if constexpr (FP8) {
+  if constexpr (FMT != kMXFP4) {
     const int64_t tiles = (p.N + 15) / 16 * (!p.offsets ? 1 : p.M < p.groups ? p.M : p.groups);
-    const int nk = p.K / 128;
+    const int nk = (p.K + 127) / 128;
     if (p.offsets) {
       // Few experts with rows: 4 waves on long runs (8 rows over 32 x 2048 x 4096: 12.0,
       // below 14.7; 128 over 64: 60.2 and 59.2, 32 over 16 x 4096 x 7168: 79 and 65).
-      if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, s);
+      if (nk > 16 && tiles >= 512 && tiles < 2048) return launch<FMT, ALIGNED, OUT, 4, 8, 2, 8>(p, s);
     } else {
       // Long rows, many of them: 7 tiles share A in a workgroup of 8 waves, one a CU, or 4 in one
       // of 4 waves (below), whichever's rounds of CUs take fewer tiles (K = 8192, N = 14336 / 18432 /
@@ -305,36 +325,36 @@ hipError_t dispatch(const Args& p, hipStream_t s) {
       // 113 / 172, 4 tiles 24 / 38 / 40 / 41 / 45 / 59 / 78 / 86 / 119 / 167; K = 4096, N = 18432 / 28672: 21 / 26
       // and 21 / 23).
       if (nk >= 48 && tiles > 768 && 7 * rounds(tiles, 7) <= 4 * rounds(tiles, 4))
-        return launch<FP8, ALIGNED, OUT, 8, 8, 7, 8>(p, s);
+        return launch<FMT, ALIGNED, OUT, 8, 8, 7, 8>(p, s);
       // The fewest tiles a workgroup that need one round of CUs (T = 1 / 2 / 3:
       // 4096 x 4096 6.6 / 7.3 / 8.7, 6144 x 4096 9.7 / 7.6 / 9.2, 10240 x 8192 - / 24.9 / 16.8;
       // 14336 x 4096: 13.6, with T = 2 13.9, T = 3 16.5).
-      if (tiles <= 256) return launch<FP8, ALIGNED, OUT, 8, 2, 1, 3>(p, s);
+      if (tiles <= 256) return launch<FMT, ALIGNED, OUT, 8, 2, 1, 3>(p, s);
       // (8192 x 28672: 4 waves on long runs 44.4, T = 2 46.5; one row 37.2 and 41.5.)
-      if (tiles <= 512 && nk >= 128) return launch<FP8, ALIGNED, OUT, 4, 8, 2, 8>(p, s);
-      if (tiles > 512 && tiles <= 768) return launch<FP8, ALIGNED, OUT, 8, 1, 3, 4>(p, s);
-      if (tiles > 768 && nk > 16) return launch<FP8, ALIGNED, OUT, 4, 8, 4, 9>(p, s);
+      if (tiles <= 512 && nk >= 128) return launch<FMT, ALIGNED, OUT, 4, 8, 2, 8>(p, s);
+      if (tiles > 512 && tiles <= 768) return launch<FMT, ALIGNED, OUT, 8, 1, 3, 4>(p, s);
+      if (tiles > 768 && nk > 16) return launch<FMT, ALIGNED, OUT, 4, 8, 4, 9>(p, s);
     }
   }
   // Two tiles, a step of each in a wave's chunk: eight waves on one run of a row
   // (mxfp4 128 over 64 x 2048 x 4096: 35.4, with 4 waves on runs of 4 steps 42.9, four tiles 37.7).
-  return launch<FP8, ALIGNED, OUT, 8, 1, 2, 3>(p, s);
+  return launch<FMT, ALIGNED, OUT, 8, 1, 2, 3>(p, s);
 }
 
 template <bool ALIGNED>
 hipError_t mxfp4(const Args& p, bool f32, hipStream_t s) {
-  if (f32) return dispatch<false, ALIGNED, kOutF32>(p, s);
-  return dispatch<false, ALIGNED, kOutBF16>(p, s);
+  if (f32) return dispatch<kMXFP4, ALIGNED, kOutF32>(p, s);
+  return dispatch<kMXFP4, ALIGNED, kOutBF16>(p, s);
 }
 
 }  // namespace
 
-// fp32 results: accumulation chains of at most 48 matrix instructions or scale
+// fp32 results but INT8's: accumulation chains of at most 48 matrix instructions or scale
 // blocks, of 128 K, in a wave.
-bool gemm_few_rows_fits(int64_t M, int64_t N, int64_t K, int64_t groups, int out_dtype) {
+bool gemm_few_rows_fits(int fmt, int64_t M, int64_t N, int64_t K, int64_t groups, int out_dtype) {
   // (The grid: 16 columns a workgroup across, passes down.)
   if (N > ((int64_t)1 << 27) || passes(M, groups) > 65535) return false;
-  return out_dtype != kOutF32 || K <= (int64_t)48 * 128 * 4;
+  return fmt == kINT8 || out_dtype != kOutF32 || K <= (int64_t)48 * 128 * 4;
 }
 
 hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
@@ -344,7 +364,8 @@ hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a
                ldc, (int)groups, (int)M, (int)N, (int)K};
   const bool f32 = out_dtype == kOutF32;
   if (fmt == kMXFP4) return K % 128 == 0 ? mxfp4<true>(p, f32, s) : mxfp4<false>(p, f32, s);
-  return f32 ? dispatch<true, true, kOutF32>(p, s) : dispatch<true, true, kOutBF16>(p, s);
+  if (fmt == kINT8) return f32 ? dispatch<kINT8, true, kOutF32>(p, s) : dispatch<kINT8, true, kOutBF16>(p, s);
+  return f32 ? dispatch<kFP8B128, true, kOutF32>(p, s) : dispatch<kFP8B128, true, kOutBF16>(p, s);
 }
 
 }  // namespace mx

@@ -192,12 +192,20 @@ hipError_t by_tile(const Args& p, hipStream_t s) {
   return launch<OUT, Geo<1, 1, 2, 2, 4>>(p, s);
 }
 
+// Few rows of A: a stream of weights, which needs long rows of them.
+bool few_rows(const Args& p) {
+  if (!p.offsets) return p.M <= 16 && (p.K >= 16 * 128 || p.N <= 8192);
+  return p.M <= (p.K >= 32 * 128 ? 12 : p.K >= 16 * 128 ? 6 : 0) * (int64_t)p.groups;
+}
+
 }  // namespace
 
 hipError_t gemm_int8(int64_t M, int64_t N, int64_t K, const void* a, const void* sa, const void* b, const void* sb,
                      const int32_t* offsets, int64_t groups, int out_dtype, void* c, int64_t ldc, hipStream_t s) {
   const Args p{(const uint8_t*)a, (const uint8_t*)b, (const float*)sa, (const float*)sb, c, offsets,
                ldc, (int)groups, (int)M, (int)N, (int)K, 0};
+  if (few_rows(p) && gemm_few_rows_fits(kINT8, M, N, K, offsets ? groups : 0, out_dtype))
+    return gemm_few_rows(kINT8, M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);
   // Tiles of 256 x 256, for a third of the CUs or more, where most are more than half full.
   if (rows_each(p) > (offsets ? 64 : 128) && tiles(p, 256, 256) >= 90)
     return gemm_int8_large(M, N, K, a, sa, b, sb, offsets, groups, out_dtype, c, ldc, s);

@@ -152,8 +152,8 @@ hipError_t gemm_fp8_large(int64_t M, int64_t N, int64_t K, const void* a, const 
                           hipStream_t s);
 
 // ---- gemm_few_rows.hip (few rows of A, or few per expert: weights streamed
-// once per 16 rows; gemm_block's shapes and arguments)
-bool gemm_few_rows_fits(int64_t M, int64_t N, int64_t K, int64_t groups, int out_dtype);
+// once per 16 rows; gemm_block's or (fmt kINT8) gemm_int8's shapes and arguments)
+bool gemm_few_rows_fits(int fmt, int64_t M, int64_t N, int64_t K, int64_t groups, int out_dtype);
 hipError_t gemm_few_rows(int fmt, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
                          const void* b, const void* sb, const int32_t* offsets, int64_t groups,
                          int out_dtype, void* c, int64_t ldc, hipStream_t s);
