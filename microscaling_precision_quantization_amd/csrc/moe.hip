@@ -81,9 +81,11 @@ __device__ __forceinline__ void unroll(F&& f) {
   unroll_at(std::forward<F>(f), std::make_integer_sequence<int, N>{});
 }
 
-// 8 MXFP4 codes times 2^(E - 127) as bf16 (E = 255: NaN).
-__device__ __forceinline__ bf16x8 expand_fp4(uint32_t q, uint32_t E) {
-  const float s = __builtin_bit_cast(float, E == 0 ? 0x00400000u : E << 23);
+// 8 MXFP4 codes times 2^(E - 127) as bf16 (E = 255: NaN), E byte j of `scales`.
+__device__ __forceinline__ bf16x8 expand_fp4(uint32_t q, uint32_t scales, int j) {
+  uint32_t e = (j < 3 ? scales << (23 - 8 * j) : scales >> 1) & 0x7F800000u;
+  e = e > 0x00400000u ? e : 0x00400000u;  // (E = 0: 2^-127, a subnormal)
+  const float s = __builtin_bit_cast(float, e);
   u32x4 o;
   o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
   o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
@@ -106,6 +108,14 @@ __device__ __forceinline__ bf16x8 expand_int8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, o);
 }
 
+// v or-ed over the four lanes of the same l % 16.
+__device__ __forceinline__ uint32_t or_over_rows(uint32_t v) {
+  auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = a[0] | a[1];
+  a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return a[0] | a[1];
+}
+
 // Sums of one workgroup: rows of A (bf16; lane (r, g) supplies row r, whose bytes
 // begin at lane offset `arow` of rA, or kOOB) times T tiles of 16 weight rows, K
 // elements each. Tile t's codes begin at row tile_row(t) of view(t); the views end with
@@ -116,7 +126,7 @@ struct Stream {
   static constexpr bool FP4 = FMT == kMXFP4, FP8 = FMT == kFP8B128X128;
   static constexpr int kSlot = 2048, kRing = W * D * kSlot, kSums = W * T * 4 * 64 * 4;
   static constexpr int kSmem = kRing > kSums ? kRing : kSums;
-  static constexpr int kFrags = FP4 ? 8 : 4;  // of A, 16 bytes each, in a step
+  static constexpr int kFrags = FP4 ? 8 : 4;  // MFMAs of a step, of 32 K each
 
   template <class View, class ScaleView, class TileRow, class Fp8Row>
   static __device__ __forceinline__ void run(uint8_t* smem, int K, __amdgpu_buffer_rsrc_t rA, uint32_t arow, View view,
@@ -139,10 +149,15 @@ struct Stream {
     const uint32_t soff = (uint32_t)r * sstride;
     const int chunks = (nk + W * S - 1) / (W * S);
     uint8_t* ring = smem + wave * (D * kSlot);
-    const int frag0 = r * 128 + ((g ^ (r >> 1)) & 7) * 16, frag1 = r * 128 + (((g + 4) ^ (r >> 1)) & 7) * 16;
+    // MFMA j takes the step's elements 32 j .. 32 j + 31, lane (r, g) 8 of row r from
+    // 32 j + 8 g on: of A 64 bytes of each row together in one load, of the codes 4 (MXFP4) or 8 bytes
+    // at an address of slots that j changes in its own bits only.
+    const int frag = FP4 ? r * 128 + ((r >> 1) & 7) * 16 + 4 * g : r * 128 + (((r >> 1) & 7) ^ (g >> 1)) * 16 + 8 * (g & 1);
+    const uint32_t alane = arow == kOOB ? kOOB : arow + 16u * (uint32_t)g;
+    const uint32_t alane_half = g < 2 ? alane : kOOB;  // INT8: K may end in the middle of 32
 
-    // MXFP4: the scales of step s, blocks 0..3 and 4..7 (this lane uses byte g of
-    // each dword), without the bytes past the row's end, which are another row's.
+    // MXFP4: the scales of step s's 8 blocks, without the bytes past the row's end, which are
+    // another row's.
     auto load_scales = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, int s) __attribute__((always_inline)) {
       const uint32_t so = s < nk ? row + (uint32_t)s * 8u : kScalarOOB;
       if (ALIGNED) {
@@ -153,7 +168,7 @@ struct Stream {
       const uint32_t b = (uint32_t)s * 8u + (uint32_t)g;
       const uint32_t x = __builtin_amdgcn_raw_buffer_load_b8(rs, b < sstride ? soff + g : kOOB, (int)so, 0);
       const uint32_t y = __builtin_amdgcn_raw_buffer_load_b8(rs, b + 4u < sstride ? soff + 4u + g : kOOB, (int)so, 0);
-      return u32x2{x << (8 * g), y << (8 * g)};
+      return u32x2{x << (8 * g), y << (8 * g)};  // (of the lanes of a row together)
     };
 
     f32x4 acc[T];
@@ -176,17 +191,15 @@ struct Stream {
 #pragma unroll
       for (int k = 0; k < D - 1; k++)
         if (k < T * S) load(k);
-      // A's fragments: of chunk g, then of chunk g + 4, of the step, in the order of the codes there.
+      // A's fragments. (The step and MFMA go into the scalar offset.)
       u32x4 a[S][kFrags];
 #pragma unroll
       for (int s = 0; s < S; s++)
 #pragma unroll
         for (int i = 0; i < kFrags; i++) {
-          constexpr uint32_t kChunk = FP4 ? 64 : 32;  // A's bytes of a 16-byte chunk of codes
-          constexpr int kPer = kChunk / 16;
-          const uint32_t chunk = (uint32_t)(s0 + s) * 8u + (uint32_t)(i / kPer * 4 + g);
-          const uint32_t off = chunk * 16u < rowbytes && arow != kOOB ? arow + chunk * kChunk + 16u * (uint32_t)(i % kPer) : kOOB;
-          a[s][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rA, off, 0, 0));
+          const int k = ((s0 + s) * kFrags + i) * 32;
+          a[s][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              rA, FMT != kINT8 || k + 32 <= K ? alane : alane_half, k < K ? k * 2 : (int)kScalarOOB, 0));
         }
       float sb[T];
       if (FP8) {
@@ -206,18 +219,29 @@ struct Stream {
         __builtin_amdgcn_sched_barrier(0);
       };
       struct Codes {
-        u32x4 h[2];
+        uint32_t q[8];
       };
       auto read = [&](int k) __attribute__((always_inline)) {
         const uint8_t* at = ring + (k % D) * kSlot;
-        return Codes{{*(const u32x4*)(at + frag0), *(const u32x4*)(at + frag1)}};
+        Codes c;
+#pragma unroll
+        for (int j = 0; j < kFrags; j++) {
+          if constexpr (FP4) {
+            c.q[j] = *(const uint32_t*)(at + (frag ^ (16 * j)));
+          } else {
+            const u32x2 v = *(const u32x2*)(at + (frag ^ (32 * j)));
+            c.q[2 * j] = v.x;
+            c.q[2 * j + 1] = v.y;
+          }
+        }
+        return c;
       };
       arrived(std::integral_constant<int, 0>{});
       Codes next = read(0);
       unroll<T * S>([&](auto kk) __attribute__((always_inline)) {
         constexpr int k = decltype(kk)::value, t = k / S, s = k % S;
         const Codes bv = next;
-        const u32x2 wscale = wsc[k % D];
+        u32x2 wscale = wsc[k % D];
         if (k + D - 1 < T * S) load(k + D - 1);
         if constexpr (k + 1 < T * S) {
           // Steps loaded behind k + 1 (the first D - 1 have all arrived).
@@ -227,21 +251,15 @@ struct Stream {
           next = read(k + 1);
         }
         f32x4 P = FP8 ? f32x4{0, 0, 0, 0} : acc[t];
+        if (FP4 && !ALIGNED) wscale = u32x2{or_over_rows(wscale.x), or_over_rows(wscale.y)};
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          if constexpr (FP4) {
-            const uint32_t E = (wscale[h] >> (8 * g)) & 0xFFu;
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand_fp4(bv.h[h][i], E), __builtin_bit_cast(bf16x8, a[s][4 * h + i]), P, 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-              const uint32_t lo = bv.h[h][2 * i], hi = bv.h[h][2 * i + 1];
-              P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(FP8 ? fp8::expand8((int)lo, (int)hi) : expand_int8(lo, hi),
-                                                          __builtin_bit_cast(bf16x8, a[s][2 * h + i]), P, 0, 0, 0);
-            }
-          }
+        for (int j = 0; j < kFrags; j++) {
+          bf16x8 w;
+          if constexpr (FP4)
+            w = expand_fp4(bv.q[j], wscale[j / 4], j % 4);
+          else
+            w = FP8 ? fp8::expand8((int)bv.q[2 * j], (int)bv.q[2 * j + 1]) : expand_int8(bv.q[2 * j], bv.q[2 * j + 1]);
+          P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, a[s][j]), P, 0, 0, 0);
         }
         if constexpr (FP8) {
           const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb[t]), s));
