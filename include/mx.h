@@ -413,7 +413,7 @@ mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   y_t = sum over j < top of weights[t][j] * down_e h,  e = ids[t][j],
  *   h = silu(gate_e x_t) * (up_e x_t),  silu(v) = v / (1 + exp(-v)).
  * fmt, block: MXFP4 (32), FP8_B128X128 (128) or INT8 (0), of both weights; hidden and inter
- *   multiples of the block (INT8: 16), at most 2^20.
+ *   multiples of the block (INT8: 16), at most 2^20, their product at most 2^30.
  * tokens <= 64, top <= 32, experts <= 1024 (more tokens: mx_gemm_grouped).
  * x: bf16 [tokens][ldx], ldx a multiple of 8, at most 2^20. ids: int32 [tokens][top], weights:
  *   fp32 [tokens][top], on the device, read by the kernels only; an id outside 0 .. experts - 1

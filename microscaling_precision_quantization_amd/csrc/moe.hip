@@ -34,6 +34,7 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 using fp8::bf16x8;
@@ -47,7 +48,7 @@ constexpr int kNonTemporal = 2;                // cache policy of a load: stream
 constexpr int W = 8;                           // waves of a workgroup
 
 // Where the parts of the workspace are: the number of passes, the passes, each slot's
-// row (-1: no expert of this call's), h and the partial results.
+// row (of ids of experts), h and the partial results.
 struct Pass {
   int expert, row, rows, unused;  // first row, rows
 };
@@ -81,11 +82,11 @@ __device__ __forceinline__ void unroll(F&& f) {
   unroll_at(std::forward<F>(f), std::make_integer_sequence<int, N>{});
 }
 
-// 8 MXFP4 codes times 2^(E - 127) as bf16 (E = 255: NaN), E byte j of `scales`.
-__device__ __forceinline__ bf16x8 expand_fp4(uint32_t q, uint32_t scales, int j) {
-  uint32_t e = (j < 3 ? scales << (23 - 8 * j) : scales >> 1) & 0x7F800000u;
-  e = e > 0x00400000u ? e : 0x00400000u;  // (E = 0: 2^-127, a subnormal)
-  const float s = __builtin_bit_cast(float, e);
+// 8 MXFP4 codes times 2^(E - 127) as bf16 (E = 255: NaN), E in `scale`'s bits 30:23. The scaled
+// converts read nothing else of their scale (checked for every E, 0 and 255 among them, with
+// any sign and significand), so what lies beside E may stay.
+__device__ __forceinline__ bf16x8 expand_fp4(uint32_t q, uint32_t scale) {
+  const float s = __builtin_bit_cast(float, scale);
   u32x4 o;
   o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
   o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
@@ -108,34 +109,41 @@ __device__ __forceinline__ bf16x8 expand_int8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, o);
 }
 
-// v or-ed over the four lanes of the same l % 16.
-__device__ __forceinline__ uint32_t or_over_rows(uint32_t v) {
-  auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  v = a[0] | a[1];
-  a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  return a[0] | a[1];
-}
+// What a workgroup does of one pass: `n` tiles of 16 weight rows, tile t of kind t % KINDS (the
+// gate's and the up projection's rows) from row 16 (t / KINDS) of its kind's view on. The views end
+// with the tiles there are. A's view and lane (r, g)'s row's first byte in it (kOOB: no such row).
+// Scales: MXFP4 a view of the tiles' rows, FP8 of all scales of the expert's kind, the views' first
+// row being row `row0` there.
+template <int KINDS>
+struct Segment {
+  __amdgpu_buffer_rsrc_t rA, rB[KINDS], rS[KINDS];
+  uint32_t arow;
+  int n, row0;
+  Pass pass;
+};
 
-// Sums of one workgroup: rows of A (bf16; lane (r, g) supplies row r, whose bytes
-// begin at lane offset `arow` of rA, or kOOB) times T tiles of 16 weight rows, K
-// elements each. Tile t's codes begin at row tile_row(t) of view(t); the views end with
-// the rows there are. `sum(t, column e)` of lane (r, g) of wave t % W, afterwards: row r,
-// columns 4 g + e of tile t.
-template <int FMT, bool ALIGNED, int S, int T, int D>
+// The products of a workgroup: its segments' rows of A (bf16) times their weight rows, K elements
+// each. Wave w takes the K steps w, w + W, ..., S of them; a row of more than W S steps takes several
+// rounds (MULTI). next(segment) gives one segment after the other, false behind the last.
+// G tiles at a time, done(segment, first tile, sums) is called with the waves' sums in LDS,
+// sums[wave][tile][lane]: lane (r, g)'s row r, columns 4 g .. 4 g + 3 of the tile.
+template <int FMT, bool ALIGNED, int KINDS, int S, bool MULTI>
 struct Stream {
   static constexpr bool FP4 = FMT == kMXFP4, FP8 = FMT == kFP8B128X128;
-  static constexpr int kSlot = 2048, kRing = W * D * kSlot, kSums = W * T * 4 * 64 * 4;
-  static constexpr int kSmem = kRing > kSums ? kRing : kSums;
+  static constexpr int D = 4, G = S == 4 ? 4 : 8;
+  static constexpr int kSlot = 2048, kRing = W * D * kSlot, kSums = W * G * 1024, kSmem = kRing + kSums;
   static constexpr int kFrags = FP4 ? 8 : 4;  // MFMAs of a step, of 32 K each
+  static constexpr int kLoads = FP4 ? (ALIGNED ? 3 : 4) : FP8 ? 3 : 2;  // of a tile's step
+  static_assert(G * S % D == 0 && G % KINDS == 0, "the ring's slots and the tiles' kinds are those of a place in the group");
+  using Seg = Segment<KINDS>;
 
-  template <class View, class ScaleView, class TileRow, class Fp8Row>
-  static __device__ __forceinline__ void run(uint8_t* smem, int K, __amdgpu_buffer_rsrc_t rA, uint32_t arow, View view,
-                                             ScaleView sview, TileRow tile_row, Fp8Row fp8_row) {
+  template <class Next, class Done>
+  static __device__ __forceinline__ void run(uint8_t* smem, int K, Next next_segment, Done done) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const uint32_t rowbytes = (uint32_t)(FP4 ? K / 2 : K);
     const int nk = (int)((rowbytes + 127) / 128);
-    const uint32_t sstride = (uint32_t)(K / 32);  // MXFP4: scale bytes per row
+    const uint32_t sstride = FP8 ? (uint32_t)(K / 128 * 4) : (uint32_t)(K / 32);  // scale bytes per row
     // Lane offsets within a tile for the weights' loads (row l / 8 + 8 h, the chunk that
     // belongs into slot l % 8); in a row's last step, chunks past its end are left out.
     const uint32_t left = rowbytes - 128u * (uint32_t)(nk - 1);
@@ -147,191 +155,161 @@ struct Stream {
       vb_last[h] = cb < left ? vb[h] : kOOB;
     }
     const uint32_t soff = (uint32_t)r * sstride;
-    const int chunks = (nk + W * S - 1) / (W * S);
     uint8_t* ring = smem + wave * (D * kSlot);
-    // MFMA j takes the step's elements 32 j .. 32 j + 31, lane (r, g) 8 of row r from
-    // 32 j + 8 g on: of A 64 bytes of each row together in one load, of the codes 4 (MXFP4) or 8 bytes
-    // at an address of slots that j changes in its own bits only.
-    const int frag = FP4 ? r * 128 + ((r >> 1) & 7) * 16 + 4 * g : r * 128 + (((r >> 1) & 7) ^ (g >> 1)) * 16 + 8 * (g & 1);
-    const uint32_t alane = arow == kOOB ? kOOB : arow + 16u * (uint32_t)g;
-    const uint32_t alane_half = g < 2 ? alane : kOOB;  // INT8: K may end in the middle of 32
+    f32x4(*sums)[G][64] = (f32x4(*)[G][64])(smem + kRing);
+    // A lane's 32 bytes of the step: chunks g and g + 4 of its row.
+    const int frag0 = r * 128 + ((g ^ (r >> 1)) & 7) * 16, frag1 = r * 128 + (((g + 4) ^ (r >> 1)) & 7) * 16;
+    const uint32_t rot = (uint32_t)(8 * g + 9) & 31u;  // MXFP4: rotating right by it takes byte g to bits 30:23
 
-    // MXFP4: the scales of step s's 8 blocks, without the bytes past the row's end, which are
-    // another row's.
-    auto load_scales = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, int s) __attribute__((always_inline)) {
-      const uint32_t so = s < nk ? row + (uint32_t)s * 8u : kScalarOOB;
-      if (ALIGNED) {
-        u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, soff, (int)so, 0));
-        if (s * 8 + 4 >= (int)sstride) v.y = 0;  // (K % 256 = 128)
-        return v;
+    const int rounds = MULTI ? (nk + W * S - 1) / (W * S) : 1;
+    int round = 0;
+    auto step = [&](int i) __attribute__((always_inline)) { return (round * S + i) * W + wave; };
+    Seg seg;
+    // The scales of a tile's step: MXFP4's of blocks 0..3 and 4..7 (this lane uses byte g of
+    // each dword, or, not ALIGNED, has only that), without the bytes past the row's end, which are
+    // another row's and might be NaN; FP8's one.
+    u32x2 wsc[D];
+    auto load = [&](auto kk, int first) __attribute__((always_inline)) {
+      // Place k from tile `first` on. (Tiles past the segment's last are past the views' ends.)
+      constexpr int k = decltype(kk)::value, kind = k / S % KINDS;
+      const int s = step(k % S);
+      const uint32_t row = (uint32_t)(first / KINDS * 16 + k / S / KINDS * 16);
+      const int so = (int)(row * rowbytes + (s < nk ? (uint32_t)s * 128u : kScalarOOB));
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(seg.rB[kind], (lds_ptr_t)(ring + (k % D) * kSlot + h * 1024), 16,
+                                                 s < nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
+      if (FP4) {
+        const int at = (int)(row * sstride + (s < nk ? (uint32_t)s * 8u : kScalarOOB));
+        if (ALIGNED) {
+          wsc[k % D] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(seg.rS[kind], soff, at, 0));
+        } else {
+          const uint32_t b = (uint32_t)s * 8u + (uint32_t)g;
+          wsc[k % D].x = __builtin_amdgcn_raw_buffer_load_b8(seg.rS[kind], b < sstride ? soff + g : kOOB, at, 0);
+          wsc[k % D].y = __builtin_amdgcn_raw_buffer_load_b8(seg.rS[kind], b + 4u < sstride ? soff + 4u + g : kOOB, at, 0);
+        }
       }
-      const uint32_t b = (uint32_t)s * 8u + (uint32_t)g;
-      const uint32_t x = __builtin_amdgcn_raw_buffer_load_b8(rs, b < sstride ? soff + g : kOOB, (int)so, 0);
-      const uint32_t y = __builtin_amdgcn_raw_buffer_load_b8(rs, b + 4u < sstride ? soff + 4u + g : kOOB, (int)so, 0);
-      return u32x2{x << (8 * g), y << (8 * g)};  // (of the lanes of a row together)
+      if (FP8)
+        wsc[k % D].x = __builtin_amdgcn_raw_buffer_load_b32(
+            seg.rS[kind], 0, (int)(((uint32_t)seg.row0 + row) / 128u * sstride + (s < nk ? (uint32_t)s * 4u : kScalarOOB)), 0);
+    };
+    u32x4 a[S][kFrags];  // (of lanes without a row: anything, for rows of the result that nobody reads)
+    // The ring's first weights, then A's fragments.
+    auto start = [&](int first) __attribute__((always_inline)) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the ring is free)
+      unroll<D - 1>([&](auto kk) __attribute__((always_inline)) { load(kk, first); });
+#pragma unroll
+      for (int i = 0; i < S; i++)
+#pragma unroll
+        for (int j = 0; j < kFrags; j++) {
+          constexpr int kPer = kFrags / 2;  // 16-byte pieces of A that meet a 16-byte chunk of codes
+          const uint32_t chunk = (uint32_t)(step(i) * 8 + j / kPer * 4 + g);
+          a[i][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              seg.rA, chunk * 16u < rowbytes ? seg.arow + (uint32_t)g * (16u * kPer) : kOOB, (step(i) * 8 + j / kPer * 4) * (16 * kPer) + j % kPer * 16, 0));
+        }
+    };
+    auto started = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    struct Codes {
+      u32x4 h[2];
+    };
+    auto read = [&](int k) __attribute__((always_inline)) {
+      const uint8_t* at = ring + (k % D) * kSlot;
+      return Codes{{*(const u32x4*)(at + frag0), *(const u32x4*)(at + frag1)}};
     };
 
-    f32x4 acc[T];
+    bool more = next_segment(seg);
+    if (!MULTI && more) start(0);
+    while (more) {
+      const int n = seg.n;
+      const Pass pass = seg.pass;
+      const int row0 = seg.row0;
+      if (!MULTI) started();
+      for (int first = 0; first < n; first += G) {
+        f32x4 acc[G];
 #pragma unroll
-    for (int j = 0; j < T; j++) acc[j] = f32x4{0, 0, 0, 0};
-
-    for (int c = 0; c < chunks; c++) {
-      const int s0 = (c * W + wave) * S;
-      // The ring's first weights, then A of all S steps, then (FP8) the weights' scales.
-      u32x2 wsc[D];  // MXFP4: the ring's scales
-      auto load = [&](int k) __attribute__((always_inline)) {
-        const int t = k / S, s = s0 + k % S;
-        const int so = s < nk ? (int)(tile_row(t) * rowbytes + (uint32_t)s * 128u) : (int)kScalarOOB;
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(view(t), (lds_ptr_t)(ring + (k % D) * kSlot + h * 1024), 16,
-                                                   s < nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
-        if (FP4) wsc[k % D] = load_scales(sview(t), tile_row(t) * sstride, s);
-      };
-#pragma unroll
-      for (int k = 0; k < D - 1; k++)
-        if (k < T * S) load(k);
-      // A's fragments. (The step and MFMA go into the scalar offset.)
-      u32x4 a[S][kFrags];
-#pragma unroll
-      for (int s = 0; s < S; s++)
-#pragma unroll
-        for (int i = 0; i < kFrags; i++) {
-          const int k = ((s0 + s) * kFrags + i) * 32;
-          a[s][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-              rA, FMT != kINT8 || k + 32 <= K ? alane : alane_half, k < K ? k * 2 : (int)kScalarOOB, 0));
-        }
-      float sb[T];
-      if (FP8) {
-#pragma unroll
-        for (int t = 0; t < T; t++) {
-          const float* p = fp8_row(t);  // null: a tile past the end
-          sb[t] = p && s0 + lane < nk ? p[s0 + lane] : 0.0f;
-        }
-      }
-      // Step k + 1's fragments are read before step k's MFMAs. Loads end in
-      // order: step k + 1's have arrived when only the later steps' are out
-      // (the first time, A's too, which came last).
-      constexpr int kLoads = FP4 ? (ALIGNED ? 3 : 4) : 2;  // of a step
-      auto arrived = [&](auto n) __attribute__((always_inline)) {
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"i"(decltype(n)::value) : "memory");
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      struct Codes {
-        uint32_t q[8];
-      };
-      auto read = [&](int k) __attribute__((always_inline)) {
-        const uint8_t* at = ring + (k % D) * kSlot;
-        Codes c;
-#pragma unroll
-        for (int j = 0; j < kFrags; j++) {
-          if constexpr (FP4) {
-            c.q[j] = *(const uint32_t*)(at + (frag ^ (16 * j)));
-          } else {
-            const u32x2 v = *(const u32x2*)(at + (frag ^ (32 * j)));
-            c.q[2 * j] = v.x;
-            c.q[2 * j + 1] = v.y;
+        for (int j = 0; j < G; j++) acc[j] = f32x4{0, 0, 0, 0};
+        for (round = 0; round < rounds; round++) {
+          if (MULTI) {
+            start(first);
+            started();
           }
-        }
-        return c;
-      };
-      arrived(std::integral_constant<int, 0>{});
-      Codes next = read(0);
-      unroll<T * S>([&](auto kk) __attribute__((always_inline)) {
-        constexpr int k = decltype(kk)::value, t = k / S, s = k % S;
-        const Codes bv = next;
-        u32x2 wscale = wsc[k % D];
-        if (k + D - 1 < T * S) load(k + D - 1);
-        if constexpr (k + 1 < T * S) {
-          // Steps loaded behind k + 1 (the first D - 1 have all arrived).
-          constexpr int last = k + D - 1 < T * S ? k + D - 1 : T * S - 1;
-          constexpr int behind = last - (k + 1);
-          if constexpr (k + 1 >= D - 1) arrived(std::integral_constant<int, behind * kLoads>{});
-          next = read(k + 1);
-        }
-        f32x4 P = FP8 ? f32x4{0, 0, 0, 0} : acc[t];
-        if (FP4 && !ALIGNED) wscale = u32x2{or_over_rows(wscale.x), or_over_rows(wscale.y)};
+          Codes next = read(0);
+          unroll<G * S>([&](auto kk) __attribute__((always_inline)) {
+            constexpr int k = decltype(kk)::value, t = k / S, i = k % S;
+            if (first + t >= n) return;  // (the last group's)
+            const Codes bv = next;
+            u32x2 wscale = wsc[k % D];
+            // Into the slot of the step before, which has been read. (MULTI: what is past
+            // the group is loaded again by the next start.)
+            load(std::integral_constant<int, k + D - 1>{}, first);
+            // Step k + 1's fragments are read before step k's MFMAs. Loads end in order: step k + 1's
+            // have arrived when only the D - 2 later steps' are out (and stores, if any, besides).
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"i"((D - 2) * kLoads) : "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (k + 1 < G * S) next = read(k + 1);
+            f32x4 P = FP8 ? f32x4{0, 0, 0, 0} : acc[t];
+            if (FP4 && ALIGNED && step(i) * 8 + 4 >= (int)sstride) wscale.y = 0;  // (K % 256 = 128)
 #pragma unroll
-        for (int j = 0; j < kFrags; j++) {
-          bf16x8 w;
-          if constexpr (FP4)
-            w = expand_fp4(bv.q[j], wscale[j / 4], j % 4);
-          else
-            w = FP8 ? fp8::expand8((int)bv.q[2 * j], (int)bv.q[2 * j + 1]) : expand_int8(bv.q[2 * j], bv.q[2 * j + 1]);
-          P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, a[s][j]), P, 0, 0, 0);
-        }
-        if constexpr (FP8) {
-          const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb[t]), s));
+            for (int h = 0; h < 2; h++) {
+              const uint32_t scale = ALIGNED ? __builtin_amdgcn_alignbit(wscale[h], wscale[h], rot) : wscale[h] << 23;
 #pragma unroll
-          for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
-        } else {
-          acc[t] = P;
+              for (int j = 0; j < kFrags / 2; j++) {
+                bf16x8 w;
+                if constexpr (FP4)
+                  w = expand_fp4(bv.h[h][j], scale);
+                else
+                  w = FP8 ? fp8::expand8((int)bv.h[h][2 * j], (int)bv.h[h][2 * j + 1]) : expand_int8(bv.h[h][2 * j], bv.h[h][2 * j + 1]);
+                P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, a[i][h * (kFrags / 2) + j]), P, 0, 0, 0);
+              }
+            }
+            if constexpr (FP8) {
+              const float f = __builtin_bit_cast(float, wscale.x);
+#pragma unroll
+              for (int e = 0; e < 4; e++) acc[t][e] = __builtin_fmaf(P[e], f, acc[t][e]);
+            } else {
+              acc[t] = P;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          });
         }
-        __builtin_amdgcn_sched_barrier(0);
-      });
+        round = 0;
+        if (first + G >= n) {
+          // The next segment's first loads, beside this one's last results.
+          more = next_segment(seg);
+          if (!MULTI && more) start(0);
+        }
+        // (Every wave has done with the last group's sums: it has passed the barrier behind them.)
+#pragma unroll
+        for (int j = 0; j < G; j++) sums[wave][j][lane] = acc[j];
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        done(pass, row0, n, first, sums);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      }
     }
-    __syncthreads();  // (every ring has been read)
-    float(*part)[T][4][64] = (float(*)[T][4][64])smem;
-#pragma unroll
-    for (int j = 0; j < T; j++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) part[wave][j][e][lane] = acc[j][e];
-    __syncthreads();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
 
-  // Tile j's sums over the waves, of this lane.
-  static __device__ __forceinline__ f32x4 sum(const uint8_t* smem, int j) {
-    const float(*part)[T][4][64] = (const float(*)[T][4][64])smem;
+  // The sums over the waves of tile j, of this lane; of its columns e, e + 1 of 4 only.
+  static __device__ __forceinline__ f32x4 sum(const f32x4 (*sums)[G][64], int j) {
     const int lane = threadIdx.x & 63;
-    f32x4 v;
+    f32x4 v = sums[0][j][lane];
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-      v[e] = part[0][j][e][lane];
+    for (int w = 1; w < W; w++) v += sums[w][j][lane];
+    return v;
+  }
+  static __device__ __forceinline__ f32x2 sum2(const f32x4 (*sums)[G][64], int j, int e) {
+    const int lane = threadIdx.x & 63;
+    f32x2 v = *((const f32x2*)&sums[0][j][lane] + e / 2);
 #pragma unroll
-      for (int w = 1; w < W; w++) v[e] += part[w][j][e][lane];
-    }
+    for (int w = 1; w < W; w++) v += *((const f32x2*)&sums[w][j][lane] + e / 2);
     return v;
   }
 };
-
-// Pass `want` of the ids' (kMoeMaxExperts words of LDS: the tokens of each expert): its expert, rows
-// before it, rows, and its tokens with all of their expert's (`skip` of these come first);
-// false: there is none. `passes`: how many there are.
-__device__ __forceinline__ bool route(const Args& p, unsigned long long* tokens_of, int want, Pass& pass,
-                                      unsigned long long& tokens, int& skip, int& passes) {
-  const int tid = threadIdx.x, lane = tid & 63, slots = p.tokens * p.top;
-  for (int i = tid; i < p.experts; i += 64 * W) tokens_of[i] = 0;
-  __syncthreads();
-  for (int i = tid; i < slots; i += 64 * W) {
-    const int id = p.ids[i];
-    if (id >= 0 && id < p.experts) atomicOr(&tokens_of[id], 1ull << (i / p.top));
-  }
-  __syncthreads();
-  bool found = false;
-  int rows0 = 0;
-  passes = 0;
-  for (int c = 0; c < p.experts; c += 64) {
-    const unsigned long long m = c + lane < p.experts ? tokens_of[c + lane] : 0;
-    const int n = __builtin_popcountll(m);
-    // Rows and passes up to this lane's expert, in one scan.
-    const int upto = groups::wave_scan(n << 16 | (n + 15) / 16);
-    const int all = __builtin_amdgcn_readlane(upto, 63);
-    if (!found && want < passes + (all & 0xFFFF)) {
-      const int l = __builtin_ctzll(__ballot(passes + (upto & 0xFFFF) > want));
-      const int before = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0;
-      const int own = __builtin_amdgcn_readlane(n, l);
-      skip = (want - passes - (before & 0xFFFF)) * 16;
-      pass = {c + l, rows0 + (before >> 16) + skip, min(own - skip, 16), 0};
-      tokens = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)m, l) |
-               (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(m >> 32), l) << 32;
-      found = true;
-    }
-    passes += all & 0xFFFF;
-    rows0 += all >> 16;
-  }
-  return found;
-}
 
 // (Said to be the same in all lanes, for the compiler to keep it in scalars.)
 __device__ __forceinline__ void uniform(Pass& p) {
@@ -340,118 +318,178 @@ __device__ __forceinline__ void uniform(Pass& p) {
   p.rows = __builtin_amdgcn_readfirstlane(p.rows);
 }
 
-// T: tiles, of the gate's and the up projection's rows in turn.
-template <int FMT, bool ALIGNED, int S, int T, int D>
-__global__ __launch_bounds__(64 * W) void moe_up_kernel(Args p) {
-  using St = Stream<FMT, ALIGNED, S, T, D>;
-  constexpr int kMask = kMoeMaxExperts * 8;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[St::kSmem > kMask ? St::kSmem : kMask];
+// The tokens of each expert as bits, from the ids, in LDS.
+__device__ __forceinline__ void route(const Args& p, unsigned long long* tokens_of) {
+  const int tid = threadIdx.x, slots = p.tokens * p.top;
+  for (int i = tid; i < p.experts; i += 64 * W) tokens_of[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < slots; i += 64 * W) {
+    const int id = p.ids[i];
+    if (id >= 0 && id < p.experts) atomicOr(&tokens_of[id], 1ull << (i / p.top));
+  }
+  __syncthreads();
+}
+
+// Rows and passes of experts c .. c + 63 up to this lane's, in one scan: rows << 16 | passes.
+__device__ __forceinline__ int scan_passes(unsigned long long tokens) {
+  const int n = __builtin_popcountll(tokens);
+  return groups::wave_scan(n << 16 | (n + 15) / 16);
+}
+
+__device__ __forceinline__ int count_passes(const Args& p, const unsigned long long* tokens_of) {
+  const int lane = threadIdx.x & 63;
+  int passes = 0;
+  for (int c = 0; c < p.experts; c += 64)
+    passes += __builtin_amdgcn_readlane(scan_passes(c + lane < p.experts ? tokens_of[c + lane] : 0), 63) & 0xFFFF;
+  return passes;
+}
+
+// Pass `want`, which there is, and its expert's tokens (`skip` of these come in passes before it).
+__device__ __forceinline__ void find_pass(const Args& p, const unsigned long long* tokens_of, int want, Pass& pass,
+                                          unsigned long long& tokens, int& skip) {
+  const int lane = threadIdx.x & 63;
+  int rows = 0;
+  for (int c = 0; c < p.experts; c += 64) {
+    const unsigned long long m = c + lane < p.experts ? tokens_of[c + lane] : 0;
+    const int upto = scan_passes(m), all = __builtin_amdgcn_readlane(upto, 63);
+    if (want >= (all & 0xFFFF)) {
+      want -= all & 0xFFFF;
+      rows += all >> 16;
+      continue;
+    }
+    const int l = __builtin_ctzll(__ballot((upto & 0xFFFF) > want));
+    const int before = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0;
+    tokens = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)m, l) |
+             (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(m >> 32), l) << 32;
+    skip = (want - (before & 0xFFFF)) * 16;
+    pass = {c + l, rows + (before >> 16) + skip, min((int)__builtin_popcountll(tokens) - skip, 16), 0};
+    break;
+  }
+  uniform(pass);
+  skip = __builtin_amdgcn_readfirstlane(skip);
+}
+
+// What a workgroup does of `all` columns (of 16) of all passes, pass by pass: an even share.
+constexpr int kGrid = 256;  // workgroups: one a CU
+__device__ __forceinline__ int share(int64_t all, int i) { return (int)(all * i / kGrid); }
+
+// A view of a MXFP4 weight's scales, rows of K / 32 bytes from `row` on; of FP8 scales, `rows` / 128 blocks
+// of rows of K / 128 from block row `row` on; else none.
+template <int FMT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_view(const void* scales, int64_t row, int rows, int K) {
+  const int64_t stride = FMT == kMXFP4 ? K / 32 : FMT == kFP8B128X128 ? K / 128 * 4 : 0;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((const uint8_t*)scales + row * stride), 0, (int)((uint32_t)rows * (uint32_t)stride), kRsrcFlags);
+}
+
+template <int FMT, bool ALIGNED, int S, bool MULTI>
+__global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
+  using St = Stream<FMT, ALIGNED, 2, S, MULTI>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[St::kSmem];
+  __shared__ unsigned long long tokens_of[kMoeMaxExperts];
+  __shared__ uint8_t token_at[W][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  Pass pass;
-  unsigned long long tokens;
-  int skip, passes;
-  const bool some = route(p, (unsigned long long*)smem, blockIdx.y, pass, tokens, skip, passes);
-  if (blockIdx.x == 0 && wave == 0) {
-    // The passes, for the kernels that follow.
-    if (blockIdx.y == 0) {
-      if (lane == 0) *p.w.count = passes;
-      for (int i = lane; i < p.tokens * p.top; i += 64)
-        if (p.ids[i] < 0 || p.ids[i] >= p.experts) p.w.row_of[i] = -1;
-    }
-    if (some) {
-      if (lane == 0) p.w.pass[blockIdx.y] = pass;
-      const int at = __builtin_popcountll(tokens & ((1ull << lane) - 1)) - skip;
-      if ((tokens >> lane & 1) && at >= 0 && at < pass.rows)
+  route(p, tokens_of);
+  const int K = p.hidden, I = p.inter, cols = I / 16;
+  const int passes = count_passes(p, tokens_of);
+  if (blockIdx.x == 0 && tid == 0) *p.w.count = passes;
+  const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
+  const int end = share((int64_t)passes * cols, blockIdx.x + 1);
+  int at = share((int64_t)passes * cols, blockIdx.x);
+  auto next = [&](Segment<2>& seg) __attribute__((always_inline)) {
+    if (at >= end) return false;
+    const int u = at / cols, c0 = at - u * cols, n = min(cols - c0, end - at);
+    at += n;
+    unsigned long long tokens = 0;
+    int skip = 0;
+    find_pass(p, tokens_of, u, seg.pass, tokens, skip);
+    const int rank = __builtin_popcountll(tokens & ((1ull << lane) - 1));
+    const bool mine = tokens >> lane & 1;
+    if (c0 == 0 && wave == 0) {
+      // The pass and its tokens' slots, for the kernels that follow.
+      if (lane == 0) p.w.pass[u] = seg.pass;
+      if (mine && rank >= skip && rank < skip + seg.pass.rows)
         for (int j = 0; j < p.top; j++)
-          if (p.ids[lane * p.top + j] == pass.expert) p.w.row_of[lane * p.top + j] = pass.row + at;
+          if (p.ids[lane * p.top + j] == seg.pass.expert) p.w.row_of[lane * p.top + j] = seg.pass.row + rank - skip;
     }
-  }
-  if (!some) return;
-  uniform(pass);
-  __syncthreads();  // (the masks have been read)
-
-  const int K = p.hidden, I = p.inter, i0 = blockIdx.x * (8 * T);
-  // Lane (r, g)'s token: the one of rank skip + r.
-  for (int i = 0; i < skip + r; i++) tokens &= tokens - 1;
-  const uint32_t arow = r < pass.rows ? (uint32_t)__builtin_ctzll(tokens) * (uint32_t)p.ldx * 2u : kOOB;
-  const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)p.x, 0, (int)(((uint32_t)(p.tokens - 1) * (uint32_t)p.ldx + (uint32_t)K) * 2u), kRsrcFlags);
-  const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K), sstride = (uint32_t)(K / 32);
-  const int nrows = min(I - i0, 8 * T);
-  const int64_t row0 = (int64_t)pass.expert * 2 * I + i0;
-  __amdgpu_buffer_rsrc_t rB[2], rS[2];
+    // Lane (r, g)'s token: the one of rank skip + r.
+    if (mine) token_at[wave][rank] = (uint8_t)lane;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    seg.arow = r < seg.pass.rows ? (uint32_t)token_at[wave][skip + r] * (uint32_t)p.ldx * 2u : kOOB;
+    seg.rA = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, (int)(((uint32_t)(p.tokens - 1) * (uint32_t)p.ldx + (uint32_t)K) * 2u), kRsrcFlags);
+    seg.n = 2 * n;
+    seg.row0 = c0 * 16;
 #pragma unroll
-  for (int u = 0; u < 2; u++) {
-    rB[u] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.up + (row0 + (int64_t)u * I) * rowbytes), 0,
-                                              (int)((uint32_t)nrows * rowbytes), kRsrcFlags);
-    rS[u] = __builtin_amdgcn_make_buffer_rsrc((void*)((const uint8_t*)p.up_scales + (FMT == kMXFP4 ? (row0 + (int64_t)u * I) * sstride : 0)), 0,
-                                              FMT == kMXFP4 ? (int)((uint32_t)nrows * sstride) : 0, kRsrcFlags);
-  }
-  St::run(
-      smem, K, rA, arow, [&](int t) { return rB[t % 2]; }, [&](int t) { return rS[t % 2]; }, [&](int t) { return (uint32_t)(t / 2 * 16); },
-      [&](int t) {
-        // (I is a multiple of 128: a tile has one row of scales.)
-        const int64_t row = i0 + t / 2 * 16 + (int64_t)(t % 2) * I;
-        return t / 2 * 16 < nrows ? (const float*)p.up_scales + ((int64_t)pass.expert * (2 * I / 128) + row / 128) * (K / 128) : nullptr;
-      });
-#pragma unroll
-  for (int u = 0; u < (T / 2 + W - 1) / W; u++) {
-    const int j = u * W + wave, col = i0 + 16 * j + 4 * g;
-    if (j >= T / 2 || 16 * j >= nrows || r >= pass.rows) break;
-    f32x4 gate = St::sum(smem, 2 * j), up = St::sum(smem, 2 * j + 1);
+    for (int k = 0; k < 2; k++) {
+      const int64_t row = ((int64_t)seg.pass.expert * 2 + k) * I + c0 * 16;
+      seg.rB[k] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.up + row * rowbytes), 0, (int)((uint32_t)(16 * n) * rowbytes), kRsrcFlags);
+      // (FP8: I is a multiple of 128, and so is each kind's first row.)
+      if (FMT == kFP8B128X128)
+        seg.rS[k] = scale_view<FMT>(p.up_scales, ((int64_t)seg.pass.expert * 2 + k) * (I / 128), I / 128, K);
+      else
+        seg.rS[k] = scale_view<FMT>(p.up_scales, row, 16 * n, K);
+    }
+    return true;
+  };
+  St::run(smem, K, next, [&](const Pass& pass, int i0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
+    // Two columns of four of a pair of tiles a wave.
+    const int j = wave / 2, e0 = wave % 2 * 2, col = i0 + 8 * first + 16 * j + 4 * g + e0;
+    if (j >= St::G / 2 || first + 2 * j >= n || r >= pass.rows) return;
+    f32x2 gate = St::sum2(sums, 2 * j, e0), up = St::sum2(sums, 2 * j + 1, e0);
     if (FMT == kINT8) {
       const float* s = (const float*)p.up_scales + (int64_t)pass.expert * 2 * I + col;
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
+      for (int e = 0; e < 2; e++) {
         gate[e] *= s[e];
         up[e] *= s[I + e];
       }
     }
-    float h[4];
+    float h[2];
 #pragma unroll
-    for (int e = 0; e < 4; e++) h[e] = gate[e] / (1.0f + expf(-gate[e])) * up[e];
-    *(u32x2*)(p.w.h + (int64_t)(pass.row + r) * I + col) = u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
-  }
+    for (int e = 0; e < 2; e++) h[e] = gate[e] / (1.0f + expf(-gate[e])) * up[e];
+    *(uint32_t*)(p.w.h + (int64_t)(pass.row + r) * I + col) = pack_bf16x2(h[0], h[1]);
+  });
 }
 
-template <int FMT, bool ALIGNED, int S, int T, int D>
-__global__ __launch_bounds__(64 * W) void moe_down_kernel(Args p) {
-  using St = Stream<FMT, ALIGNED, S, T, D>;
+template <int FMT, bool ALIGNED, int S, bool MULTI>
+__global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
+  using St = Stream<FMT, ALIGNED, 1, S, MULTI>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[St::kSmem];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  if ((int)blockIdx.y >= *p.w.count) return;
-  Pass pass = p.w.pass[blockIdx.y];
-  uniform(pass);
-  const int K = p.inter, N = p.hidden, n0 = blockIdx.x * (16 * T);
-  const __amdgpu_buffer_rsrc_t rA = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(p.w.h + (int64_t)pass.row * K), 0, (int)((uint32_t)(pass.rows * K) * 2u), kRsrcFlags);
-  const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K), sstride = (uint32_t)(K / 32);
-  const int nrows = min(N - n0, 16 * T);
-  const int64_t row0 = (int64_t)pass.expert * N + n0;
-  const __amdgpu_buffer_rsrc_t rB =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(p.down + row0 * rowbytes), 0, (int)((uint32_t)nrows * rowbytes), kRsrcFlags);
-  const __amdgpu_buffer_rsrc_t rS = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)((const uint8_t*)p.down_scales + (FMT == kMXFP4 ? row0 * sstride : 0)), 0, FMT == kMXFP4 ? (int)((uint32_t)nrows * sstride) : 0, kRsrcFlags);
-  St::run(
-      smem, K, rA, r < pass.rows ? (uint32_t)(r * K) * 2u : kOOB, [&](int) { return rB; }, [&](int) { return rS; },
-      [&](int t) { return (uint32_t)(t * 16); },
-      [&](int t) {
-        return t * 16 < nrows ? (const float*)p.down_scales + ((int64_t)pass.expert * ((N + 127) / 128) + (n0 + t * 16) / 128) * (K / 128) : nullptr;
-      });
-#pragma unroll
-  for (int u = 0; u < (T + W - 1) / W; u++) {
-    const int j = u * W + wave, col = n0 + 16 * j + 4 * g;
-    if (j >= T || 16 * j >= nrows || r >= pass.rows) break;
-    f32x4 v = St::sum(smem, j);
+  const int K = p.inter, N = p.hidden, cols = N / 16;
+  const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
+  const int passes = *p.w.count, end = share((int64_t)passes * cols, blockIdx.x + 1);
+  int at = share((int64_t)passes * cols, blockIdx.x);
+  auto next = [&](Segment<1>& seg) __attribute__((always_inline)) {
+    if (at >= end) return false;
+    const int u = at / cols, c0 = at - u * cols, n = min(cols - c0, end - at);
+    at += n;
+    seg.pass = p.w.pass[u];
+    uniform(seg.pass);
+    seg.arow = r < seg.pass.rows ? (uint32_t)(r * K) * 2u : kOOB;
+    seg.rA = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w.h + (int64_t)seg.pass.row * K), 0, (int)((uint32_t)(seg.pass.rows * K) * 2u), kRsrcFlags);
+    seg.n = n;
+    seg.row0 = c0 * 16;
+    const int64_t row = (int64_t)seg.pass.expert * N + c0 * 16;
+    seg.rB[0] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.down + row * rowbytes), 0, (int)((uint32_t)(16 * n) * rowbytes), kRsrcFlags);
+    if (FMT == kFP8B128X128)
+      seg.rS[0] = scale_view<FMT>(p.down_scales, (int64_t)seg.pass.expert * ((N + 127) / 128), (N + 127) / 128, K);
+    else
+      seg.rS[0] = scale_view<FMT>(p.down_scales, row, 16 * n, K);
+    return true;
+  };
+  St::run(smem, K, next, [&](const Pass& pass, int n0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
+    const int col = n0 + 16 * (first + wave) + 4 * g;
+    if (wave >= St::G || first + wave >= n || r >= pass.rows) return;
+    f32x4 v = St::sum(sums, wave);
     if (FMT == kINT8) {
       const float* s = (const float*)p.down_scales + (int64_t)pass.expert * N + col;
 #pragma unroll
       for (int e = 0; e < 4; e++) v[e] *= s[e];
     }
     *(f32x4*)(p.w.part + (int64_t)(pass.row + r) * N + col) = v;
-  }
+  });
 }
 
 template <int OUT>
@@ -460,8 +498,9 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(Args p) {
   if (n >= p.hidden) return;
   f32x4 y = {0, 0, 0, 0};
   for (int j = 0; j < p.top; j++) {
+    const int id = p.ids[t * p.top + j];
+    if (id < 0 || id >= p.experts) continue;
     const int row = p.w.row_of[t * p.top + j];
-    if (row < 0) continue;
     const f32x4 v = *(const f32x4*)(p.w.part + (int64_t)row * p.hidden + n);
     const float w = p.weights[t * p.top + j];
 #pragma unroll
@@ -478,24 +517,29 @@ int64_t align(int64_t n) { return (n + 255) / 256 * 256; }
 // Passes that any ids can need.
 int64_t most_passes(int64_t slots, int64_t experts) { return groups::max_row_tiles(slots, experts, 16); }
 
-template <int FMT, bool UP, int S, int T, int D>
+template <int FMT, bool UP, int S, bool MULTI>
 hipError_t launch(const Args& p, hipStream_t s) {
-  const int64_t tiles = UP ? (p.inter + 8 * T - 1) / (8 * T) : (p.hidden + 16 * T - 1) / (16 * T);
-  const dim3 grid((unsigned)tiles, (unsigned)most_passes((int64_t)p.tokens * p.top, p.experts));
   const int K = UP ? p.hidden : p.inter;
-  if constexpr (UP) {
-    if (FMT == kMXFP4 && K % 128 != 0) return launch_kernel(&moe_up_kernel<FMT, false, S, T, D>, grid, 64 * W, 0, s, p);
-    return launch_kernel(&moe_up_kernel<FMT, true, S, T, D>, grid, 64 * W, 0, s, p);
-  } else {
-    if (FMT == kMXFP4 && K % 128 != 0) return launch_kernel(&moe_down_kernel<FMT, false, S, T, D>, grid, 64 * W, 0, s, p);
-    return launch_kernel(&moe_down_kernel<FMT, true, S, T, D>, grid, 64 * W, 0, s, p);
+  if constexpr (FMT == kMXFP4) {
+    if (K % 128 != 0) return launch_kernel(UP ? &moe_up_kernel<FMT, false, S, MULTI> : &moe_down_kernel<FMT, false, S, MULTI>, dim3(kGrid), 64 * W, 0, s, p);
   }
+  return launch_kernel(UP ? &moe_up_kernel<FMT, true, S, MULTI> : &moe_down_kernel<FMT, true, S, MULTI>, dim3(kGrid), 64 * W, 0, s, p);
+}
+
+// Steps a wave: as few as take a row's in one round, within the registers that A's fragments of them take.
+template <int FMT, bool UP>
+hipError_t by_length(const Args& p, hipStream_t s) {
+  const int K = UP ? p.hidden : p.inter, nk = (K + (FMT == kMXFP4 ? 255 : 127)) / (FMT == kMXFP4 ? 256 : 128);
+  if (nk <= W) return launch<FMT, UP, 1, false>(p, s);
+  if (nk <= 2 * W) return launch<FMT, UP, 2, false>(p, s);
+  if (nk <= 4 * W) return launch<FMT, UP, 4, false>(p, s);
+  return launch<FMT, UP, 4, true>(p, s);
 }
 
 template <int FMT>
 hipError_t run(const Args& p, int out_dtype, hipStream_t s) {
-  MX_TRY((launch<FMT, true, 1, 2, 3>(p, s)));
-  MX_TRY((launch<FMT, false, 1, 2, 3>(p, s)));
+  MX_TRY((by_length<FMT, true>(p, s)));
+  MX_TRY((by_length<FMT, false>(p, s)));
   const dim3 grid((unsigned)((p.hidden + 1023) / 1024), (unsigned)p.tokens);
   if (out_dtype == kOutF32) return launch_kernel(&moe_combine_kernel<kOutF32>, grid, 256, 0, s, p);
   return launch_kernel(&moe_combine_kernel<kOutBF16>, grid, 256, 0, s, p);

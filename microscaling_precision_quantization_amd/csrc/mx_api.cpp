@@ -41,6 +41,7 @@ constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxExtent = (int64_t)1 << 30;
 constexpr int64_t kW4A16MaxK = 65536;
 constexpr int64_t kMoeMaxWidth = (int64_t)1 << 20;  // hidden, inter and x's row stride of mx_moe
+constexpr int64_t kMoeMaxWeight = (int64_t)1 << 30;  // hidden inter: 32-bit offsets in an expert's projection
 constexpr int64_t kMaxGroups = 65535;  // experts of a grouped GEMM (a grid dimension)
 
 mx_status hip_status(hipError_t e) {
@@ -352,7 +353,7 @@ mx_status mx_moe(mx_format fmt, int block, mx_round rnd, int64_t tokens, int64_t
   // (0: a size or a limit)
   const size_t need = mx_moe_workspace_bytes(tokens, top, experts, hidden, inter);
   if (need == 0 || hidden % granule_of(fmt) != 0 || inter % granule_of(fmt) != 0) return MX_ERR_INVALID_ARG;
-  if (experts * 2 * inter > kMaxElems / hidden) return MX_ERR_INVALID_ARG;
+  if (hidden > kMoeMaxWeight / inter) return MX_ERR_INVALID_ARG;
   // Rows of x are read 16 bytes at a time at 32-bit offsets, those of y written 4 elements at a time.
   if (ldx < hidden || ldx % 8 != 0 || ldx > kMoeMaxWidth || ldy < hidden || ldy % 4 != 0 || ldy > kMaxExtent) return MX_ERR_INVALID_ARG;
   if (!x || !ids || !weights || !up || !up_scales || !down || !down_scales || !y || !workspace) return MX_ERR_INVALID_ARG;
