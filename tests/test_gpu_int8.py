@@ -125,7 +125,8 @@ def _operands(M, N, K, seed, G=1):
 SHAPES = [(1, 1, 16), (1, 16, 128), (3, 5, 48), (16, 256, 4096), (16, 2000, 2064), (7, 4099, 8192), (2, 20000, 6160), (16, 12304, 2048),
           (9, 6000, 16400), (16, 10000, 4112), (3, 13000, 4112),
           (17, 100, 144), (33, 64, 272), (40, 9000, 528), (48, 2000, 512), (64, 2048, 1040), (130, 129, 400), (300, 2048, 256), (777, 2000, 2448),
-          (128, 8192, 640), (1500, 1003, 1024), (1500, 4096, 1040), (900, 8200, 784), (2304, 2300, 112), (2100, 2600, 16), (2100, 2605, 272)]
+          (128, 8192, 640), (1500, 1003, 1024), (1500, 4096, 1040), (900, 8200, 784), (2304, 2300, 112), (2100, 2600, 16), (2100, 2605, 272),
+          (2560, 2570, 112), (2600, 2600, 16), (2600, 2605, 1040)]
 
 
 @pytest.mark.parametrize("out", [F32, BF16])
@@ -215,7 +216,8 @@ def _grouped(a, b, offsets):
 
 GROUPED = [([1], 16, 16), ([0, 1, 0], 40, 48), ([3, 0, 2, 1], 200, 2064), ([1] * 40 + [0] * 30, 96, 4096), ([20, 31, 0, 9] * 6, 1400, 400),
            ([70, 150, 1, 0, 300], 300, 144), ([200, 0, 700, 33], 2000, 272), ([129, 64, 65, 128, 1], 1100, 784), ([40] * 16, 1000, 512),
-           ([600, 250, 0, 900], 2100, 112), ([300, 513, 255, 256, 257], 2600, 400), ([17, 5, 90], 3000, 4112), ([700], 130, 2048), ([1, 0, 2, 3] * 4, 1100, 4112), ([20, 0, 1, 3] * 4, 1100, 4112)]
+           ([600, 250, 0, 900], 2100, 112), ([300, 513, 255, 256, 257], 2600, 400), ([17, 5, 90], 3000, 4112), ([700], 130, 2048), ([1, 0, 2, 3] * 4, 1100, 4112), ([20, 0, 1, 3] * 4, 1100, 4112), ([600, 250, 0, 900, 513], 5200, 144),
+           ([31, 64, 65, 129, 2, 90], 4000, 1040), ([30] * 40, 1500, 272)]
 
 
 @pytest.mark.parametrize("out", [F32, BF16])
