@@ -195,10 +195,9 @@ struct Stream {
             seg.rS[kind], 0, (int)(((uint32_t)seg.row0 + row) / 128u * sstride + (s < nk ? (uint32_t)s * 4u : kScalarOOB)), 0);
     };
     u32x4 a[S][kFrags];  // (of lanes without a row: anything, for rows of the result that nobody reads)
-    // The ring's first weights, then A's fragments.
+    // A's fragments, then the ring's first weights. (The other way round A's loads wait for the weights'.)
     auto start = [&](int first) __attribute__((always_inline)) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the ring is free)
-      unroll<D - 1>([&](auto kk) __attribute__((always_inline)) { load(kk, first); });
 #pragma unroll
       for (int i = 0; i < S; i++)
 #pragma unroll
@@ -208,6 +207,8 @@ struct Stream {
           a[i][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
               seg.rA, chunk * 16u < rowbytes ? seg.arow + (uint32_t)g * (16u * kPer) : kOOB, (step(i) * 8 + j / kPer * 4) * (16 * kPer) + j % kPer * 16, 0));
         }
+      __builtin_amdgcn_sched_barrier(0);
+      unroll<D - 1>([&](auto kk) __attribute__((always_inline)) { load(kk, first); });
     };
     auto started = [&]() __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
@@ -222,12 +223,16 @@ struct Stream {
       return Codes{{*(const u32x4*)(at + frag0), *(const u32x4*)(at + frag1)}};
     };
 
-    bool more = next_segment(seg);
-    if (!MULTI && more) start(0);
+    if (!next_segment(seg)) return;
+    if (!MULTI) start(0);
+    bool more = true;
     while (more) {
       const int n = seg.n;
       const Pass pass = seg.pass;
       const int row0 = seg.row0;
+      // (What comes next is found out beside the first loads.)
+      Seg after;
+      more = next_segment(after);
       if (!MULTI) started();
       for (int first = 0; first < n; first += G) {
         f32x4 acc[G];
@@ -281,7 +286,7 @@ struct Stream {
         round = 0;
         if (first + G >= n) {
           // The next segment's first loads, beside this one's last results.
-          more = next_segment(seg);
+          seg = after;
           if (!MULTI && more) start(0);
         }
         // (Every wave has done with the last group's sums: it has passed the barrier behind them.)
@@ -370,9 +375,36 @@ __device__ __forceinline__ void find_pass(const Args& p, const unsigned long lon
   skip = __builtin_amdgcn_readfirstlane(skip);
 }
 
-// What a workgroup does of `all` columns (of 16) of all passes, pass by pass: an even share.
+// What workgroup b does of `passes` passes over `cols` columns (of 16): all of them one after the
+// other from `at` to `end`. An even share, which begins or ends within a pass, or, where that takes
+// less time, a part of one pass: beginning with another pass costs about as much as kSwitch columns.
 constexpr int kGrid = 256;  // workgroups: one a CU
-__device__ __forceinline__ int share(int64_t all, int i) { return (int)(all * i / kGrid); }
+constexpr int kSwitch = 2;
+struct Share {
+  int at, end, pass, col;  // pass and column of `at`
+};
+__device__ __forceinline__ Share share(int passes, int cols, int b) {
+  Share s;
+  const int all = passes * cols, each = kGrid / max(passes, 1), more = kGrid - passes * each;  // (all: at most 2^27)
+  const int part = (cols + max(each, 1) - 1) / max(each, 1);
+  if (each > 0 && part <= all / kGrid + 1 + kSwitch) {
+    // `more` passes have a workgroup more than the others.
+    const bool first = b < more * (each + 1);
+    const int w = first ? each + 1 : each, i = first ? b : b - more * (each + 1), pass = i / w;
+    const int n = first ? (cols + each) / (each + 1) : part;
+    s.pass = (first ? 0 : more) + pass;
+    s.col = min((i - pass * w) * n, cols);
+    s.at = s.pass * cols + s.col;
+    s.end = min(s.at + n, (s.pass + 1) * cols);
+    if (s.pass >= passes) s.end = s.at;  // (no passes)
+  } else {
+    s.at = (int)((int64_t)all * b / kGrid);
+    s.end = (int)((int64_t)all * (b + 1) / kGrid);
+    s.pass = s.at / cols;
+    s.col = s.at - s.pass * cols;
+  }
+  return s;
+}
 
 // A view of a MXFP4 weight's scales, rows of K / 32 bytes from `row` on; of FP8 scales, `rows` / 128 blocks
 // of rows of K / 128 from block row `row` on; else none.
@@ -395,26 +427,31 @@ __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
   const int passes = count_passes(p, tokens_of);
   if (blockIdx.x == 0 && tid == 0) *p.w.count = passes;
   const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
-  const int end = share((int64_t)passes * cols, blockIdx.x + 1);
-  int at = share((int64_t)passes * cols, blockIdx.x);
+  Share mine = share(passes, cols, blockIdx.x);
   auto next = [&](Segment<2>& seg) __attribute__((always_inline)) {
-    if (at >= end) return false;
-    const int u = at / cols, c0 = at - u * cols, n = min(cols - c0, end - at);
-    at += n;
+    if (mine.at >= mine.end) return false;
+    const int u = mine.pass, c0 = mine.col, n = min(cols - c0, mine.end - mine.at);
+    mine = {mine.at + n, mine.end, u + 1, 0};
     unsigned long long tokens = 0;
     int skip = 0;
     find_pass(p, tokens_of, u, seg.pass, tokens, skip);
     const int rank = __builtin_popcountll(tokens & ((1ull << lane) - 1));
-    const bool mine = tokens >> lane & 1;
+    const bool has = tokens >> lane & 1;
     if (c0 == 0 && wave == 0) {
       // The pass and its tokens' slots, for the kernels that follow.
       if (lane == 0) p.w.pass[u] = seg.pass;
-      if (mine && rank >= skip && rank < skip + seg.pass.rows)
-        for (int j = 0; j < p.top; j++)
-          if (p.ids[lane * p.top + j] == seg.pass.expert) p.w.row_of[lane * p.top + j] = seg.pass.row + rank - skip;
+      if (has && rank >= skip && rank < skip + seg.pass.rows)
+        for (int j0 = 0; j0 < p.top; j0 += 8) {
+          int id[8];
+#pragma unroll
+          for (int j = 0; j < 8; j++) id[j] = p.ids[lane * p.top + min(j0 + j, p.top - 1)];
+#pragma unroll
+          for (int j = 0; j < 8; j++)
+            if (j0 + j < p.top && id[j] == seg.pass.expert) p.w.row_of[lane * p.top + j0 + j] = seg.pass.row + rank - skip;
+        }
     }
-    // Lane (r, g)'s token: the one of rank skip + r.
-    if (mine) token_at[wave][rank] = (uint8_t)lane;
+    // Row r's token is the one of rank skip + r.
+    if (has) token_at[wave][rank] = (uint8_t)lane;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     seg.arow = r < seg.pass.rows ? (uint32_t)token_at[wave][skip + r] * (uint32_t)p.ldx * 2u : kOOB;
     seg.rA = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, (int)(((uint32_t)(p.tokens - 1) * (uint32_t)p.ldx + (uint32_t)K) * 2u), kRsrcFlags);
@@ -460,24 +497,23 @@ __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
   const int r = lane & 15, g = lane >> 4;
   const int K = p.inter, N = p.hidden, cols = N / 16;
   const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
-  const int passes = *p.w.count, end = share((int64_t)passes * cols, blockIdx.x + 1);
-  int at = share((int64_t)passes * cols, blockIdx.x);
+  Share mine = share(*p.w.count, cols, blockIdx.x);
   auto next = [&](Segment<1>& seg) __attribute__((always_inline)) {
-    if (at >= end) return false;
-    const int u = at / cols, c0 = at - u * cols, n = min(cols - c0, end - at);
-    at += n;
+    if (mine.at >= mine.end) return false;
+    const int u = mine.pass, c0 = mine.col, n = min(cols - c0, mine.end - mine.at);
+    mine = {mine.at + n, mine.end, u + 1, 0};
     seg.pass = p.w.pass[u];
     uniform(seg.pass);
     seg.arow = r < seg.pass.rows ? (uint32_t)(r * K) * 2u : kOOB;
     seg.rA = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w.h + (int64_t)seg.pass.row * K), 0, (int)((uint32_t)(seg.pass.rows * K) * 2u), kRsrcFlags);
     seg.n = n;
     seg.row0 = c0 * 16;
-    const int64_t row = (int64_t)seg.pass.expert * N + c0 * 16;
-    seg.rB[0] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.down + row * rowbytes), 0, (int)((uint32_t)(16 * n) * rowbytes), kRsrcFlags);
+    const int64_t row0 = (int64_t)seg.pass.expert * N + c0 * 16;
+    seg.rB[0] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.down + row0 * rowbytes), 0, (int)((uint32_t)(16 * n) * rowbytes), kRsrcFlags);
     if (FMT == kFP8B128X128)
       seg.rS[0] = scale_view<FMT>(p.down_scales, (int64_t)seg.pass.expert * ((N + 127) / 128), (N + 127) / 128, K);
     else
-      seg.rS[0] = scale_view<FMT>(p.down_scales, row, 16 * n, K);
+      seg.rS[0] = scale_view<FMT>(p.down_scales, row0, 16 * n, K);
     return true;
   };
   St::run(smem, K, next, [&](const Pass& pass, int n0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
