@@ -110,6 +110,16 @@ __device__ __forceinline__ bf16x8 expand_int8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, o);
 }
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A view of memory that is the same in all lanes, said so for the compiler to keep it in scalars (with
+// views in VGPRs it loops over the lanes' at each load: 102 -> 99 us of a gate and up product of 64 tokens).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)base;
+  const uint64_t u = (uint64_t)(uint32_t)uniform((int)(uint32_t)b) | (uint64_t)(uint32_t)uniform((int)(b >> 32)) << 32;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)u, 0, uniform((int)bytes), kRsrcFlags);
+}
+
 // What a workgroup does of one pass: `n` tiles of 16 weight rows, tile t of kind t % KINDS (the
 // gate's and the up projection's rows) from row 16 (t / KINDS) of its kind's view on. The views end
 // with the tiles there are. A's view and lane (r, g)'s row's first byte in it (kOOB: no such row).
@@ -317,11 +327,10 @@ struct Stream {
   }
 };
 
-// (Said to be the same in all lanes, for the compiler to keep it in scalars.)
 __device__ __forceinline__ void uniform(Pass& p) {
-  p.expert = __builtin_amdgcn_readfirstlane(p.expert);
-  p.row = __builtin_amdgcn_readfirstlane(p.row);
-  p.rows = __builtin_amdgcn_readfirstlane(p.rows);
+  p.expert = uniform(p.expert);
+  p.row = uniform(p.row);
+  p.rows = uniform(p.rows);
 }
 
 // The tokens of each expert as bits, from the ids, in LDS.
@@ -372,7 +381,7 @@ __device__ __forceinline__ void find_pass(const Args& p, const unsigned long lon
     break;
   }
   uniform(pass);
-  skip = __builtin_amdgcn_readfirstlane(skip);
+  skip = uniform(skip);
 }
 
 // What workgroup b does of `passes` passes over `cols` columns (of 16): all of them one after the
@@ -403,7 +412,7 @@ __device__ __forceinline__ Share share(int passes, int cols, int b) {
     s.pass = s.at / cols;
     s.col = s.at - s.pass * cols;
   }
-  return s;
+  return {uniform(s.at), uniform(s.end), uniform(s.pass), uniform(s.col)};
 }
 
 // A view of a MXFP4 weight's scales, rows of K / 32 bytes from `row` on; of FP8 scales, `rows` / 128 blocks
@@ -411,7 +420,7 @@ __device__ __forceinline__ Share share(int passes, int cols, int b) {
 template <int FMT>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_view(const void* scales, int64_t row, int rows, int K) {
   const int64_t stride = FMT == kMXFP4 ? K / 32 : FMT == kFP8B128X128 ? K / 128 * 4 : 0;
-  return __builtin_amdgcn_make_buffer_rsrc((void*)((const uint8_t*)scales + row * stride), 0, (int)((uint32_t)rows * (uint32_t)stride), kRsrcFlags);
+  return view((const uint8_t*)scales + row * stride, (uint32_t)rows * (uint32_t)stride);
 }
 
 template <int FMT, bool ALIGNED, int S, bool MULTI>
@@ -424,7 +433,7 @@ __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
   const int r = lane & 15, g = lane >> 4;
   route(p, tokens_of);
   const int K = p.hidden, I = p.inter, cols = I / 16;
-  const int passes = count_passes(p, tokens_of);
+  const int passes = uniform(count_passes(p, tokens_of));
   if (blockIdx.x == 0 && tid == 0) *p.w.count = passes;
   const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
   Share mine = share(passes, cols, blockIdx.x);
@@ -454,13 +463,13 @@ __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
     if (has) token_at[wave][rank] = (uint8_t)lane;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     seg.arow = r < seg.pass.rows ? (uint32_t)token_at[wave][skip + r] * (uint32_t)p.ldx * 2u : kOOB;
-    seg.rA = __builtin_amdgcn_make_buffer_rsrc((void*)p.x, 0, (int)(((uint32_t)(p.tokens - 1) * (uint32_t)p.ldx + (uint32_t)K) * 2u), kRsrcFlags);
+    seg.rA = view(p.x, ((uint32_t)(p.tokens - 1) * (uint32_t)p.ldx + (uint32_t)K) * 2u);
     seg.n = 2 * n;
     seg.row0 = c0 * 16;
 #pragma unroll
     for (int k = 0; k < 2; k++) {
       const int64_t row = ((int64_t)seg.pass.expert * 2 + k) * I + c0 * 16;
-      seg.rB[k] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.up + row * rowbytes), 0, (int)((uint32_t)(16 * n) * rowbytes), kRsrcFlags);
+      seg.rB[k] = view(p.up + row * rowbytes, (uint32_t)(16 * n) * rowbytes);
       // (FP8: I is a multiple of 128, and so is each kind's first row.)
       if (FMT == kFP8B128X128)
         seg.rS[k] = scale_view<FMT>(p.up_scales, ((int64_t)seg.pass.expert * 2 + k) * (I / 128), I / 128, K);
@@ -497,7 +506,7 @@ __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
   const int r = lane & 15, g = lane >> 4;
   const int K = p.inter, N = p.hidden, cols = N / 16;
   const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
-  Share mine = share(*p.w.count, cols, blockIdx.x);
+  Share mine = share(uniform(*p.w.count), cols, blockIdx.x);
   auto next = [&](Segment<1>& seg) __attribute__((always_inline)) {
     if (mine.at >= mine.end) return false;
     const int u = mine.pass, c0 = mine.col, n = min(cols - c0, mine.end - mine.at);
@@ -505,11 +514,11 @@ __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
     seg.pass = p.w.pass[u];
     uniform(seg.pass);
     seg.arow = r < seg.pass.rows ? (uint32_t)(r * K) * 2u : kOOB;
-    seg.rA = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w.h + (int64_t)seg.pass.row * K), 0, (int)((uint32_t)(seg.pass.rows * K) * 2u), kRsrcFlags);
+    seg.rA = view(p.w.h + (int64_t)seg.pass.row * K, (uint32_t)(seg.pass.rows * K) * 2u);
     seg.n = n;
     seg.row0 = c0 * 16;
     const int64_t row0 = (int64_t)seg.pass.expert * N + c0 * 16;
-    seg.rB[0] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.down + row0 * rowbytes), 0, (int)((uint32_t)(16 * n) * rowbytes), kRsrcFlags);
+    seg.rB[0] = view(p.down + row0 * rowbytes, (uint32_t)(16 * n) * rowbytes);
     if (FMT == kFP8B128X128)
       seg.rS[0] = scale_view<FMT>(p.down_scales, (int64_t)seg.pass.expert * ((N + 127) / 128), (N + 127) / 128, K);
     else
