@@ -42,8 +42,8 @@ using fp8::bf16x8;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr uint32_t kRsrcFlags = 0x00020000u;  // raw buffer, gfx9 data format
-// Lane and scalar offsets past every buffer's range (256 rows of at most 2^22
-// bytes); their sum is one too.
+// Lane and scalar offsets past every view's range (at most 2^30 bytes). A lane's offset of
+// kOOB and a scalar one of kScalarOOB past a view's last row do not meet: their sum may wrap.
 constexpr uint32_t kOOB = 0x80000000u, kScalarOOB = 0x40000000u;
 constexpr int kNonTemporal = 2;                // cache policy of a load: streamed
 constexpr int W = 8;                           // waves of a workgroup
@@ -189,7 +189,7 @@ struct Stream {
 #pragma unroll
       for (int h = 0; h < 2; h++)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(seg.rB[kind], (lds_ptr_t)(ring + (k % D) * kSlot + h * 1024), 16,
-                                                 s < nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
+                                                 s != nk - 1 ? vb[h] : vb_last[h], so, 0, kNonTemporal);
       if (FP4) {
         const int at = (int)(row * sstride + (s < nk ? (uint32_t)s * 8u : kScalarOOB));
         if (ALIGNED) {

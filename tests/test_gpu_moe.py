@@ -103,6 +103,31 @@ def test_exact_layers(fmt, T, E, top, kind):
         assert torch.equal(mx.moe(x, ids, weights, up, down), y.float().bfloat16())
 
 
+@pytest.mark.parametrize("fmt,H,I", [("mxfp4", 6176, 160), ("mxfp4", 8192, 96), ("mxfp4", 8224, 96), ("mxfp4", 96, 4224), ("mxfp4", 128, 8352),
+                                     ("mxfp4", 18464, 32), ("fp8_b128x128", 2176, 128), ("fp8_b128x128", 4224, 256), ("fp8_b128x128", 128, 4096),
+                                     ("fp8_b128x128", 256, 8576), ("int8", 2064, 48), ("int8", 4096, 16), ("int8", 4112, 80), ("int8", 16, 2192),
+                                     ("int8", 176, 8240)])
+def test_long_rows(fmt, H, I):
+    """Rows of two to nine steps a wave, in one round of loads and in several, whole steps and parts of one."""
+    require_gpu()
+    for T, E, top, kind in ((1, 2, 1, "distinct"), (20, 3, 2, "any"), (64, 5, 2, "distinct")):
+        x, up, down, vu, vd = _exact_layer(fmt, T, E, H, I, H + I)
+        ids, weights = _ids(T, E, top, T + H, kind)
+        assert 64 * 18 * 2 * I * top * 2 < 2**24 * 8  # (as above)
+        assert torch.equal(mx.moe(x, ids, weights, up, down, F32).double(), _exact(x, ids, weights, vu, vd)), (T, kind)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("T,E,top,kind", [(64, 400, 6, "distinct"), (64, 1024, 32, "any"), (50, 1000, 8, "any")])
+def test_more_passes_than_workgroups(fmt, T, E, top, kind):
+    require_gpu()
+    H, I = (288, 160) if fmt == "mxfp4" else (256, 128)
+    x, up, down, vu, vd = _exact_layer(fmt, T, E, H, I, 4)
+    ids, weights = _ids(T, E, top, T * H + I, kind)
+    assert 64 * 18 * 2 * I * top * 2 < 2**24 * 8  # (as above)
+    assert torch.equal(mx.moe(x, ids, weights, up, down, F32).double(), _exact(x, ids, weights, vu, vd))
+
+
 @pytest.mark.parametrize("out", [F32, BF16])
 @pytest.mark.parametrize("T,E,top", [(1, 8, 2), (5, 12, 4), (31, 6, 3)])
 @pytest.mark.parametrize("fmt", list(FMTS))
