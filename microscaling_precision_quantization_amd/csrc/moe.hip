@@ -9,7 +9,8 @@
 //  1. moe_up: h = silu(gate) up, in fp32, rounded to bf16, the activations' type, as the matrix
 //     cores take it. Each workgroup finds the passes from the ids by itself: a bit per token
 //     and expert in LDS, counted and scanned. Those with a pass's first columns write it
-//     down for what follows.
+//     down for what follows, and each what its like of moe_down begins with (which would else find that from the
+//     number of passes and its pass, one load after the other: 0.7 us), once its own first loads are out.
 //  2. moe_down: the rows' partial results, fp32.
 //  3. moe_combine: each token's partial results times their weights, in the ids' order. (In moe_down,
 //     by the last pass to be done with a column: no faster, as XCDs see each other's results only past
@@ -48,13 +49,20 @@ constexpr uint32_t kOOB = 0x80000000u, kScalarOOB = 0x40000000u;
 constexpr int kNonTemporal = 2;                // cache policy of a load: streamed
 constexpr int W = 8;                           // waves of a workgroup
 
-// Where the parts of the workspace are: the number of passes, the passes, each slot's
+// Where the parts of the workspace are: what each workgroup of moe_down begins with, the passes, each slot's
 // row (of ids of experts), h and the partial results.
 struct Pass {
   int expert, row, rows, unused;  // first row, rows
 };
+struct Share {
+  int at, end, pass, col;  // of columns of 16 of all passes, one after the other; pass and column of `at`
+};
+struct Begin {
+  Share share;
+  Pass pass;
+};
 struct Work {
-  int* count;
+  Begin* begin;
   Pass* pass;
   int* row_of;
   uint16_t* h;
@@ -135,7 +143,8 @@ struct Segment {
 
 // The products of a workgroup: its segments' rows of A (bf16) times their weight rows, K elements
 // each. Wave w takes the K steps w, w + W, ..., S of them; a row of more than W S steps takes several
-// rounds (MULTI). next(segment) gives one segment after the other, false behind the last.
+// rounds (MULTI). next(segment) gives one segment after the other, false behind the last. opened() is called
+// when its first loads are on their way, or there is none.
 // G tiles at a time, done(segment, first tile, sums) is called with the waves' sums in LDS,
 // sums[wave][tile][lane]: lane (r, g)'s row r, columns 4 g .. 4 g + 3 of the tile.
 template <int FMT, bool ALIGNED, int KINDS, int S, bool MULTI>
@@ -148,8 +157,8 @@ struct Stream {
   static_assert(G * S % D == 0 && G % KINDS == 0, "the ring's slots and the tiles' kinds are those of a place in the group");
   using Seg = Segment<KINDS>;
 
-  template <class Next, class Done>
-  static __device__ __forceinline__ void run(uint8_t* smem, int K, Next next_segment, Done done) {
+  template <class Next, class Opened, class Done>
+  static __device__ __forceinline__ void run(uint8_t* smem, int K, Next next_segment, Opened opened, Done done) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const uint32_t rowbytes = (uint32_t)(FP4 ? K / 2 : K);
@@ -233,14 +242,15 @@ struct Stream {
       return Codes{{*(const u32x4*)(at + frag0), *(const u32x4*)(at + frag1)}};
     };
 
-    if (!next_segment(seg)) return;
+    bool more = next_segment(seg);
+    if (!more) return opened();
     if (!MULTI) start(0);
-    bool more = true;
     while (more) {
       const int n = seg.n;
       const Pass pass = seg.pass;
       const int row0 = seg.row0;
       // (What comes next is found out beside the first loads.)
+      opened();
       Seg after;
       more = next_segment(after);
       if (!MULTI) started();
@@ -389,9 +399,6 @@ __device__ __forceinline__ void find_pass(const Args& p, const unsigned long lon
 // less time, a part of one pass: beginning with another pass costs about as much as kSwitch columns.
 constexpr int kGrid = 256;  // workgroups: one a CU
 constexpr int kSwitch = 2;
-struct Share {
-  int at, end, pass, col;  // pass and column of `at`
-};
 __device__ __forceinline__ Share share(int passes, int cols, int b) {
   Share s;
   const int all = passes * cols, each = kGrid / max(passes, 1), more = kGrid - passes * each;  // (all: at most 2^27)
@@ -434,9 +441,14 @@ __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
   route(p, tokens_of);
   const int K = p.hidden, I = p.inter, cols = I / 16;
   const int passes = uniform(count_passes(p, tokens_of));
-  if (blockIdx.x == 0 && tid == 0) *p.w.count = passes;
   const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
   Share mine = share(passes, cols, blockIdx.x);
+  // What is to be written down for the kernels that follow: the pass `opens` that this segment is the first of, with
+  // its tokens; before the first one, what this workgroup of moe_down begins with.
+  int opens = -1, opens_skip = 0;
+  Pass opens_pass{};
+  unsigned long long opens_tokens = 0;
+  bool first_segment = true;
   auto next = [&](Segment<2>& seg) __attribute__((always_inline)) {
     if (mine.at >= mine.end) return false;
     const int u = mine.pass, c0 = mine.col, n = min(cols - c0, mine.end - mine.at);
@@ -444,21 +456,12 @@ __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
     unsigned long long tokens = 0;
     int skip = 0;
     find_pass(p, tokens_of, u, seg.pass, tokens, skip);
+    opens = c0 == 0 ? u : -1;
+    opens_pass = seg.pass;
+    opens_tokens = tokens;
+    opens_skip = skip;
     const int rank = __builtin_popcountll(tokens & ((1ull << lane) - 1));
     const bool has = tokens >> lane & 1;
-    if (c0 == 0 && wave == 0) {
-      // The pass and its tokens' slots, for the kernels that follow.
-      if (lane == 0) p.w.pass[u] = seg.pass;
-      if (has && rank >= skip && rank < skip + seg.pass.rows)
-        for (int j0 = 0; j0 < p.top; j0 += 8) {
-          int id[8];
-#pragma unroll
-          for (int j = 0; j < 8; j++) id[j] = p.ids[lane * p.top + min(j0 + j, p.top - 1)];
-#pragma unroll
-          for (int j = 0; j < 8; j++)
-            if (j0 + j < p.top && id[j] == seg.pass.expert) p.w.row_of[lane * p.top + j0 + j] = seg.pass.row + rank - skip;
-        }
-    }
     // Row r's token is the one of rank skip + r.
     if (has) token_at[wave][rank] = (uint8_t)lane;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -478,7 +481,31 @@ __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
     }
     return true;
   };
-  St::run(smem, K, next, [&](const Pass& pass, int i0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
+  auto opened = [&]() __attribute__((always_inline)) {
+    if (wave == 0 && opens >= 0) {
+      const int rank = __builtin_popcountll(opens_tokens & ((1ull << lane) - 1)) - opens_skip;
+      if (lane == 0) p.w.pass[opens] = opens_pass;
+      if ((opens_tokens >> lane & 1) && rank >= 0 && rank < opens_pass.rows)
+        for (int j0 = 0; j0 < p.top; j0 += 8) {
+          int id[8];
+#pragma unroll
+          for (int j = 0; j < 8; j++) id[j] = p.ids[lane * p.top + min(j0 + j, p.top - 1)];
+#pragma unroll
+          for (int j = 0; j < 8; j++)
+            if (j0 + j < p.top && id[j] == opens_pass.expert) p.w.row_of[lane * p.top + j0 + j] = opens_pass.row + rank;
+        }
+    }
+    opens = -1;
+    if (first_segment && wave == 1) {
+      Begin b{share(passes, p.hidden / 16, blockIdx.x), Pass{}};
+      unsigned long long tokens = 0;
+      int skip = 0;
+      if (b.share.at < b.share.end) find_pass(p, tokens_of, b.share.pass, b.pass, tokens, skip);
+      if (lane == 0) p.w.begin[blockIdx.x] = b;
+    }
+    first_segment = false;
+  };
+  St::run(smem, K, next, opened, [&](const Pass& pass, int i0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
     // Two columns of four of a pair of tiles a wave.
     const int j = wave / 2, e0 = wave % 2 * 2, col = i0 + 8 * first + 16 * j + 4 * g + e0;
     if (j >= St::G / 2 || first + 2 * j >= n || r >= pass.rows) return;
@@ -506,12 +533,15 @@ __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
   const int r = lane & 15, g = lane >> 4;
   const int K = p.inter, N = p.hidden, cols = N / 16;
   const uint32_t rowbytes = (uint32_t)(FMT == kMXFP4 ? K / 2 : K);
-  Share mine = share(uniform(*p.w.count), cols, blockIdx.x);
+  const Begin begin = p.w.begin[blockIdx.x];
+  Share mine = {uniform(begin.share.at), uniform(begin.share.end), uniform(begin.share.pass), uniform(begin.share.col)};
+  bool first_segment = true;
   auto next = [&](Segment<1>& seg) __attribute__((always_inline)) {
     if (mine.at >= mine.end) return false;
     const int u = mine.pass, c0 = mine.col, n = min(cols - c0, mine.end - mine.at);
     mine = {mine.at + n, mine.end, u + 1, 0};
-    seg.pass = p.w.pass[u];
+    seg.pass = first_segment ? begin.pass : p.w.pass[u];
+    first_segment = false;
     uniform(seg.pass);
     seg.arow = r < seg.pass.rows ? (uint32_t)(r * K) * 2u : kOOB;
     seg.rA = view(p.w.h + (int64_t)seg.pass.row * K, (uint32_t)(seg.pass.rows * K) * 2u);
@@ -525,7 +555,7 @@ __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
       seg.rS[0] = scale_view<FMT>(p.down_scales, row0, 16 * n, K);
     return true;
   };
-  St::run(smem, K, next, [&](const Pass& pass, int n0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
+  St::run(smem, K, next, [] {}, [&](const Pass& pass, int n0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
     const int col = n0 + 16 * (first + wave) + 4 * g;
     if (wave >= St::G || first + wave >= n || r >= pass.rows) return;
     f32x4 v = St::sum(sums, wave);
@@ -609,7 +639,7 @@ hipError_t run(const Args& p, int out_dtype, hipStream_t s) {
 
 size_t moe_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t hidden, int64_t inter) {
   const int64_t slots = tokens * top;
-  return (size_t)(256 + align(most_passes(slots, experts) * (int64_t)sizeof(Pass)) + align(slots * 4) + align(slots * inter * 2) +
+  return (size_t)(align(kGrid * (int64_t)sizeof(Begin)) + align(most_passes(slots, experts) * (int64_t)sizeof(Pass)) + align(slots * 4) + align(slots * inter * 2) +
                   align(slots * hidden * 4));
 }
 
@@ -624,7 +654,7 @@ hipError_t moe(int fmt, int64_t tokens, int64_t top, int64_t experts, int64_t hi
     return r;
   };
   Work w;
-  w.count = (int*)take(4);
+  w.begin = (Begin*)take(kGrid * (int64_t)sizeof(Begin));
   w.pass = (Pass*)take(most_passes(slots, experts) * (int64_t)sizeof(Pass));
   w.row_of = (int*)take(slots * 4);
   w.h = (uint16_t*)take(slots * inter * 2);
