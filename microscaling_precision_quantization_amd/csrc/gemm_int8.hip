@@ -212,12 +212,23 @@ int64_t tiles(const Args& p, int bm, int bn) {
   return tm * ((p.N + bn - 1) / bn);
 }
 
+template <class G>
+int64_t workgroups(const Args& p) {
+  const int64_t n = p.offsets ? groups::max_row_tiles(p.M, p.groups, G::BM) : (p.M + G::BM - 1) / G::BM;
+  return groups::grid_size(n, (p.N + G::BN - 1) / G::BN);
+}
+
+// Whether a grid's 2^32 threads are enough. (gemm_block_fits: those of 64 x 128 by expert and 128 x 128 are.)
+template <class G>
+bool fits(const Args& p) {
+  return workgroups<G>(p) * G::kThreads < (int64_t)1 << 32;
+}
+
 template <int OUT, class G>
 hipError_t launch(const Args& a, hipStream_t s) {
   Args p = a;
   p.tiles_n = (int)((p.N + G::BN - 1) / G::BN);
-  const int64_t n = p.offsets ? groups::max_row_tiles(p.M, p.groups, G::BM) : (p.M + G::BM - 1) / G::BM;
-  return launch_kernel(&gemm_int8_kernel<OUT, G>, dim3((unsigned)groups::grid_size(n, p.tiles_n)), G::kThreads, 0, s, p);
+  return launch_kernel(&gemm_int8_kernel<OUT, G>, dim3((unsigned)workgroups<G>(p)), G::kThreads, 0, s, p);
 }
 
 // The tile: 32 x 32, 64 x 64, 64 x 128 or 128 x 128 (the last in 8 waves that divide K: 36 us, 39
@@ -236,11 +247,14 @@ hipError_t launch(const Args& a, hipStream_t s) {
 template <int OUT>
 hipError_t by_tile(const Args& p, hipStream_t s) {
   const int64_t t64 = tiles(p, 64, 64);
-  if (p.M <= 32 || t64 < 150 || (p.offsets && rows_each(p) <= 24)) return launch<OUT, Geo<1, 1, 2, 2, 1, 2, 6>>(p, s);
+  using Tile32 = Geo<1, 1, 2, 2, 1, 2, 6>;
+  using Tile64 = Geo<2, 1, 2, 4, 1, 2, 3>;
+  using Tile64x128 = Geo<2, 2, 2, 4, 1, 2, 3>;
+  if ((p.M <= 32 || t64 < 150 || (p.offsets && rows_each(p) <= 24)) && fits<Tile32>(p)) return launch<OUT, Tile32>(p, s);
   if (t64 <= 256) return launch<OUT, Geo<2, 1, 2, 4, 1, 2, 4>>(p, s);
   if (tiles(p, 64, 128) <= 256) return launch<OUT, Geo<2, 2, 2, 4, 1, 2, 4>>(p, s);
-  if (p.K <= 1024) return launch<OUT, Geo<2, 2, 2, 4, 1, 2, 3>>(p, s);
-  if (p.offsets) return launch<OUT, Geo<2, 1, 2, 4, 1, 2, 3>>(p, s);
+  if (p.offsets && p.K > 1024 && fits<Tile64>(p)) return launch<OUT, Tile64>(p, s);
+  if (p.offsets || (p.K <= 1024 && fits<Tile64x128>(p))) return launch<OUT, Tile64x128>(p, s);
   return launch<OUT, Geo<4, 4, 2, 2, 2, 1, 4>>(p, s);
 }
 

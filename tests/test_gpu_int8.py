@@ -220,6 +220,27 @@ GROUPED = [([1], 16, 16), ([0, 1, 0], 40, 48), ([3, 0, 2, 1], 200, 2064), ([1] *
            ([31, 64, 65, 129, 2, 90], 4000, 1040), ([30] * 40, 1500, 272)]
 
 
+@pytest.mark.parametrize("M,groups,N", [(32, 0, (1 << 29) + 48), (4096, 4096, 1 << 17)])
+def test_more_small_tiles_than_a_grid(M, groups, N):
+    """Few rows of a weight, or of each of many experts, and so many columns that tiles of 32 x 32 are more than a launch may have."""
+    require_gpu()
+    K, E = 16, max(groups, 1)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    a = mx.QTensor(mx.MX_FMT_INT8, M, K, torch.randint(0, 256, (M, K), dtype=torch.uint8, device="cuda", generator=g), torch.ones(M, device="cuda"))
+    b = mx.QTensor(mx.MX_FMT_INT8, E * N, K, torch.randint(0, 256, (E * N, K), dtype=torch.uint8, device="cuda", generator=g),
+                   torch.ones(E * N, device="cuda"), groups=E)
+    if groups:
+        c = mx.gemm_grouped(a, b, torch.arange(E + 1, dtype=torch.int32, device="cuda"))
+    else:
+        c = mx.gemm(a, b, BF16)
+    av = a.codes.view(torch.int8).float()
+    for at in (0, N // 3 // 64 * 64 + 16, N - 4096):
+        bv = b.codes.view(E, N, K)[:, at:at + 4096].view(torch.int8).float()
+        # (sums of at most 16 * 2^14: exact in fp32)
+        want = torch.cat([av[i:i + 1] @ bv[i].t() for i in range(E)]) if groups else av @ bv[0].t()
+        assert torch.equal(c[:, at:at + 4096], want.bfloat16()), at
+
+
 @pytest.mark.parametrize("out", [F32, BF16])
 @pytest.mark.parametrize("sizes,N,K", GROUPED)
 def test_grouped(sizes, N, K, out):
