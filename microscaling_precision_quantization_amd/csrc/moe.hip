@@ -433,9 +433,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_view(const void* scales,
 template <int FMT, bool ALIGNED, int S, bool MULTI>
 __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
   using St = Stream<FMT, ALIGNED, 2, S, MULTI>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[St::kSmem];
-  __shared__ unsigned long long tokens_of[kMoeMaxExperts];
-  __shared__ uint8_t token_at[W][64];
+  // One array for all. (With several the compiler waits for all loads under way before it reads any, as it can not
+  // tell which array they go to.)
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[St::kSmem + kMoeMaxExperts * 8 + W * 64];
+  unsigned long long* tokens_of = (unsigned long long*)(smem + St::kSmem);
+  uint8_t(*token_at)[64] = (uint8_t(*)[64])(smem + St::kSmem + kMoeMaxExperts * 8);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   route(p, tokens_of);
