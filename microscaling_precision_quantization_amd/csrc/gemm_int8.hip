@@ -48,6 +48,8 @@ struct Geo {
   static constexpr int kRpb = 64 / kCpr;                        // rows per 1 KB load of a wave
   static constexpr int kOffB = BM * kRow, kStage = kOffB + BN * kRow;
   static constexpr int kLoads = (BM + BN) / kRpb / kWaves;  // of a wave and step
+  static constexpr int kReads = KPW * (TMW + TNW);          // LDS reads of its fragments
+  static_assert(kReads <= 15, "a wait's count");
   static constexpr int kSums = WK > 1 ? kWaves * TMW * TNW * 1024 : 0;
   static constexpr int kSmem = NS * kStage > kSums ? NS * kStage : kSums;
   static_assert(kRow >= 128 && kRow <= 1024 && kSmem <= 160 * 1024 && (NS - 1) * kLoads < 64 && NS >= 3, "step");
@@ -139,8 +141,8 @@ __global__ __launch_bounds__(G::kThreads) void gemm_int8_kernel(Args p) {
   // Step s's products, beside the reads of step s + 1's fragments.
   auto step = [&](int s, const Frags& cur, Frags& nxt) __attribute__((always_inline)) {
     // Step s + 1 has arrived (the later steps' loads may still be out), and every wave
-    // has the fragments of step s - 1, whose stage takes step s + NS - 1.
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"((G::NS - 3) * G::kLoads) : "memory");
+    // has the fragments of step s - 1 (those of step s may still be out), whose stage takes step s + NS - 1.
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(%1)\n\ts_barrier" ::"i"((G::NS - 3) * G::kLoads), "i"(G::kReads) : "memory");
     issue(s + G::NS - 1, smem + (at == 0 ? G::NS - 1 : at - 1) * G::kStage);
     at = at == G::NS - 1 ? 0 : at + 1;
     read(smem + at * G::kStage, nxt);
