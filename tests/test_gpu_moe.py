@@ -345,3 +345,38 @@ def test_experts_past_32_bits():
     small = torch.tensor([[2, 0], [1, 2]], dtype=torch.int32, device="cuda")
     y, tol = ref.layer(x, small, weights, torch.cat(us), torch.cat(ds))
     ref.check(got, y, tol, F32)
+
+
+@pytest.mark.parametrize("H,I", [(1 << 20, 1024), (1024, 1 << 20)])
+@pytest.mark.parametrize("fmt", ["int8", "fp8_b128x128"])
+def test_widest(fmt, H, I):
+    """The largest widths and weights there may be; exact, as few values of x and of h are not zero."""
+    require_gpu()
+    T, g = 3, _gen(7)
+
+    def stack(v):  # whole numbers -2 .. 2
+        rows, cols = v.shape
+        if fmt == "int8":
+            return mx.QTensor(FMTS[fmt], rows, cols, v.view(torch.uint8), torch.ones(rows, device="cuda"))
+        a = v.abs().view(torch.uint8)
+        return mx.QTensor(FMTS[fmt], rows, cols, (a * 8 + 0x30) * (a > 0) | (v < 0) * torch.tensor(0x80, dtype=torch.uint8, device="cuda"),
+                          torch.ones(-(-rows // 128), cols // 128, device="cuda"))
+    up = torch.randint(-2, 3, (2 * I, H), dtype=torch.int8, device="cuda", generator=g)
+    busy = torch.cat([torch.randint(0, I, (500,), device="cuda", generator=g), torch.tensor([0, I - 1], device="cuda")])
+    idle = torch.ones(I, dtype=torch.bool, device="cuda")
+    idle[busy] = False
+    up[:I] = 0
+    up[:I, 0] = 1
+    up[I:][idle] = 0
+    up[I:, 0] = 0
+    down = torch.randint(-2, 3, (H, I), dtype=torch.int8, device="cuda", generator=g)
+    x = torch.zeros(T, H, device="cuda")
+    at = torch.cat([torch.randint(1, H - 1, (2,), device="cuda", generator=g), torch.tensor([0, H - 1], device="cuda")])
+    x[:, at[:2]], x[:, H - 1], x[:, 0] = 2, 3, 64
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    weights = torch.tensor([[1.0], [0.5], [2.0]], device="cuda")
+    lin = up[I:][:, at].double() @ x[:, at].double().t()
+    assert len(set(at.tolist())) == 4 and lin.abs().max() <= 14  # so every sum is of multiples of 64, at most 64 * 14 * 2 * 502
+    h = 64 * lin[busy.unique()]
+    y = (down[:, busy.unique()].double() @ h).t() * weights.double()
+    assert torch.equal(mx.moe(x.bfloat16(), ids, weights, stack(up), stack(down), F32).double(), y)
