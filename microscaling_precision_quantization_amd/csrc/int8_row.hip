@@ -21,7 +21,9 @@
 // fp32 step of amax / 127, at worst 2^-10 of it.
 //
 // Bound by HBM: 3 bytes an element, each read and written once. A row stays in
-// registers between its amax and its codes.
+// registers between its amax and its codes. Measured in us: 28672 x 8192 117 (6.0 TB/s), 8192 x 8192
+// 34, 1024 x 8192 5.8. With non-temporal stores of the codes 110, 33 and 6.1, but the product of
+// these with 4096 columns, which then finds them in no cache, takes 30, 3 and 2.5 more.
 #include "bf16.h"
 #include "fp8_encode.h"
 #include "mx_internal.h"
