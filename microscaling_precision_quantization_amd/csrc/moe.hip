@@ -275,14 +275,18 @@ struct Stream {
             if (first + t >= n) return;  // (the last group's)
             const Codes bv = next;
             u32x2 wscale = wsc[k % D];
-            // Into the slot of the step before, which has been read. (MULTI: what is past
-            // the group is loaded again by the next start.)
-            load(std::integral_constant<int, k + D - 1>{}, first);
+            // Into the slot of the step before, which has been read. (MULTI: nothing past the group, as the next
+            // start loads anew. Its scales would be unused, the compiler would leave their loads out, and the waits,
+            // which count a step's loads, would end before they should.)
+            constexpr int last = !MULTI || k + D - 1 < G * S ? k + D - 1 : G * S - 1;  // the last step loaded
+            if constexpr (last == k + D - 1) load(std::integral_constant<int, last>{}, first);
             // Step k + 1's fragments are read before step k's MFMAs. Loads end in order: step k + 1's
-            // have arrived when only the D - 2 later steps' are out (and stores, if any, besides).
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("s_waitcnt vmcnt(%0)" ::"i"((D - 2) * kLoads) : "memory");
-            __builtin_amdgcn_sched_barrier(0);
+            // have arrived when only the later steps' are out (and stores, if any, besides).
+            if constexpr (last > k) {
+              __builtin_amdgcn_sched_barrier(0);
+              asm volatile("s_waitcnt vmcnt(%0)" ::"i"((last - (k + 1)) * kLoads) : "memory");
+              __builtin_amdgcn_sched_barrier(0);
+            }
             if constexpr (k + 1 < G * S) next = read(k + 1);
             f32x4 P = FP8 ? f32x4{0, 0, 0, 0} : acc[t];
             if (FP4 && ALIGNED && step(i) * 8 + 4 >= (int)sstride) wscale.y = 0;  // (K % 256 = 128)

@@ -380,3 +380,53 @@ def test_widest(fmt, H, I):
     h = 64 * lin[busy.unique()]
     y = (down[:, busy.unique()].double() @ h).t() * weights.double()
     assert torch.equal(mx.moe(x.bfloat16(), ids, weights, stack(up), stack(down), F32).double(), y)
+
+
+def _scaled(fmt, v, seed, rows_at_one=0):
+    """A stack of whole numbers in `fmt` with scales of 1 and 2 (by block, INT8 by row; the first rows' 1), and its values."""
+    q, (E, rows, cols) = _whole(fmt, v), v.shape
+    two = torch.randint(0, 2, q.scales.shape, device="cuda", generator=_gen(seed))
+    if fmt == "fp8_b128x128":
+        two[:, :rows_at_one // 128] = 0
+        by_row = two.repeat_interleave(128, 1)[:, :rows].repeat_interleave(128, 2)
+    else:
+        two.view(E, rows, -1)[:, :rows_at_one] = 0
+        by_row = two.view(E, rows, -1).repeat_interleave(32 if fmt == "mxfp4" else cols, 2)
+    q.scales += two.to(q.scales.dtype)
+    return q, v.double() * (1 + by_row)
+
+
+def _dense_layer(fmt, T, E, H, I, seed):
+    """As _exact_layer, but a twelfth of x and two thirds of the up and down weights are not zero, so
+    that a wrong code of any step changes a result."""
+    g = _gen(seed)
+    up = torch.randint(-1, 2, (E, 2 * I, H), dtype=torch.int8, device="cuda", generator=g)
+    up[:, :I] = 0
+    up[:, :I, 0] = 1
+    up[:, I:, 0] = 0
+    down = torch.randint(-1, 2, (E, H, I), dtype=torch.int8, device="cuda", generator=g)
+    x = torch.randint(0, 2, (T, H), device="cuda", generator=g) * 2.0 - 1
+    x *= torch.rand(T, H, device="cuda", generator=g) < 1 / 12
+    x[:, 0] = 64
+    up, vu = _scaled(fmt, up, seed + 1, I)
+    down, vd = _scaled(fmt, down, seed + 2)
+    return x.bfloat16(), up, down, vu, vd
+
+
+@pytest.mark.parametrize("fmt,H,I", [("mxfp4", 8224, 8416), ("mxfp4", 8448, 8320), ("mxfp4", 4096, 14336), ("fp8_b128x128", 5120, 7168),
+                                     ("fp8_b128x128", 7168, 5120), ("int8", 5120, 5136), ("int8", 7168, 4112)])
+def test_dense_long_rows(fmt, H, I):
+    """Rows of several rounds of loads, bit for bit, on weights larger than the last-level cache. Tiles of a
+    workgroup that fill their groups and that do not."""
+    require_gpu()
+    E = 6
+    x, up, down, vu, vd = _dense_layer(fmt, 40, E, H, I, H + I)
+    # h is 64 times a whole number that bf16 holds; down's sums are of multiples of 64 and, weighted, of 64 / 8, all
+    # below 2^24 of them.
+    lin = torch.stack([vu[e, I:] @ x.double().t() for e in range(E)])
+    assert lin.abs().max() <= 256 and vd.abs().sum(2).max() * 256 < 2**24
+    assert max((vd[e] @ lin[e]).abs().max() for e in range(E)) * 64 * 2 * 3 < 2**24 * 8
+    for T, top, kind in ((1, 1, "distinct"), (2, 2, "distinct"), (5, 3, "any"), (40, 2, "distinct")):
+        ids, weights = _ids(T, E, top, T + H, kind)
+        got = mx.moe(x[:T], ids, weights, up, down, F32)
+        assert torch.equal(got.double(), _exact(x[:T], ids, weights, vu, vd)), (T, kind)
