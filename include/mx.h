@@ -424,10 +424,11 @@ mx_status mx_gemm_grouped(mx_format fmt_a, mx_format fmt_b, int block, mx_round 
  *   without experts).
  * workspace: device scratch of at least mx_moe_workspace_bytes(...) bytes, 16-byte aligned,
  *   needing no initialization; calls that may overlap need one each.
- * Sums are fp32 over exactly expanded codes, in a fixed order; h is rounded to bf16
- * once. With the products of a row of codes and its scale in fp32's range, and in units
- * of u = 2^-24: gate_e x and up_e x err by at most (hidden / 16 + 12) u times the sum of their
- * terms' magnitudes, h then by 2^-8 of itself, and down_e h by (inter / 16 + 12) u times its own.
+ * Sums are fp32 over exactly expanded codes, in a fixed order; h enters its products as
+ * two bf16 numbers, the nearest and what is left. With the products of a row of codes and its
+ * scale in fp32's range, and in units of u = 2^-24: gate_e x and up_e x err by at most
+ * (hidden / 16 + 12) u times the sum of their terms' magnitudes, h then by 2^-17 of itself, and
+ * down_e h by (inter / 8 + 12) u times its own.
  */
 size_t mx_moe_workspace_bytes(int64_t tokens, int64_t top, int64_t experts, int64_t hidden,
                               int64_t inter);

@@ -6,11 +6,13 @@
 // at most 16 tokens at a time. Tokens of one expert are a group; up to 16 of them a
 // pass; the (token, expert) pairs, sorted by expert and token, are the rows of h and of the
 // partial results.
-//  1. moe_up: h = silu(gate) up, in fp32, rounded to bf16, the activations' type, as the matrix
-//     cores take it. Each workgroup finds the passes from the ids by itself: a bit per token
-//     and expert in LDS, counted and scanned. Those with a pass's first columns write it
-//     down for what follows, and each what its like of moe_down begins with (which would else find that from the
-//     number of passes and its pass, one load after the other: 0.7 us), once its own first loads are out.
+//  1. moe_up: h = silu(gate) up, in fp32, written as two bf16 numbers for the matrix cores, the nearest
+//     and what is left. (One alone, a rounding of 2^-8 of each element, put bf16 results 2.4e-3 from 64
+//     bits, which their own rounding puts 1.7e-3 from it, and fp32 results as far.) Each workgroup finds
+//     the passes from the ids by itself: a bit per token and expert in LDS, counted and scanned. Those
+//     with a pass's first columns write it down for what follows, and each what its like of moe_down
+//     begins with (which would else find that from the number of passes and its pass, one load after the
+//     other: 0.7 us), once its own first loads are out.
 //  2. moe_down: the rows' partial results, fp32.
 //  3. moe_combine: each token's partial results times their weights, in the ids' order. (In moe_down,
 //     by the last pass to be done with a column: no faster, as XCDs see each other's results only past
@@ -133,6 +135,24 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t view(const void* base, uint32_
   return __builtin_amdgcn_make_buffer_rsrc((void*)u, 0, uniform((int)bytes), kRsrcFlags);
 }
 
+// A number as two in bf16: the nearest (or, next to fp32's largest, the largest), as bits, and what is left. Their sum is
+// within 2^-17 of it: what is left is at most half a step of the first, exactly, and is rounded by half of its own.
+struct Split {
+  uint32_t high;
+  float low;
+};
+__device__ __forceinline__ Split split(float v) {
+  const bool finite = __builtin_fabsf(v) < __builtin_inff();
+  uint32_t high = bf16_bits(v);
+  if (finite && (high & 0x7FFFu) == 0x7F80u) high = __builtin_bit_cast(uint32_t, v) >> 16;
+  return {high, finite ? v - __builtin_bit_cast(float, high << 16) : 0.0f};
+}
+
+// Lane (r, g)'s value from lane ((r + 8) % 16, g).
+__device__ __forceinline__ float row_plus8(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x128 /* row_ror:8 */, 0xF, 0xF, false));
+}
+
 // What a workgroup does of one pass: `n` tiles of 16 weight rows, tile t of kind t % KINDS (the
 // gate's and the up projection's rows) from row 16 (t / KINDS) of its kind's view on. The views end
 // with the tiles there are. A's view and lane (r, g)'s row's first byte in it (kOOB: no such row).
@@ -152,7 +172,9 @@ struct Segment {
 // when its first loads are on their way, or there is none.
 // G tiles at a time, done(segment, first tile, sums) is called with the waves' sums in LDS,
 // sums[wave][tile][lane]: lane (r, g)'s row r, columns 4 g .. 4 g + 3 of the tile.
-template <int FMT, bool ALIGNED, int KINDS, int S, bool MULTI>
+// PARTS: 1, or 2 where a row of A holds K numbers' high parts and then their low ones (split), which
+// take registers and matrix instructions of their own.
+template <int FMT, bool ALIGNED, int KINDS, int S, bool MULTI, int PARTS>
 struct Stream {
   static constexpr bool FP4 = FMT == kMXFP4, FP8 = FMT == kFP8B128X128;
   // (D = 6, with which G is 4 or 6: 2 to 6% slower. S = 4 leaves VGPRs for the sums of 4 tiles.)
@@ -219,19 +241,19 @@ struct Stream {
         wsc[k % D].x = __builtin_amdgcn_raw_buffer_load_b32(
             seg.rS[kind], 0, (int)(((uint32_t)seg.row0 + row) / 128u * sstride + (s < nk ? (uint32_t)s * 4u : kScalarOOB)), 0);
     };
-    u32x4 a[S][kFrags];  // (of lanes without a row: anything, for rows of the result that nobody reads)
+    u32x4 a[PARTS][S][kFrags];  // (of lanes without a row: anything, for rows of the result that nobody reads)
     // A's fragments, then the ring's first weights. (The other way round A's loads wait for the weights'.)
     auto start = [&](int first) __attribute__((always_inline)) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the ring is free)
 #pragma unroll
-      for (int i = 0; i < S; i++)
-#pragma unroll
-        for (int j = 0; j < kFrags; j++) {
-          constexpr int kPer = kFrags / 2;  // 16-byte pieces of A that meet a 16-byte chunk of codes
-          const uint32_t chunk = (uint32_t)(step(i) * 8 + j / kPer * 4 + g);
-          a[i][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-              seg.rA, chunk * 16u < rowbytes ? seg.arow + (uint32_t)g * (16u * kPer) : kOOB, (step(i) * 8 + j / kPer * 4) * (16 * kPer) + j % kPer * 16, 0));
-        }
+      for (int n = 0; n < PARTS * S * kFrags; n++) {
+        const int part = n / (S * kFrags), i = n / kFrags % S, j = n % kFrags;
+        constexpr int kPer = kFrags / 2;  // 16-byte pieces of A that meet a 16-byte chunk of codes
+        const uint32_t chunk = (uint32_t)(step(i) * 8 + j / kPer * 4 + g);
+        a[part][i][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+            seg.rA, chunk * 16u < rowbytes ? seg.arow + (uint32_t)g * (16u * kPer) : kOOB,
+            part * 2 * K + (step(i) * 8 + j / kPer * 4) * (16 * kPer) + j % kPer * 16, 0));
+      }
       __builtin_amdgcn_sched_barrier(0);
       unroll<D - 1>([&](auto kk) __attribute__((always_inline)) { load(kk, first); });
     };
@@ -300,7 +322,9 @@ struct Stream {
                   w = expand_fp4(bv.h[h][j], scale);
                 else
                   w = FP8 ? fp8::expand8((int)bv.h[h][2 * j], (int)bv.h[h][2 * j + 1]) : expand_int8(bv.h[h][2 * j], bv.h[h][2 * j + 1]);
-                P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, a[i][h * (kFrags / 2) + j]), P, 0, 0, 0);
+#pragma unroll
+                for (int part = 0; part < PARTS; part++)
+                  P = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, a[part][i][h * (kFrags / 2) + j]), P, 0, 0, 0);
               }
             }
             if constexpr (FP8) {
@@ -444,7 +468,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_view(const void* scales,
 
 template <int FMT, bool ALIGNED, int S, bool MULTI>
 __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
-  using St = Stream<FMT, ALIGNED, 2, S, MULTI>;
+  using St = Stream<FMT, ALIGNED, 2, S, MULTI, 1>;
   // One array for all. (With several the compiler waits for all loads under way before it reads any, as it can not
   // tell which array they go to.)
   __shared__ __attribute__((aligned(1024))) uint8_t smem[St::kSmem + kMoeMaxExperts * 8 + W * 64];
@@ -532,16 +556,22 @@ __global__ __launch_bounds__(64 * W, 2) void moe_up_kernel(Args p) {
         up[e] *= s[I + e];
       }
     }
-    float h[2];
+    Split h[2];
 #pragma unroll
-    for (int e = 0; e < 2; e++) h[e] = gate[e] / (1.0f + expf(-gate[e])) * up[e];
-    *(uint32_t*)(p.w.h + (int64_t)(pass.row + r) * I + col) = pack_bf16x2(h[0], h[1]);
+    for (int e = 0; e < 2; e++) h[e] = split(gate[e] / (1.0f + expf(-gate[e])) * up[e]);
+    uint16_t* at = p.w.h + (int64_t)(pass.row + r) * 2 * I + col;
+    *(uint32_t*)at = h[0].high | h[1].high << 16;
+    *(uint32_t*)(at + I) = pack_bf16x2(h[0].low, h[1].low);
   });
 }
 
-template <int FMT, bool ALIGNED, int S, bool MULTI>
+// FEW: no pass has more than 8 rows. Their low parts are then A's rows 8 to 15, and the results of rows r and r + 8 are
+// added: no more loads and products than h in one part takes (one token, 8 experts of 4096 x 2048, MXFP4, the layer 30.8
+// -> 31.0 us). Else a lane's row has both, twice the loads of A and the products (64 tokens, all of 64 experts, 171.5 -> 179;
+// 17 tokens, 2 of 5 of 2880 x 1440 23.0 -> 24.2; 32 tokens, INT8, 4 of 64 of 4096 x 2048 237 -> 239).
+template <int FMT, bool ALIGNED, int S, bool MULTI, bool FEW>
 __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
-  using St = Stream<FMT, ALIGNED, 1, S, MULTI>;
+  using St = Stream<FMT, ALIGNED, 1, S, MULTI, FEW ? 1 : 2>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[St::kSmem];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -557,8 +587,9 @@ __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
     seg.pass = first_segment ? begin.pass : p.w.pass[u];
     first_segment = false;
     uniform(seg.pass);
-    seg.arow = r < seg.pass.rows ? (uint32_t)(r * K) * 2u : kOOB;
-    seg.rA = view(p.w.h + (int64_t)seg.pass.row * K, (uint32_t)(seg.pass.rows * K) * 2u);
+    const int row = FEW ? r % 8 : r;
+    seg.arow = row < seg.pass.rows ? (uint32_t)(row * K) * 4u + (row != r ? (uint32_t)K * 2u : 0u) : kOOB;
+    seg.rA = view(p.w.h + (int64_t)seg.pass.row * 2 * K, (uint32_t)(seg.pass.rows * K) * 4u);
     seg.n = n;
     seg.row0 = c0 * 16;
     const int64_t row0 = (int64_t)seg.pass.expert * N + c0 * 16;
@@ -571,8 +602,13 @@ __global__ __launch_bounds__(64 * W, 2) void moe_down_kernel(Args p) {
   };
   St::run(smem, K, next, [] {}, [&](const Pass& pass, int n0, int n, int first, const f32x4(*sums)[St::G][64]) __attribute__((always_inline)) {
     const int col = n0 + 16 * (first + wave) + 4 * g;
-    if (wave >= St::G || first + wave >= n || r >= pass.rows) return;
+    if (wave >= St::G || first + wave >= n) return;
     f32x4 v = St::sum(sums, wave);
+    if (FEW) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) v[e] += row_plus8(v[e]);
+    }
+    if (r >= pass.rows) return;
     if (FMT == kINT8) {
       const float* s = (const float*)p.down_scales + (int64_t)pass.expert * N + col;
 #pragma unroll
@@ -621,29 +657,45 @@ int64_t align(int64_t n) { return (n + 255) / 256 * 256; }
 // Passes that any ids can need.
 int64_t most_passes(int64_t slots, int64_t experts) { return groups::max_row_tiles(slots, experts, 16); }
 
-template <int FMT, bool UP, int S, bool MULTI>
+// FEW: of moe_down.
+template <int FMT, bool UP, int S, bool MULTI, bool FEW>
 hipError_t launch(const Args& p, hipStream_t s) {
-  const int K = UP ? p.hidden : p.inter;
+  auto product = [&](auto aligned) {
+    constexpr bool ALIGNED = decltype(aligned)::value;
+    if constexpr (UP)
+      return launch_kernel(&moe_up_kernel<FMT, ALIGNED, S, MULTI>, dim3(kGrid), 64 * W, 0, s, p);
+    else
+      return launch_kernel(&moe_down_kernel<FMT, ALIGNED, S, MULTI, FEW>, dim3(kGrid), 64 * W, 0, s, p);
+  };
   if constexpr (FMT == kMXFP4) {
-    if (K % 128 != 0) return launch_kernel(UP ? &moe_up_kernel<FMT, false, S, MULTI> : &moe_down_kernel<FMT, false, S, MULTI>, dim3(kGrid), 64 * W, 0, s, p);
+    if ((UP ? p.hidden : p.inter) % 128 != 0) return product(std::false_type{});
   }
-  return launch_kernel(UP ? &moe_up_kernel<FMT, true, S, MULTI> : &moe_down_kernel<FMT, true, S, MULTI>, dim3(kGrid), 64 * W, 0, s, p);
+  return product(std::true_type{});
 }
 
-// Steps a wave: as few as take a row's in one round, within the registers that A's fragments of them take.
-template <int FMT, bool UP>
+// Steps a wave: as few as take a row's in one round, within the registers that A's fragments of them take (both
+// parts of 4 steps of MXFP4: too many. In rounds of 2: 16 tokens, 2 of 8 experts of 4096 x 14336, 157 us; 154 with one
+// part in rounds of 4).
+template <int FMT, bool UP, bool FEW>
 hipError_t by_length(const Args& p, hipStream_t s) {
   const int K = UP ? p.hidden : p.inter, nk = (K + (FMT == kMXFP4 ? 255 : 127)) / (FMT == kMXFP4 ? 256 : 128);
-  if (nk <= W) return launch<FMT, UP, 1, false>(p, s);
-  if (nk <= 2 * W) return launch<FMT, UP, 2, false>(p, s);
-  if (nk <= 4 * W) return launch<FMT, UP, 4, false>(p, s);
-  return launch<FMT, UP, 4, true>(p, s);
+  if (nk <= W) return launch<FMT, UP, 1, false, FEW>(p, s);
+  if (nk <= 2 * W) return launch<FMT, UP, 2, false, FEW>(p, s);
+  if constexpr (FMT == kMXFP4 && !UP && !FEW) {
+    return launch<FMT, UP, 2, true, FEW>(p, s);
+  } else {
+    if (nk <= 4 * W) return launch<FMT, UP, 4, false, FEW>(p, s);
+    return launch<FMT, UP, 4, true, FEW>(p, s);
+  }
 }
 
 template <int FMT>
 hipError_t run(const Args& p, int out_dtype, hipStream_t s) {
-  MX_TRY((by_length<FMT, true>(p, s)));
-  MX_TRY((by_length<FMT, false>(p, s)));
+  MX_TRY((by_length<FMT, true, false>(p, s)));
+  if (p.tokens <= 8)
+    MX_TRY((by_length<FMT, false, true>(p, s)));
+  else
+    MX_TRY((by_length<FMT, false, false>(p, s)));
   const dim3 grid((unsigned)((p.hidden + 1023) / 1024), (unsigned)p.tokens);
   if (out_dtype == kOutF32) return launch_kernel(&moe_combine_kernel<kOutF32>, grid, 256, 0, s, p);
   return launch_kernel(&moe_combine_kernel<kOutBF16>, grid, 256, 0, s, p);
@@ -653,7 +705,7 @@ hipError_t run(const Args& p, int out_dtype, hipStream_t s) {
 
 size_t moe_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t hidden, int64_t inter) {
   const int64_t slots = tokens * top;
-  return (size_t)(align(kGrid * (int64_t)sizeof(Begin)) + align(most_passes(slots, experts) * (int64_t)sizeof(Pass)) + align(slots * 4) + align(slots * inter * 2) +
+  return (size_t)(align(kGrid * (int64_t)sizeof(Begin)) + align(most_passes(slots, experts) * (int64_t)sizeof(Pass)) + align(slots * 4) + align(slots * inter * 4) +
                   align(slots * hidden * 4));
 }
 
@@ -671,7 +723,7 @@ hipError_t moe(int fmt, int64_t tokens, int64_t top, int64_t experts, int64_t hi
   w.begin = (Begin*)take(kGrid * (int64_t)sizeof(Begin));
   w.pass = (Pass*)take(most_passes(slots, experts) * (int64_t)sizeof(Pass));
   w.row_of = (int*)take(slots * 4);
-  w.h = (uint16_t*)take(slots * inter * 2);
+  w.h = (uint16_t*)take(slots * inter * 4);
   w.part = (float*)take(slots * hidden * 4);
   const Args p{(const uint16_t*)x, ids, weights, (const uint8_t*)up, (const uint8_t*)down, up_scales, down_scales, y, ldx, ldy,
                (int)tokens, (int)top, (int)experts, (int)hidden, (int)inter, w};

@@ -27,7 +27,7 @@ def stack_values(q, mx):
     return (v * torch.where(s == 255, float("nan"), torch.exp2(s.double() - 127))).view(g, rows, cols)
 
 
-def layer(x, ids, weights, up, down, random=True):
+def layer(x, ids, weights, up, down, random=True, parts=1):
     """(y, tolerance before the result's own rounding) in 64 bits; up, down: values.
     Errors, u = 2^-24: a product's sums (K / 16 + 12) u of their terms' magnitudes; the
     silu, whose slope is at most 1.1, and the product after it 16 u (1 + |gate|) of h
@@ -36,7 +36,9 @@ def layer(x, ids, weights, up, down, random=True):
     terms. With `random` the roundings of h, each within its bound b_i = 2^-8 |h_i d_i| of a
     term and of either sign as likely, add up to at most sqrt(2 ln(2 n / 1e-9) sum of b_i^2), but
     for a probability of 1e-9 that one of n outputs passes it (Hoeffding's inequality); otherwise to
-    the sum of the b_i."""
+    the sum of the b_i. With h in two `parts`, the nearest bf16 number and what is left of it, in bf16: of h in
+    [1, 2) at most 2^-8 is left, exactly, and rounded by at most 2^-17 (below 2^-8 its steps are 2^-16 at most); the
+    products are twice as many, and so are the roundings of their sums."""
     T, H = x.shape
     E, I = up.shape[0], down.shape[2]
     x, w = x.double(), weights.double()
@@ -51,11 +53,11 @@ def layer(x, ids, weights, up, down, random=True):
         dg, dl = ((H / 16 + 12) * U * mag).split(I)
         h = gate * torch.sigmoid(gate) * lin
         dh = 1.1 * dg * (lin.abs() + dl) + (gate * torch.sigmoid(gate)).abs() * dl + 16 * U * (1 + gate.abs()) * h.abs() + 2.0**-130
-        b = 2.0**-8 * (h.abs() + dh) + 2.0**-134
+        b = (2.0**-8 if parts == 1 else 2.0**-17) * (h.abs() + dh) + 2.0**-134
         d, aw = down[e].abs(), w[t, j].abs()
         out = down[e] @ h
         y[t] += w[t, j] * out
-        tol[t] += aw * (d @ dh + (I / 16 + 12) * U * (d @ (h.abs() + dh + b)))
+        tol[t] += aw * (d @ dh + (parts * I / 16 + 12) * U * (d @ (h.abs() + dh + b)))
         if random:
             var[t] += aw**2 * ((d * d) @ (b * b))
         else:

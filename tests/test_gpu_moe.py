@@ -430,3 +430,65 @@ def test_dense_long_rows(fmt, H, I):
         ids, weights = _ids(T, E, top, T + H, kind)
         got = mx.moe(x[:T], ids, weights, up, down, F32)
         assert torch.equal(got.double(), _exact(x[:T], ids, weights, vu, vd)), (T, kind)
+
+
+PARTED = {"mxfp4": [(256, 352), (256, 2176), (288, 4224), (256, 8352)], "fp8_b128x128": [(256, 384), (256, 1152), (128, 2176), (256, 4224)],
+          "int8": [(144, 400), (176, 1040), (144, 2064), (208, 4112)]}
+
+
+@pytest.mark.parametrize("T,E,top,kind", [(1, 3, 2, "distinct"), (8, 2, 1, "one"), (9, 2, 1, "one"), (7, 5, 3, "any"), (40, 4, 2, "distinct")])
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_h_of_more_bits_than_bf16(fmt, T, E, top, kind):
+    """h of whole numbers of up to 12 bits, which two bf16 numbers hold and one does not: bit for bit."""
+    require_gpu()
+    for H, I in PARTED[fmt]:
+        g = _gen(H + I + T)
+        _, up, down, vu, vd = _dense_layer(fmt, T, E, H, I, H + I)
+        x = torch.randint(-50, 51, (T, H), device="cuda", generator=g).float()
+        x[:, 0] = 64
+        lin = torch.stack([vu[e, I:] @ x.double().t() for e in range(E)])
+        out = torch.stack([vd[e] @ lin[e] for e in range(E)])
+        # (sums of multiples of 64 and, weighted, of 64 / 8; the high part of a number is at most twice it)
+        assert 256 < lin.abs().max() < 2**12 and max((vd[e].abs() @ lin[e].abs()).max() for e in range(E)) * 2 < 2**24
+        assert out.abs().max() * 64 * 2 * top < 2**24 * 8
+        ids, weights = _ids(T, E, top, T + H, kind)
+        x = x.bfloat16()
+        assert torch.equal(mx.moe(x, ids, weights, up, down, F32).double(), _exact(x, ids, weights, vu, vd)), (H, I)
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("T,E,top", [(1, 8, 2), (8, 12, 4), (9, 3, 2), (31, 6, 3)])
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_random_layers_in_32_bits(fmt, T, E, top, out):
+    """Within the roundings of fp32 sums and of h's two parts, 2^-17: an fp32 result is one, and a bf16 one is rounded once."""
+    require_gpu()
+    for H, I in SIZES[fmt][1:] + PARTED[fmt][2:]:
+        g = _gen(H * I + T)
+        x = torch.randn(T, H, device="cuda", generator=g).bfloat16()
+        up = mx.quantize((torch.randn(E, 2 * I, H, device="cuda", generator=g) * H**-0.5).bfloat16(), fmt)
+        down = mx.quantize((torch.randn(E, H, I, device="cuda", generator=g) * 0.02).bfloat16(), fmt)
+        ids, _ = _ids(T, E, top, H)
+        weights = torch.softmax(torch.randn(T, top, device="cuda", generator=g), 1)
+        y, tol = ref.layer(x, ids, weights, ref.stack_values(up, mx), ref.stack_values(down, mx), parts=2)
+        ref.check(mx.moe(x, ids, weights, up, down, out), y, tol, out)
+
+
+@pytest.mark.parametrize("T", [2, 12])
+def test_largest_h(T):
+    """h past bf16's largest number but not fp32's, and infinite h, whose low part is none."""
+    require_gpu()
+    H = I = 128
+    ones = torch.ones(1, 2 * I, H, device="cuda")
+    up = _whole("int8", ones)
+    up.scales[I:] = float.fromhex("0x1.ff8p121")
+    down = _whole("int8", torch.eye(H, device="cuda")[None])
+    down.scales[:] = 0.5
+    x = torch.zeros(T, H, device="cuda")
+    x[:, 0] = 1
+    up.scales[:I] = 64  # gate 64, h = 64 * 0x1.ff8p121
+    ids, weights = torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda")
+    got = mx.moe(x.bfloat16(), ids, weights, up, down, F32)
+    assert (got == float.fromhex("0x1.ff8p126")).all()
+    up.scales[I:] = 1e37  # h = 6.4e38
+    down = _whole("int8", ones[:, :I].contiguous())
+    assert (mx.moe(x.bfloat16(), ids, weights, up, down, F32) == float("inf")).all()
