@@ -492,3 +492,30 @@ def test_largest_h(T):
     up.scales[I:] = 1e37  # h = 6.4e38
     down = _whole("int8", ones[:, :I].contiguous())
     assert (mx.moe(x.bfloat16(), ids, weights, up, down, F32) == float("inf")).all()
+
+
+@pytest.mark.parametrize("H", [256, 288])
+@pytest.mark.parametrize("lo,hi,power", [(0, 3, 125), (124, 130, 0), (251, 254, -125)])
+def test_mxfp4_scales_beside_any_others(H, lo, hi, power):
+    """Blocks whose scales are the smallest and largest there are, next to scales of any kind: the
+    expansion takes a scale with its neighbours' bits beside it."""
+    require_gpu()
+    T, E, top, I = 16, 3, 2, 128
+    g = _gen(H + lo)
+    # (codes of at most 1.5, so that a weight under the largest scale is finite)
+    code = torch.randint(0, 4, (E * 2 * I, H), device="cuda", generator=g) | torch.randint(0, 2, (E * 2 * I, H), device="cuda", generator=g) * 8
+    codes = (code[:, ::2] | code[:, 1::2] << 4).to(torch.uint8)
+    scales = torch.randint(0, 255, (E * 2 * I, H // 32), device="cuda", generator=g)
+    at = torch.randint(0, 2, (H // 32,), device="cuda", generator=g).bool()
+    at[0], at[-1] = True, True
+    scales[:, at] = torch.randint(lo, hi + 1, (E * 2 * I, int(at.sum())), device="cuda", generator=g)
+    up = mx.QTensor(FMTS["mxfp4"], E * 2 * I, H, codes, scales.to(torch.uint8), groups=E)
+    down = mx.quantize((torch.randn(E, H, I, device="cuda", generator=g) * 0.02).bfloat16(), "mxfp4")
+    block = at.nonzero().flatten()[torch.randint(0, int(at.sum()), (T,), device="cuda", generator=g)]
+    x = torch.zeros(T, H, device="cuda")
+    x[torch.arange(T), block * 32 + torch.randint(0, 32, (T,), device="cuda", generator=g)] = 2.0**power
+    x = x.bfloat16()
+    ids, weights = _ids(T, E, top, H)
+    y, tol = ref.layer(x, ids, weights, ref.stack_values(up, mx), ref.stack_values(down, mx), random=False, parts=2)
+    assert (y != 0).any(1).sum() > T // 2
+    ref.check(mx.moe(x, ids, weights, up, down, F32), y, tol, F32)
