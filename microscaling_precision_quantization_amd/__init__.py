@@ -572,7 +572,9 @@ def moe(x, ids, weights, up, down, out_dtype=None, out=None, workspace=None):
     of another rank) adds nothing. up: a stack of [2 * inter][hidden] weights, each gate
     above up; down: a stack of [hidden][inter] ones (mxfp4, fp8_b128x128 or int8;
     quantize of a 3-D tensor), the same format for both. The activations stay bf16:
-    with few tokens the weights' bytes are what a layer costs."""
+    with few tokens the weights' bytes are what a layer costs. workspace: at least
+    mx_moe_workspace_bytes(tokens, top, experts, hidden, inter) bytes on the device, of its own for each
+    of calls that may overlap (allocated for the call without it)."""
     import torch
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in (torch.float32, torch.bfloat16):

@@ -308,7 +308,8 @@ hipError_t launch(const Args& p, hipStream_t s) {
 int64_t rounds(int64_t tiles, int T) { return (tiles + 256 * T - 1) / (256 * T); }
 
 // Experts that have rows are taken as min(groups, M). Times in us at 16 rows,
-// FP8, N x K (by expert: rows over experts x N x K); INT8's rows are as long.
+// FP8, N x K (by expert: rows over experts x N x K). INT8 takes the same, as its rows are as long; of it were measured
+// 2048 x 2048 2.8 (one row), 4096 x 4096 6.0, 10240 x 8192 17.3, 28672 x 8192 37.6 and, 128 rows over 64 x 2048 x 4096, 64.
 template <int FMT, bool ALIGNED, int OUT>
 hipError_t dispatch(const Args& p, hipStream_t s) {
   if constexpr (FMT != kMXFP4) {

@@ -16,8 +16,9 @@
 // A step's fragments are read from LDS beside the products of the step before (1500 x 2048 x 4096 24.0 -> 22.8
 // us, 64 x 2048 x 4096 7.5 -> 6.7). 128 x 128 tiles have 8 waves of 64 x 64: WK = 2 groups of WM x WN waves, which
 // take half of each step's K each, so that a fragment is read as often as by 4 waves; their sums,
-// exact integers, meet in LDS at the end. What bounds the small tiles is the rate of loads into LDS: about
-// 75 KB/us a CU where rows begin on lines, 48 where they do not (K = 2448: 777 x 2000 14.2 us; 120 and 70 alone).
+// exact integers, meet in LDS at the end. What bounds the small tiles: the rate of loads into LDS, about
+// 75 KB/us a CU where rows begin on lines and 48 where they do not (120 and 70 alone; 777 x 2000 fp32 results of
+// K = 2448 14.7 us, of 2432 11.9), the first loads, and the chain of loads and stores at the end (below).
 //
 // B goes first into the MFMA: lane r + 16 g then holds C[row r][columns 4 g ..
 // 4 g + 3] of a tile, one row (one s_A) and a run of columns to store.
@@ -175,7 +176,8 @@ __global__ __launch_bounds__(G::kThreads) void gemm_int8_kernel(Args p) {
   const bool vec_ok = p.ldc % 4 == 0;
 #pragma unroll
   for (int q = 0; q < G::TMW * G::TNW; q += G::WK) {
-    // (Column by column of tiles, where one wave has them all: s_B's loads are then shared.)
+    // (Column by column of tiles where one wave has them all. The compiler loads each tile's five scales anew, and
+    // waits for them and for the store before: a chain of such round trips ends the kernel.)
     const int at = G::WK > 1 ? q : q % G::TMW * G::TNW + q / G::TMW, tile = at + (G::WK > 1 ? wk : 0);
     const int col = n0 + (wn * G::TNW + tile % G::TNW) * 16 + 4 * g, lrow = (wm * G::TMW + tile / G::TNW) * 16 + r;
     if (lrow >= mrows) continue;

@@ -1,10 +1,10 @@
 // GEMM of 8-bit integers under a scale per row of A and of B, the large-tile kernel
 // (dense or by expert; the mathematics is gemm_int8.hip's).
 //
-// Bound by the matrix cores and their power: a K step of 128 takes a 256 x 256 tile's SIMDs 2048
+// Bound by the matrix cores: a K step of 128 takes a 256 x 256 tile's SIMDs 2048
 // cycles of MFMA each, against 1536 of LDS reads and 512 of writes. Measured, 6000 x 8192 x 8192
-// (bf16 result): 300 us, 2.7 POPS; a step 1.3 us at the 1.95 GHz that the clock falls to (1.07 us at 2.3 GHz
-// without its loads), first loads and epilogue 10 us a round of tiles. 32 x 32 x 32 MFMAs: 310 us; 4 waves
+// (bf16 result): 300 us, 2.7 POPS, the MFMAs 64% busy at the 1.95 GHz that the clock falls to; a step 1.3 us (1.07 us at
+// 2.3 GHz without its loads), first loads and epilogue, with its waits for scales, 10 us a round of tiles. 32 x 32 x 32 MFMAs: 310 us; 4 waves
 // of 128 x 128, which read a third less LDS but leave a SIMD one wave: 310 to 325.
 //  * 8 waves (two per SIMD) of 128 x 64. A wave's step is 8 groups of eight 16 x 16 x 64
 //    MFMAs, one group per 16 rows; the tile's 16-row groups go to the two rows of

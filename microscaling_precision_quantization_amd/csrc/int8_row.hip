@@ -37,7 +37,7 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
-constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // of 256 threads: a grid's 2^32
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // of 256 threads: 2^31, half of what a launch may have; each takes further rows
 
 __device__ __forceinline__ uint32_t chunk_absmax(u32x4 v) {
   const uint32_t m = 0x7FFF7FFFu;
@@ -138,7 +138,8 @@ __global__ __launch_bounds__(kThreads) void quant_int8_kernel(const u32x4* __res
   }
 }
 
-// Longer rows: read twice, the second time from the caches.
+// Longer rows: read twice, the second time from the caches, with one load on its way a thread: 8192 x 28672 184 us, where
+// 28672 x 8192 takes 104.
 __global__ __launch_bounds__(kThreads) void quant_int8_long_kernel(const u32x4* __restrict__ x, u32x2* __restrict__ codes,
                                                                    float* __restrict__ scales, int64_t rows, int64_t cpr) {
   __shared__ uint32_t part[4];
@@ -160,7 +161,8 @@ __global__ __launch_bounds__(kThreads) void quant_int8_long_kernel(const u32x4* 
   }
 }
 
-// y = fl32(code * s), 8 elements a thread and pass.
+// y = fl32(code * s), 8 elements a thread and pass. 8192 x 8192 to bf16 31 us (5 TB/s and more: HBM), to fp32 102 (3.3 TB/s):
+// there each of a thread's two stores leaves out every other 16 bytes of the lines that the wave's cover.
 template <int OUT>
 __global__ __launch_bounds__(kThreads) void dequant_int8_kernel(const u32x2* __restrict__ codes,
                                                                 const float* __restrict__ scales,

@@ -2,8 +2,8 @@
 // weights (MXFP4, FP8 under fp32 scales per 128 x 128, INT8 under a scale per row):
 //   y_t = sum over j of w_tj down_e( silu(gate_e x_t) * up_e x_t ),  e = ids_tj.
 //
-// Bound by HBM: every weight of the experts that a token chose is read once, and meets
-// at most 16 tokens at a time. Tokens of one expert are a group; up to 16 of them a
+// Bound by HBM: every weight of the experts that a token chose is read once for each 16 of the
+// tokens that chose it. Tokens of one expert are a group; up to 16 of them a
 // pass; the (token, expert) pairs, sorted by expert and token, are the rows of h and of the
 // partial results.
 //  1. moe_up: h = silu(gate) up, in fp32, written as two bf16 numbers for the matrix cores, the nearest
@@ -28,8 +28,11 @@
 //
 // Measured in us, experts of 4096 x 2048 (gate and up + down + combine, traced): MXFP4, one token, 8 experts, 17 + 9 +
 // 3 (at 6.56 TB/s, a large copy's rate, its weights would take 11 + 5.5; each launch is about 3 us short of that
-// rate); 64 tokens, 61 experts, 98 + 56 + 5 (6.2 and 5.6 TB/s; without the expansion the same, without sums and
-// results 92 + 48); INT8, 32 tokens, 46 experts, 118 + 63 + 5 (6.7 and 6.3 TB/s).
+// rate); 64 tokens, all of 64 experts, 110 + 59 + 5 (5.2 and 4.8 TB/s of codes and scales; h in one part 107 + 55; 61
+// experts so 98 + 56, without the expansion the same, without sums and results 92 + 48); INT8, 32 tokens, 46 experts, 118
+// + 63 + 5 (6.7 and 6.3 TB/s). Rows of several rounds, whole layers: FP8, 4 tokens, 11 of 16 experts of 5120 x 5120 198
+// (132 at that rate), 14 of 32 of 7168 x 2048 126 (91); INT8, 11 of 16 of 5120 x 5120 201 (132): a second round of S = 4 steps
+// a wave has little to do, and each round waits for all loads before it begins.
 #include <type_traits>
 #include <utility>
 
