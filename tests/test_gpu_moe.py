@@ -519,3 +519,47 @@ def test_mxfp4_scales_beside_any_others(H, lo, hi, power):
     y, tol = ref.layer(x, ids, weights, ref.stack_values(up, mx), ref.stack_values(down, mx), random=False, parts=2)
     assert (y != 0).any(1).sum() > T // 2
     ref.check(mx.moe(x, ids, weights, up, down, F32), y, tol, F32)
+
+
+@pytest.mark.parametrize("fmt", list(FMTS))
+def test_at_most_eight_tokens(fmt):
+    """Where the low parts of h are rows of the matrix instructions: NaN and Inf reach their own tokens only, an expert
+    of NaN its own, and a captured call follows its inputs, beside eager ones on another stream."""
+    require_gpu()
+    T, E, top, H, I = 8, 3, 2, 256, 1152
+    x, up, down, vu, vd = _dense_layer(fmt, T, E, H, I, 12)
+    ids, weights = _ids(T, E, top, 3)
+    clean = mx.moe(x, ids, weights, up, down, F32)
+    assert torch.equal(clean.double(), _exact(x, ids, weights, vu, vd))
+    bad = x.clone()
+    bad[1, 7], bad[6, H - 1] = float("nan"), float("inf")
+    keep = [0, 2, 3, 4, 5, 7]
+    got = mx.moe(bad, ids, weights, up, down, F32)
+    assert torch.isnan(got[[1, 6]]).all() and torch.equal(got[keep], clean[keep])
+    s = down.scales.view(E, -1)
+    old = s[1].clone()
+    s[1] = 255 if fmt == "mxfp4" else float("nan")
+    got = mx.moe(x, ids, weights, up, down, F32)
+    s[1] = old
+    hit = (ids == 1).any(1)
+    assert 0 < hit.sum() < T and torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mx.moe(x, ids, weights, up, down)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = mx.moe(x, ids, weights, up, down, F32)
+    for i, kind in enumerate(("any", "one", "none", "distinct")):
+        a, b = _ids(T, E, top, 20 + i, kind)
+        ids.copy_(a)
+        weights.copy_(b)
+        want = _exact(x, ids, weights, vu, vd)
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            eager = mx.moe(x, ids, weights, up, down, F32)
+        torch.cuda.synchronize()
+        assert torch.equal(y.double(), want) and torch.equal(eager, y), kind
